@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define RGC_ABI_VERSION 6
+#define RGC_ABI_VERSION 7
 
 typedef enum {
   RGC_OK = 0,
@@ -73,7 +73,7 @@ typedef enum {
   RGC_ERR_ALIGN = 4,       /* a base pointer or leading dimension is misaligned */
   RGC_ERR_WORKSPACE = 5,   /* workspace missing or smaller than the query */
   RGC_ERR_HIP = 6,         /* a kernel launch failed */
-  RGC_ERR_VALUE = 7,       /* a scalar argument is not finite */
+  RGC_ERR_VALUE = 7,       /* a scalar argument is not finite or out of its range */
   RGC_ERR_SCRATCH = 8      /* rgc_apply_noalloc: more scratch needed than its static buffer holds */
 } rgc_status_t;
 
@@ -377,6 +377,109 @@ rgc_status_t rgc_linear_backward(const uint16_t* D, int64_t ldd, const uint16_t*
                                  const uint16_t* XP, float* C, uint16_t* dX, int64_t lddx, int64_t T,
                                  int64_t d, int64_t k, int64_t r, void* ws, size_t ws_bytes,
                                  void* stream);
+
+/* ---- The vocabulary head's loss -------------------------------------------
+ *
+ * A linear layer W (V x k, one row per vocabulary entry) and the softmax cross
+ * entropy of its outputs, without keeping them: z = X W^T is formed in tiles,
+ * reduced and dropped.
+ *
+ * Forward, for T tokens: lse[t] = log sum_v exp z_tv, loss[t] = lse[t] -
+ * z_t,targets[t]. A token whose target lies outside 0 .. V-1 is ignored: its
+ * loss is 0 (its lse is still written). No mean is taken: the caller weighs
+ * the tokens. With r > 0 also XP = bf16(X P), exactly as rgc_project makes it.
+ *   X: T x k bf16, row stride ldx; W: V x k bf16, row stride ldw; targets:
+ *   int64[T]; loss, lse: float[T]; P: k x r bf16; XP: T x r bf16 (P and XP may
+ *   be NULL when r = 0). z in fp32 (MFMA products of bf16, one fp32 sum each),
+ *   maxima and sums of exponentials in fp32 in a fixed order.
+ *
+ * Backward, from grad[t] = dL/dloss[t] and the forward's lse:
+ *   D_tv = grad[t] (exp(z_tv - lse[t]) - [v = targets[t]]), 0 for an ignored
+ *   token, formed from z again for one piece of the vocabulary after another;
+ *   dX = bf16(D W): T x k, row stride lddx, overwritten; each piece's D rounded
+ *   to bf16, the pieces added in fp32;
+ *   C += D^T XP with r > 0: V x r fp32, as rgc_accumulate adds, D as two bf16
+ *   terms (hi + lo, 2^-17 relative), so that C's error is that of fp32 sums.
+ *   C is what rgc_apply turns into the head's update. r = 0 (XP and C may then
+ *   be NULL) is a frozen head: dX alone.
+ * Limits: T and k at most 65536, V at most 2^24 and, with r > 0, a multiple of
+ * 8 in the backward (as every layer's d); k, ldx, ldw and lddx multiples of 8,
+ * leading dimensions at most 2^23; X, W, P, XP, C and dX 16-byte aligned; r 0 or a
+ * supported rank. T = 0 is a no-op. The workspaces hold the tiles' partial
+ * results (forward) and one piece's D with dX's fp32 sums (backward). */
+size_t rgc_linear_cross_entropy_forward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r);
+rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                              const uint16_t* P, const int64_t* targets, float* loss, float* lse,
+                                              uint16_t* XP, int64_t T, int64_t V, int64_t k, int64_t r, void* ws,
+                                              size_t ws_bytes, void* stream);
+size_t rgc_linear_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r);
+rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                               const int64_t* targets, const float* lse, const float* grad,
+                                               const uint16_t* XP, float* C, uint16_t* dX, int64_t lddx, int64_t T,
+                                               int64_t V, int64_t k, int64_t r, void* ws, size_t ws_bytes,
+                                               void* stream);
+
+/* ---- Layer norms ------------------------------------------------------------
+ *
+ * Row norms between the sketched layers, with their weights' gradients (which
+ * are small and stay dense). For every row x of n elements:
+ *   mu = mean(x) (0 for RGC_NORM_RMS), rstd = 1/sqrt(mean((x - mu)^2) + eps),
+ *   xhat = (x - mu) rstd, y = xhat weight + bias.
+ * Backward, from dY and the forward's mean and rstd: with h = dy weight,
+ *   dx = rstd (h - mean(h) - xhat mean(h xhat)) (RMS: without mean(h)),
+ *   dweight = sum over rows of dy xhat, dbias = sum over rows of dy; both
+ *   overwritten, and zero for rows = 0.
+ * X, Y, dY, dX: rows x n of type xt, row strides ld* >= n elements (at most
+ * 2^31); weight, bias, dweight, dbias: n elements of type wt; mean, rstd:
+ * float[rows]. weight NULL stands for ones, bias NULL for none; mean and rstd
+ * may be NULL in the forward (not kept), mean in an RMS backward; dbias NULL
+ * is not formed. Everything in fp32, fixed order, one rounding per output.
+ * Any n from 1 to 65536 and rows up to 2^31; pointers aligned to their
+ * elements (16-byte aligned rows of a multiple of 8 elements move in 16-byte
+ * vectors, others element by element). eps must be finite and not negative. */
+typedef enum { RGC_BF16 = 0, RGC_F32 = 1 } rgc_dtype_t;
+typedef enum { RGC_NORM_LAYER = 0, RGC_NORM_RMS = 1 } rgc_norm_kind_t;
+
+rgc_status_t rgc_layer_norm_forward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* X, int64_t ldx,
+                                    const void* weight, const void* bias, double eps, void* Y, int64_t ldy,
+                                    float* mean, float* rstd, int64_t rows, int64_t n, void* stream);
+size_t rgc_layer_norm_backward_workspace_size(int64_t rows, int64_t n);
+rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* dY,
+                                     int64_t lddy, const void* X, int64_t ldx, const void* weight, const float* mean,
+                                     const float* rstd, void* dX, int64_t lddx, void* dweight, void* dbias,
+                                     int64_t rows, int64_t n, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- AdamW for the tensors that keep a dense gradient -------------------------
+ *
+ * One step over n tensors (gains, biases, embeddings). Tensor i: numels[i]
+ * contiguous elements of parameters Ps[i] (type pt, in place), gradients Gs[i]
+ * (type gt) and moments Ms[i], Vs[i] (in place). In fp32, for every element:
+ *   g' = g * *grad_scale (1 if NULL: e.g. a clipping coefficient, on the device)
+ *   m <- beta1 m + (1 - beta1) g',  v <- beta2 v + (1 - beta2) g'^2
+ *   p <- p (1 - lr weight_decay)
+ *        - lr/(1 - beta1^step) * m / (sqrt(v)/sqrt(1 - beta2^step) + eps)
+ * A *grad_scale that is not finite skips the step: nothing changes.
+ * bf16 parameters are rounded stochastically as rgc_apply's weights are, with
+ * the bits of Philox4x32-10 (counter (e/8 low, e/8 high, 4, i), key = seed)
+ * for element e of tensor i: half e%2 of word (e%8)/2. The same arguments give
+ * the same bits; draw another seed every step.
+ * state_bits 32: Ms and Vs are fp32. state_bits 8: Ms holds m and Vs holds
+ * sqrt(v) as e4m3 bytes in units of a scale per block of 128 elements,
+ * Mscales[i] and Vscales[i], float[(numels[i] + 127) / 128]: the power of two
+ * (at least 2^-126) that brings the block's largest finite magnitude into 128
+ * .. 256. m is rounded to nearest, sqrt(v) stochastically (with the other half
+ * of the word), never to zero unless it is zero; an infinite or NaN moment
+ * becomes a NaN byte and does not count for the scale. All states start as
+ * zero bytes. Mscales and Vscales may be NULL with 32 bits.
+ * Arrays are HOST arrays of n entries, n without limit (48 tensors a launch);
+ * parameters, gradients and moments 16-byte aligned, at most 2^34 elements. A
+ * tensor may be listed once only. RGC_ERR_VALUE: step < 1, a beta outside
+ * [0, 1), eps <= 0 (as fp32), or a scalar that is not finite. */
+rgc_status_t rgc_adamw_batch(int64_t n, rgc_dtype_t pt, rgc_dtype_t gt, int state_bits, void* const* Ps,
+                             const void* const* Gs, void* const* Ms, void* const* Vs, float* const* Mscales,
+                             float* const* Vscales, const int64_t* numels, double lr, double beta1, double beta2,
+                             double eps, double weight_decay, int64_t step, const float* grad_scale, uint64_t seed,
+                             void* stream);
 
 /* ---- Test hooks (same library; used by the parity tests) ----------------- */
 

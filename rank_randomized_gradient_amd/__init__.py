@@ -27,6 +27,11 @@ from .rgc import (  # noqa: F401
     rgc_linear_forward,
     rgc_linear_forward_batch,
     rgc_linear_backward,
+    rgc_linear_cross_entropy_forward,
+    rgc_linear_cross_entropy_backward,
+    rgc_layer_norm_forward,
+    rgc_layer_norm_backward,
+    rgc_adamw_batch,
     rgc_sample_projection,
     rgc_sample_projections,
     rgc_test_philox,

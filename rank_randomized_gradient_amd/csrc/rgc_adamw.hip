@@ -1,0 +1,314 @@
+// One AdamW step over many tensors, with moments in fp32 or in 8 bits:
+//
+//   g' = scale g,  m <- b1 m + (1 - b1) g',  v <- b2 v + (1 - b2) g'^2
+//   p <- p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// in fp32 whatever the stored types. bf16 parameters are rounded
+// stochastically, as the sketched update's weights are: no fp32 copy is kept,
+// and a step far below half a unit in the last place still moves the weight
+// in expectation.
+//
+// 8-bit moments: m and sqrt(v) are e4m3 values in blocks of 128 with one
+// power-of-two scale each, chosen so that the block's largest finite magnitude
+// lies in 128 .. 256 units (below e4m3's largest, 448). Powers of two make the
+// scaling exact, so the only error is the rounding to four significant bits.
+// m changes by up to 1 - b1 of itself a step, of the order of e4m3's step, and
+// is rounded to nearest. sqrt(v) changes by at most (1 - b2) / 2 of itself
+// while the gradient is small, far below half a step: rounded to nearest it
+// would never decay, so it is rounded stochastically. What is not zero never
+// rounds to zero, since a zero sqrt(v) under a momentum that is not zero
+// would leave eps alone to divide by. Infinities and NaN become NaN codes and
+// are left out of the scale: they spoil their own elements only.
+//
+// Bound by memory: 2 p + g + 16 bytes an element in fp32 states, 2 p + g + 4
+// in 8 bits (10 bytes for bf16). Eight consecutive elements to a thread, so
+// one Philox call (128 bits) serves the thread: element j of the eight takes
+// half j % 2 of word j / 2 for its parameter and the other half, its
+// neighbour's, for its second moment, which makes an element's two rounding
+// errors independent of each other. A block of 128 is sixteen lanes, so its
+// maxima are lane rotations within a row of sixteen.
+#include <math.h>
+
+#include "rgc_internal.hpp"
+
+namespace rgc {
+namespace {
+
+constexpr int kAdamThreads = 256;
+constexpr int kAdamChunk = kAdamThreads * 8;  // elements of a workgroup
+constexpr int kAdamTensors = 48;              // tensors of a launch: their table travels in the kernel's arguments
+constexpr uint32_t kTagAdam = 4;              // counter word 2 of the rounding bits
+
+struct AdamTensor {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  int64_t n;
+};
+
+struct AdamArgs {
+  int count;
+  uint32_t first;  // index of the launch's first tensor within the call
+  uint32_t key0, key1;
+  float b1, c1, b2, c2;  // b1, 1 - b1, b2, 1 - b2
+  float keep;            // 1 - lr wd
+  float size;            // lr / (1 - b1^t)
+  float root;            // 1 / sqrt(1 - b2^t)
+  float eps;
+  const float* scale;  // gradients' factor, or null
+  uint32_t base[kAdamTensors + 1];  // first workgroup of each tensor
+  AdamTensor t[kAdamTensors];
+};
+
+__device__ __forceinline__ void load8(const float* p, int64_t at, int count, float (&f)[8]) {
+  if (count == 8) {
+    const float4 a = *reinterpret_cast<const float4*>(p + at), b = *reinterpret_cast<const float4*>(p + at + 4);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j < count ? p[at + j] : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, int64_t at, int count, float (&f)[8]) {
+  if (count == 8) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p + at);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j < count ? bf16_bits_to_f32(p[at + j]) : 0.f;
+  }
+}
+__device__ __forceinline__ void store8(float* p, int64_t at, int count, const float (&f)[8]) {
+  if (count == 8) {
+    *reinterpret_cast<float4*>(p + at) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(p + at + 4) = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < count) p[at + j] = f[j];
+  }
+}
+
+// Eight e4m3 codes (two dwords) and their values.
+__device__ __forceinline__ void load_codes(const uint8_t* p, int64_t at, int count, float unit, float (&f)[8]) {
+  uint32_t w[2] = {0u, 0u};
+  if (count == 8) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p + at);
+    w[0] = a.x, w[1] = a.y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < count) w[j / 4] |= (uint32_t)p[at + j] << (8 * (j & 3));
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[h], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[h], true);
+    f[4 * h] = lo[0] * unit, f[4 * h + 1] = lo[1] * unit, f[4 * h + 2] = hi[0] * unit, f[4 * h + 3] = hi[1] * unit;
+  }
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t at, int count, const float (&f)[8]) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int q = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h], f[4 * h + 1], 0, false);
+    w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2], f[4 * h + 3], q, true);
+  }
+  if (count == 8) {
+    *reinterpret_cast<uint2*>(p + at) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < count) p[at + j] = (uint8_t)(w[j / 4] >> (8 * (j & 3)));
+  }
+}
+
+// Maximum over the sixteen lanes of a row, in all of them (values not negative).
+__device__ __forceinline__ float row_max(float v) {
+  // row rotations by 8, 4, 2 and 1
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false)));
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false)));
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x122, 0xF, 0xF, false)));
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x121, 0xF, 0xF, false)));
+  return v;
+}
+
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+
+// Exponent field of the unit that brings `top` into 128 .. 256, at least 1
+// (2^-126, the smallest normal number, for a block of zeros too).
+__device__ __forceinline__ uint32_t unit_exponent(float top) {
+  const int e = (int)(__float_as_uint(top) >> 23) - 7;
+  return (uint32_t)(e < 1 ? 1 : e);
+}
+
+template <typename PT, typename GT, bool EIGHT>
+__global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs a) {
+  const float scale = a.scale ? *a.scale : 1.f;
+  if (!finite(scale)) return;  // gradients that overflowed: the step is skipped
+  int lo = 0, hi = a.count - 1;
+  while (lo < hi) {  // the last tensor whose first workgroup is not behind this one
+    const int mid = (lo + hi + 1) / 2;
+    if (a.base[mid] <= blockIdx.x) lo = mid;
+    else hi = mid - 1;
+  }
+  const AdamTensor& t = a.t[lo];
+  const int64_t at = (int64_t)(blockIdx.x - a.base[lo]) * kAdamChunk + (int64_t)threadIdx.x * 8;
+  const int64_t left = t.n - at;
+  const int count = left >= 8 ? 8 : left > 0 ? (int)left : 0;  // 0: past the end, but still a lane of its block's maxima
+  PT* P = static_cast<PT*>(t.p);
+  float p[8], g[8], m[8], v[8];
+  load8(P, at, count, p);
+  load8(static_cast<const GT*>(t.g), at, count, g);
+  const int64_t block = at / 128;
+  const bool any = block * 128 < t.n;
+  if constexpr (EIGHT) {
+    load_codes(static_cast<const uint8_t*>(t.m), at, count, any ? t.ms[block] : 0.f, m);
+    load_codes(static_cast<const uint8_t*>(t.v), at, count, any ? t.vs[block] : 0.f, v);
+  } else {
+    load8(static_cast<const float*>(t.m), at, count, m);
+    load8(static_cast<const float*>(t.v), at, count, v);
+  }
+  float root[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    g[j] = g[j] * scale;
+    m[j] = m[j] * a.b1 + g[j] * a.c1;
+    if constexpr (EIGHT) v[j] = v[j] * v[j];
+    v[j] = v[j] * a.b2 + g[j] * g[j] * a.c2;
+    root[j] = sqrtf(v[j]);
+    p[j] = p[j] * a.keep - a.size * (m[j] / (root[j] * a.root + a.eps));
+  }
+  u32x4 bits{0u, 0u, 0u, 0u};
+  if constexpr (EIGHT || sizeof(PT) == 2) {
+    const uint64_t group = (uint64_t)at / 8;
+    bits = philox4x32_10(u32x4{(uint32_t)group, (uint32_t)(group >> 32), kTagAdam, a.first + (uint32_t)lo}, a.key0, a.key1);
+  }
+  const uint32_t word[4] = {bits.x, bits.y, bits.z, bits.w};
+  if constexpr (sizeof(PT) == 2) {
+    if (count == 8) {
+      *reinterpret_cast<uint4*>(P + at) =
+          make_uint4(f32x2_to_bf16x2_sr(p[0], p[1], word[0]), f32x2_to_bf16x2_sr(p[2], p[3], word[1]),
+                     f32x2_to_bf16x2_sr(p[4], p[5], word[2]), f32x2_to_bf16x2_sr(p[6], p[7], word[3]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < count) P[at + j] = (uint16_t)f32_to_bf16_sr(p[j], j & 1 ? word[j / 2] >> 16 : word[j / 2] & 0xFFFFu);
+    }
+  } else {
+    store8(P, at, count, p);
+  }
+  if constexpr (EIGHT) {
+    float mt = 0.f, vt = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      mt = fmaxf(mt, finite(m[j]) ? fabsf(m[j]) : 0.f);
+      vt = fmaxf(vt, finite(root[j]) ? root[j] : 0.f);
+    }
+    const uint32_t me = unit_exponent(row_max(mt)), ve = unit_exponent(row_max(vt));
+    const float im = __uint_as_float((254u - me) << 23), iv = __uint_as_float((254u - ve) << 23);  // 1 / unit
+    float qm[8], qv[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float nan = __uint_as_float(0x7FC00000u);
+      qm[j] = finite(m[j]) ? m[j] * im : nan;
+      // three bits of mantissa, the 20 below them rounded by 16 random bits;
+      // e4m3's subnormals have the step of its smallest normal numbers, 2^-9,
+      // so they are rounded lifted by 2^-6, where fp32 truncates at that step
+      const uint32_t r = j & 1 ? word[j / 2] & 0xFFFFu : word[j / 2] >> 16;
+      const float x = root[j] * iv;
+      const float lift = x < 0.015625f ? 0.015625f : 0.f;
+      const float y = __uint_as_float((__float_as_uint(x + lift) + (r << 4)) & 0xFFF00000u) - lift;
+      qv[j] = !finite(root[j]) ? nan : x > 0.f ? fmaxf(y, 0.001953125f) : 0.f;
+    }
+    store_codes(static_cast<uint8_t*>(t.m), at, count, qm);
+    store_codes(static_cast<uint8_t*>(t.v), at, count, qv);
+    if (any && (threadIdx.x & 15) == 0) {
+      t.ms[block] = __uint_as_float(me << 23);
+      t.vs[block] = __uint_as_float(ve << 23);
+    }
+  } else {
+    store8(static_cast<float*>(t.m), at, count, m);
+    store8(static_cast<float*>(t.v), at, count, v);
+  }
+}
+
+template <typename PT, typename GT>
+void launch(const AdamArgs& a, bool eight, hipStream_t s) {
+  const dim3 grid(a.base[a.count]);
+  if (eight) hipLaunchKernelGGL((adamw_kernel<PT, GT, true>), grid, dim3(kAdamThreads), 0, s, a);
+  else hipLaunchKernelGGL((adamw_kernel<PT, GT, false>), grid, dim3(kAdamThreads), 0, s, a);
+}
+
+bool dtype_ok(rgc_dtype_t t) { return t == RGC_BF16 || t == RGC_F32; }
+
+}  // namespace
+}  // namespace rgc
+
+using namespace rgc;
+
+extern "C" rgc_status_t rgc_adamw_batch(int64_t n, rgc_dtype_t pt, rgc_dtype_t gt, int state_bits, void* const* Ps,
+                                        const void* const* Gs, void* const* Ms, void* const* Vs, float* const* Mscales,
+                                        float* const* Vscales, const int64_t* numels, double lr, double beta1,
+                                        double beta2, double eps, double weight_decay, int64_t step,
+                                        const float* grad_scale, uint64_t seed, void* stream) {
+  if (n < 0) return RGC_ERR_SHAPE;
+  if (!dtype_ok(pt) || !dtype_ok(gt) || (state_bits != 8 && state_bits != 32) || n > INT32_MAX) return RGC_ERR_UNSUPPORTED;
+  // scalars that would divide by zero or give values that are not finite for finite inputs
+  if (!(fabs(lr) <= 1e30) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps <= 1e30) ||
+      !((float)eps > 0) || !(fabs(weight_decay) <= 1e30) || step < 1)
+    return RGC_ERR_VALUE;
+  if (n == 0) return RGC_OK;
+  const bool eight = state_bits == 8;
+  if (!Ps || !Gs || !Ms || !Vs || !numels || (eight && (!Mscales || !Vscales))) return RGC_ERR_NULL;
+  if (!aligned_to(grad_scale, 4)) return RGC_ERR_ALIGN;
+  for (int64_t i = 0; i < n; ++i) {
+    if (numels[i] < 0) return RGC_ERR_SHAPE;
+    if (numels[i] > int64_t(1) << 34) return RGC_ERR_UNSUPPORTED;
+    if (numels[i] == 0) continue;
+    if (!Ps[i] || !Gs[i] || !Ms[i] || !Vs[i] || (eight && (!Mscales[i] || !Vscales[i]))) return RGC_ERR_NULL;
+    if (!aligned16(Ps[i]) || !aligned16(Gs[i]) || !aligned16(Ms[i]) || !aligned16(Vs[i]) ||
+        (eight && (!aligned_to(Mscales[i], 4) || !aligned_to(Vscales[i], 4))))
+      return RGC_ERR_ALIGN;
+  }
+  AdamArgs a{};
+  a.key0 = (uint32_t)seed, a.key1 = (uint32_t)(seed >> 32);
+  a.b1 = (float)beta1, a.c1 = (float)(1 - beta1), a.b2 = (float)beta2, a.c2 = (float)(1 - beta2);
+  a.keep = (float)(1 - lr * weight_decay);
+  a.size = (float)(lr / (1 - pow(beta1, (double)step)));
+  a.root = (float)(1 / sqrt(1 - pow(beta2, (double)step)));
+  a.eps = (float)eps;
+  a.scale = grad_scale;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  // launches of up to kAdamTensors consecutive tensors and 2^23 workgroups (2^31 threads)
+  for (int64_t i = 0; i < n;) {
+    a.first = (uint32_t)i;
+    a.count = 0;
+    uint64_t groups = 0;
+    while (i < n && a.count < kAdamTensors) {
+      const uint64_t need = ((uint64_t)numels[i] + kAdamChunk - 1) / kAdamChunk;
+      if (a.count > 0 && groups + need > (uint64_t(1) << 23)) break;
+      AdamTensor& t = a.t[a.count];
+      t.p = Ps[i], t.g = Gs[i], t.m = Ms[i], t.v = Vs[i], t.n = numels[i];
+      t.ms = eight ? Mscales[i] : nullptr, t.vs = eight ? Vscales[i] : nullptr;
+      a.base[a.count++] = (uint32_t)groups;
+      groups += need;
+      ++i;
+    }
+    a.base[a.count] = (uint32_t)groups;
+    if (groups == 0) continue;
+    if (pt == RGC_F32) {
+      if (gt == RGC_F32) launch<float, float>(a, eight, s);
+      else launch<float, uint16_t>(a, eight, s);
+    } else {
+      if (gt == RGC_F32) launch<uint16_t, float>(a, eight, s);
+      else launch<uint16_t, uint16_t>(a, eight, s);
+    }
+    if (hipGetLastError() != hipSuccess) return RGC_ERR_HIP;
+  }
+  return RGC_OK;
+}

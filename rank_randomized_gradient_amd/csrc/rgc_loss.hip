@@ -1,0 +1,443 @@
+// A linear layer and its softmax cross entropy over a large vocabulary,
+// without keeping the logits, and the gradient that feeds the layer's input
+// and its sketch. W: V x k, a row per vocabulary entry; X: T x k.
+//
+//   z = X W^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,y(t)
+//   D_tv = g_t (exp(z_tv - lse_t) - [v = y(t)])
+//   dX = D W,  C += D^T XP
+//
+// Tokens whose target lies outside 0 .. V-1 are ignored: no loss and a zero
+// row of D.
+//
+// Forward: every 256 x 256 tile of z is reduced in registers to its rows'
+// maxima and sums of exponentials; a second launch joins the tiles of a row.
+// Backward: the vocabulary goes by in pieces. A piece's D is formed from z
+// again (z costs 2 T V k operations a second time; keeping it would cost 2 T V
+// bytes and more), written in bf16 to the workspace, and used twice from
+// there while it is in the last-level cache: D W, added to dX in fp32, and
+// D^T XP, added to the sketch by the sketch's own accumulation.
+//
+// The sketch is fp32, and a D rounded once to bf16 would put an error of 2^-9
+// into each of its terms. So with a sketch D is kept as two bf16 terms,
+// D = hi + lo (error 2^-17), stacked along the tokens: C += [hi; lo]^T [XP; XP]
+// is one accumulation over 2 T tokens. dX is rounded to bf16 itself and takes
+// hi alone.
+//
+// Bound by MFMA: 2 T V k operations for the loss, 6 T V k + 4 T V r for the
+// gradient. Where dX has few tiles (few tokens), each is split over K among
+// several workgroups, which add into slabs of their own; a last launch adds
+// the slabs and rounds. All sums have a fixed order.
+#include "rgc_gemm_tile.hpp"
+
+namespace rgc {
+namespace {
+
+constexpr int64_t kCeMaxVocab = int64_t(1) << 24;
+constexpr int kCeDown = 8;        // tile rows walked together
+constexpr int kCeMaxSplit = 16;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct CeArgs {
+  const uint16_t* X;
+  const uint16_t* W;   // the piece's first row
+  const int64_t* targets;
+  int64_t ldx, ldw;
+  int64_t T, V, k;     // V: rows of the piece
+  int64_t v0;          // vocabulary index of the piece's first row
+  int64_t vocab;       // rows of the whole vocabulary
+  int64_t mtiles, ntiles;
+  float2* part;        // forward: (maximum, sum) of each tile row, [tile][token]
+  float* zt;           // forward: the target's logit
+  const float* lse;    // backward
+  const float* grad;
+  uint16_t* hi;        // backward: T x ldd, bf16
+  uint16_t* lo;        // or null
+  int64_t ldd;
+};
+
+// The target's column counted from a lane's first one (the lane holds columns
+// 16 nt + e from there), or a number that is none of them.
+__device__ __forceinline__ int target_column(int64_t y, int64_t v0, int64_t V, int64_t first) {
+  const int64_t c = y - v0, at = c - first;
+  return c >= 0 && c < V && at >= 0 && at < 64 ? (int)at : -1;
+}
+
+__global__ __launch_bounds__(kGtThreads, 1) void ce_forward_kernel(CeArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[kGtLds];
+  int64_t i, j;
+  gt_place(gt_logical(blockIdx.x, gridDim.x), a.mtiles, a.ntiles, kCeDown, &i, &j);
+  const int64_t m0 = i * kGtTile, n0 = j * kGtTile;
+  GtTile<false> t;
+  t.init(a.X + m0 * a.ldx, a.ldx, a.W + n0 * a.ldw, a.ldw, a.T - m0, a.V - n0, a.k, smem);
+  t.run();
+
+  const int g = t.lane >> 4, li = t.lane & 15, wm = t.wave & 1, wn = t.wave >> 1;
+  float* rows = reinterpret_cast<float*>(smem);  // [row][wn]: maximum, sum
+  const int64_t first = n0 + 64 * wn + 4 * g;
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) {
+    const int row = 128 * wm + 16 * mt + li;
+    const bool live = m0 + row < a.T;
+    const int64_t y = live ? a.targets[m0 + row] : -1;
+    const int at = target_column(y, a.v0, a.V, first);
+    float z[4][4], top = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        z[nt][e] = first + 16 * nt + e < a.V ? t.acc[mt][nt][e] : -INFINITY;
+        top = fmaxf(top, z[nt][e]);
+        if (16 * nt + e == at) a.zt[m0 + row] = z[nt][e];
+      }
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const float base = top == -INFINITY ? 0.f : top;
+    float s = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s += exp2f((z[nt][e] - base) * kLog2e);
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (g == 0) {
+      rows[8 * row + 2 * wn] = top;
+      rows[8 * row + 2 * wn + 1] = s;
+    }
+  }
+  __syncthreads();
+  const int row = threadIdx.x;
+  if (row < kGtTile && m0 + row < a.T) {
+    float top = rows[8 * row], s = 0.f;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, rows[8 * row + 2 * w]);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) s += rows[8 * row + 2 * w + 1] * exp2f((rows[8 * row + 2 * w] - base) * kLog2e);
+    a.part[j * a.T + m0 + row] = make_float2(top, s);
+  }
+}
+
+// lse and loss of 64 tokens per workgroup: sixteen waves take every sixteenth
+// tile each, then their maxima and sums are joined in wave order.
+__global__ __launch_bounds__(1024) void ce_finish_kernel(CeArgs a, float* loss, float* lse) {
+  __shared__ float tops[16][64], sums[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * 64 + lane;
+  float top = -INFINITY, s = 0.f;
+  if (t < a.T) {
+#pragma unroll 4
+    for (int64_t j = wave; j < a.ntiles; j += 16) {
+      const float2 p = a.part[j * a.T + t];
+      const float m = fmaxf(top, p.x), base = m == -INFINITY ? 0.f : m;
+      s = s * exp2f((top - base) * kLog2e) + p.y * exp2f((p.x - base) * kLog2e);
+      top = m;
+    }
+  }
+  tops[wave][lane] = top;
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && t < a.T) {
+    for (int w = 1; w < 16; ++w) top = fmaxf(top, tops[w][lane]);
+    const float base = top == -INFINITY ? 0.f : top;
+    s = 0.f;
+    for (int w = 0; w < 16; ++w) s += sums[w][lane] * exp2f((tops[w][lane] - base) * kLog2e);
+    const float l = top + logf(s);
+    const int64_t y = a.targets[t];
+    lse[t] = l;
+    loss[t] = y >= 0 && y < a.V ? l - a.zt[t] : 0.f;
+  }
+}
+
+// A piece's D, hi (and lo): T x ldd, zero in the columns behind the piece.
+__global__ __launch_bounds__(kGtThreads, 1) void ce_d_kernel(CeArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[kGtLds];
+  int64_t i, j;
+  gt_place(gt_logical(blockIdx.x, gridDim.x), a.mtiles, a.ntiles, kCeDown, &i, &j);
+  const int64_t m0 = i * kGtTile, n0 = j * kGtTile;
+  GtTile<false> t;
+  t.init(a.X + m0 * a.ldx, a.ldx, a.W + n0 * a.ldw, a.ldw, a.T - m0, a.V - n0, a.k, smem);
+  t.run();
+
+  const int g = t.lane >> 4, li = t.lane & 15, wm = t.wave & 1, wn = t.wave >> 1;
+  const int64_t first = n0 + 64 * wn + 4 * g;
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) {
+    const int64_t row = m0 + 128 * wm + 16 * mt + li;
+    if (row >= a.T) continue;
+    const int64_t y = a.targets[row];
+    const bool kept = y >= 0 && y < a.vocab;
+    const int at = target_column(y, a.v0, a.V, first);
+    const float lse = a.lse[row], gr = a.grad[row];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      float d[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = exp2f((t.acc[mt][nt][e] - lse) * kLog2e);
+        d[e] = kept && first + 16 * nt + e < a.V ? (16 * nt + e == at ? p - 1.f : p) * gr : 0.f;
+      }
+      const uint2 h = make_uint2(f32x2_to_bf16x2_rne(d[0], d[1]), f32x2_to_bf16x2_rne(d[2], d[3]));
+      *reinterpret_cast<uint2*>(a.hi + row * a.ldd + first + 16 * nt) = h;
+      if (a.lo)
+        *reinterpret_cast<uint2*>(a.lo + row * a.ldd + first + 16 * nt) =
+            make_uint2(f32x2_to_bf16x2_rne(d[0] - __uint_as_float(h.x << 16), d[1] - __uint_as_float(h.x & 0xFFFF0000u)),
+                       f32x2_to_bf16x2_rne(d[2] - __uint_as_float(h.y << 16), d[3] - __uint_as_float(h.y & 0xFFFF0000u)));
+    }
+  }
+}
+
+struct DxArgs {
+  const uint16_t* D;  // T x ldd, the piece's hi terms
+  const uint16_t* W;  // the piece's first row
+  int64_t ldd, ldw;
+  int64_t T, K, k;    // K: rows of the piece
+  int64_t mtiles, ntiles;
+  int64_t steps;      // 64-row steps of K to each split
+  float* slab;        // [split][T][k] fp32, or null (one piece, one split)
+  int first;          // the first piece: the slab is written, not added to
+  uint16_t* dX;       // the last piece of an unsplit product: rounded here; else null
+  int64_t lddx;
+};
+
+__global__ __launch_bounds__(kGtThreads, 1) void ce_dx_kernel(DxArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[kGtLds];
+  const int64_t tiles = a.mtiles * a.ntiles;
+  const int64_t place = gt_logical(blockIdx.x, gridDim.x);
+  const int64_t split = place / tiles;
+  int64_t i, j;
+  gt_place(place - split * tiles, a.mtiles, a.ntiles, kCeDown, &i, &j);
+  const int64_t m0 = i * kGtTile, n0 = j * kGtTile;
+  const int64_t k0 = split * a.steps * kGtStep;
+  const int64_t K = a.K - k0 < a.steps * kGtStep ? a.K - k0 : a.steps * kGtStep;
+  GtTile<true> t;
+  t.init(a.D + m0 * a.ldd + k0, a.ldd, a.W + k0 * a.ldw + n0, a.ldw, a.T - m0, a.k - n0, K, smem);
+  if (K > 0) t.run();
+
+  const int g = t.lane >> 4, li = t.lane & 15, wm = t.wave & 1, wn = t.wave >> 1;
+  float* slab = a.slab ? a.slab + split * a.T * a.k : nullptr;
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) {
+    const int64_t row = m0 + 128 * wm + 16 * mt + li;
+    if (row >= a.T) continue;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      const int64_t col = n0 + 64 * wn + 16 * nt + 4 * g;
+      if (col >= a.k) continue;  // k is a multiple of 8: four columns are all in or all out
+      f32x4_t v = t.acc[mt][nt];
+      if (!a.first) v += *reinterpret_cast<const f32x4_t*>(slab + row * a.k + col);
+      if (a.dX)
+        *reinterpret_cast<uint2*>(a.dX + row * a.lddx + col) =
+            make_uint2(f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3]));
+      else
+        *reinterpret_cast<f32x4_t*>(slab + row * a.k + col) = v;
+    }
+  }
+}
+
+// dX = bf16(sum of the slabs), eight columns to a thread.
+__global__ __launch_bounds__(256) void ce_join_kernel(const float* slab, int splits, int64_t T, int64_t k, uint16_t* dX,
+                                                      int64_t lddx) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (at >= T * k) return;
+  f32x4_t u = *reinterpret_cast<const f32x4_t*>(slab + at), v = *reinterpret_cast<const f32x4_t*>(slab + at + 4);
+#pragma unroll 4
+  for (int s = 1; s < splits; ++s) {
+    u += *reinterpret_cast<const f32x4_t*>(slab + s * T * k + at);
+    v += *reinterpret_cast<const f32x4_t*>(slab + s * T * k + at + 4);
+  }
+  const int64_t row = at / k, col = at - row * k;
+  *reinterpret_cast<uint4*>(dX + row * lddx + col) =
+      make_uint4(f32x2_to_bf16x2_rne(u[0], u[1]), f32x2_to_bf16x2_rne(u[2], u[3]), f32x2_to_bf16x2_rne(v[0], v[1]),
+                 f32x2_to_bf16x2_rne(v[2], v[3]));
+}
+
+// XP twice over, for the two terms of D (16-byte vectors; 8-byte ones end a
+// rank-4 XP of an odd token count).
+__global__ __launch_bounds__(256) void ce_twice_kernel(const uint2* XP, int64_t n, uint2* out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) out[i] = out[n + i] = XP[i];
+}
+
+int64_t tiles_of(int64_t n) { return (n + kGtTile - 1) / kGtTile; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// How the backward goes through the vocabulary and divides dX's sums.
+struct Plan {
+  int64_t piece;   // vocabulary rows of a piece
+  int64_t pieces;
+  int64_t splits;  // of dX's sums within a piece
+  bool stacked;    // hi and lo in one accumulation of 2 T tokens
+  size_t d, xp, slab, acc;  // bytes of the workspace's parts
+};
+
+Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
+  Plan p{};
+  const int64_t terms = r > 0 ? 2 : 1;
+  // a piece's D stays within half of the 256 MB last-level cache
+  int64_t piece = (int64_t(128) << 20) / (T * 2 * terms) / kGtTile * kGtTile;
+  if (piece < 1024) piece = 1024;
+  if (piece > kMaxTiledDim) piece = kMaxTiledDim;
+  p.pieces = (V + piece - 1) / piece;
+  p.piece = tiles_of((V + p.pieces - 1) / p.pieces) * kGtTile;
+  p.pieces = (V + p.piece - 1) / p.piece;
+  // as many splits as keep the compute units busy with the fewest rounds of tiles a split
+  const int64_t tiles = tiles_of(T) * tiles_of(k), cus = device_compute_units();
+  int64_t best = 1;
+  double cost = 1e30;
+  for (int64_t s = 1; s <= kCeMaxSplit; ++s) {
+    const double c = (double)((tiles * s + cus - 1) / cus) / (double)s + 0.004 * (double)s;
+    if (c < cost) cost = c, best = s;
+  }
+  const int64_t steps = (p.piece + kGtStep - 1) / kGtStep;
+  p.splits = best < steps ? best : steps;
+  p.stacked = 2 * T <= kMaxTiledDim;
+  p.d = up256((size_t)(terms * T * p.piece) * 2);
+  p.xp = r > 0 && p.stacked ? up256((size_t)(2 * T * r) * 2) : 0;
+  p.slab = p.pieces > 1 || p.splits > 1 ? up256((size_t)(p.splits * T * k) * 4) : 0;
+  if (r > 0) {
+    // every width the pieces have: the whole ones and the last
+    const int64_t tokens = p.stacked ? 2 * T : T, last = V - (p.pieces - 1) * p.piece;
+    const size_t a = rgc_accumulate_workspace_size(tokens, p.piece, r), b = rgc_accumulate_workspace_size(tokens, last, r);
+    p.acc = up256(a > b ? a : b);
+  }
+  return p;
+}
+
+rgc_status_t check_rows(const void* p, int64_t ld, int64_t width) {
+  if (!p) return RGC_ERR_NULL;
+  if (ld < width) return RGC_ERR_SHAPE;
+  if (ld > kMaxLeadingDim) return RGC_ERR_UNSUPPORTED;
+  if (!aligned16(p) || (ld % 8) != 0) return RGC_ERR_ALIGN;
+  return RGC_OK;
+}
+
+bool shape_ok(int64_t T, int64_t V, int64_t k, int64_t r) {
+  return T > 0 && V > 0 && k > 0 && r >= 0 && r <= k && T <= kMaxTiledDim && V <= kCeMaxVocab && k <= kMaxTiledDim &&
+         k % 8 == 0 && (r == 0 || rank_supported(r));
+}
+
+rgc_status_t check_shape(int64_t T, int64_t V, int64_t k, int64_t r) {
+  if (T < 0 || V <= 0 || k <= 0 || r < 0 || r > k) return RGC_ERR_SHAPE;
+  if (T > 0 && !shape_ok(T, V, k, r)) return RGC_ERR_UNSUPPORTED;
+  return RGC_OK;
+}
+
+rgc_status_t launched() { return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP; }
+
+size_t part_bytes(int64_t T, int64_t V) { return up256((size_t)(tiles_of(V) * T) * 8); }
+
+}  // namespace
+}  // namespace rgc
+
+using namespace rgc;
+
+extern "C" size_t rgc_linear_cross_entropy_forward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r) {
+  if (!shape_ok(T, V, k, r)) return 0;
+  return part_bytes(T, V) + up256((size_t)T * 4) + (r > 0 ? rgc_project_workspace_size(T, k, r) : 0);
+}
+
+extern "C" rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                                         const uint16_t* P, const int64_t* targets, float* loss,
+                                                         float* lse, uint16_t* XP, int64_t T, int64_t V, int64_t k,
+                                                         int64_t r, void* ws, size_t ws_bytes, void* stream) {
+  rgc_status_t st = check_shape(T, V, k, r);
+  if (st != RGC_OK || T == 0) return st;
+  if ((st = check_rows(X, ldx, k)) != RGC_OK) return st;
+  if ((st = check_rows(W, ldw, k)) != RGC_OK) return st;
+  if (!targets || !loss || !lse || (r > 0 && (!P || !XP))) return RGC_ERR_NULL;
+  if (!aligned_to(targets, 8) || !aligned_to(loss, 4) || !aligned_to(lse, 4) ||
+      (r > 0 && (!aligned16(P) || !aligned16(XP))))
+    return RGC_ERR_ALIGN;
+  if (!ws || ws_bytes < rgc_linear_cross_entropy_forward_workspace_size(T, V, k, r)) return RGC_ERR_WORKSPACE;
+  if (!aligned_to(ws, 256)) return RGC_ERR_ALIGN;
+  char* at = static_cast<char*>(ws);
+  CeArgs a{};
+  a.X = X, a.W = W, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = T, a.V = a.vocab = V, a.k = k;
+  a.mtiles = tiles_of(T), a.ntiles = tiles_of(V);
+  a.part = reinterpret_cast<float2*>(at);
+  at += part_bytes(T, V);
+  a.zt = reinterpret_cast<float*>(at);
+  at += up256((size_t)T * 4);
+  if (a.mtiles * a.ntiles >= int64_t(1) << 23) return RGC_ERR_UNSUPPORTED;  // threads of a launch
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (r > 0) {  // the layer's X P, as rgc_project makes it
+    st = rgc_project(X, ldx, P, XP, T, k, r, at, ws_bytes - (size_t)(at - static_cast<char*>(ws)), stream);
+    if (st != RGC_OK) return st;
+  }
+  hipLaunchKernelGGL(ce_forward_kernel, dim3((unsigned)(a.mtiles * a.ntiles)), dim3(kGtThreads), 0, s, a);
+  if ((st = launched()) != RGC_OK) return st;
+  hipLaunchKernelGGL(ce_finish_kernel, dim3((unsigned)((T + 63) / 64)), dim3(1024), 0, s, a, loss, lse);
+  return launched();
+}
+
+extern "C" size_t rgc_linear_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r) {
+  if (!shape_ok(T, V, k, r)) return 0;
+  const Plan p = plan_of(T, V, k, r);
+  return p.d + p.xp + p.slab + p.acc;
+}
+
+extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                                          const int64_t* targets, const float* lse, const float* grad,
+                                                          const uint16_t* XP, float* C, uint16_t* dX, int64_t lddx,
+                                                          int64_t T, int64_t V, int64_t k, int64_t r, void* ws,
+                                                          size_t ws_bytes, void* stream) {
+  rgc_status_t st = check_shape(T, V, k, r);
+  if (st != RGC_OK || T == 0) return st;
+  if (r > 0 && V % 8 != 0) return RGC_ERR_UNSUPPORTED;  // the sketch has a layer's widths
+  if ((st = check_rows(X, ldx, k)) != RGC_OK) return st;
+  if ((st = check_rows(W, ldw, k)) != RGC_OK) return st;
+  if ((st = check_rows(dX, lddx, k)) != RGC_OK) return st;
+  if (!targets || !lse || !grad || (r > 0 && (!XP || !C))) return RGC_ERR_NULL;
+  if (!aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(grad, 4) ||
+      (r > 0 && (!aligned16(XP) || !aligned16(C))))
+    return RGC_ERR_ALIGN;
+  const Plan p = plan_of(T, V, k, r);
+  if (!ws || ws_bytes < p.d + p.xp + p.slab + p.acc) return RGC_ERR_WORKSPACE;
+  if (!aligned_to(ws, 256)) return RGC_ERR_ALIGN;
+  char* at = static_cast<char*>(ws);
+  uint16_t* D = reinterpret_cast<uint16_t*>(at);
+  uint16_t* twice = reinterpret_cast<uint16_t*>(at + p.d);
+  float* slab = p.slab ? reinterpret_cast<float*>(at + p.d + p.xp) : nullptr;
+  char* acc = at + p.d + p.xp + p.slab;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (r > 0 && p.stacked) {
+    const int64_t n = T * r / 4;
+    hipLaunchKernelGGL(ce_twice_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
+                       reinterpret_cast<const uint2*>(XP), n, reinterpret_cast<uint2*>(twice));
+    if ((st = launched()) != RGC_OK) return st;
+  }
+  CeArgs a{};
+  a.X = X, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = T, a.vocab = V, a.k = k;
+  a.lse = lse, a.grad = grad, a.mtiles = tiles_of(T);
+  DxArgs x{};
+  x.ldw = ldw, x.T = T, x.k = k, x.mtiles = tiles_of(T), x.ntiles = tiles_of(k), x.slab = slab, x.lddx = lddx;
+  for (int64_t q = 0; q < p.pieces; ++q) {
+    const int64_t v0 = q * p.piece, rows = V - v0 < p.piece ? V - v0 : p.piece;
+    a.W = W + v0 * ldw, a.V = rows, a.v0 = v0, a.ntiles = tiles_of(rows);
+    a.ldd = a.ntiles * kGtTile;
+    a.hi = D, a.lo = r > 0 ? D + T * a.ldd : nullptr;
+    hipLaunchKernelGGL(ce_d_kernel, dim3((unsigned)(a.mtiles * a.ntiles)), dim3(kGtThreads), 0, s, a);
+    if ((st = launched()) != RGC_OK) return st;
+    x.D = a.hi, x.W = a.W, x.ldd = a.ldd, x.K = rows, x.first = q == 0;
+    x.steps = ((rows + kGtStep - 1) / kGtStep + p.splits - 1) / p.splits;
+    x.dX = p.splits == 1 && q == p.pieces - 1 ? dX : nullptr;
+    hipLaunchKernelGGL(ce_dx_kernel, dim3((unsigned)(x.mtiles * x.ntiles * p.splits)), dim3(kGtThreads), 0, s, x);
+    if ((st = launched()) != RGC_OK) return st;
+    if (r > 0) {
+      float* c = C + v0 * r;
+      if (p.stacked) {
+        st = rgc_accumulate(D, a.ldd, twice, c, 2 * T, rows, r, acc, p.acc, stream);
+      } else {
+        st = rgc_accumulate(a.hi, a.ldd, XP, c, T, rows, r, acc, p.acc, stream);
+        if (st == RGC_OK) st = rgc_accumulate(a.lo, a.ldd, XP, c, T, rows, r, acc, p.acc, stream);
+      }
+      if (st != RGC_OK) return st;
+    }
+  }
+  if (p.splits > 1) {
+    const int64_t n = (T * k / 8 + 255) / 256;
+    hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)n), dim3(256), 0, s, slab, (int)p.splits, T, k, dX, lddx);
+    st = launched();
+  }
+  return st;
+}

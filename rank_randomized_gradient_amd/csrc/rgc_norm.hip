@@ -1,0 +1,578 @@
+// Layer norm and root-mean-square norm, forward and backward with the weights'
+// gradients, for rows of up to 65536 elements in bf16 or fp32.
+//
+//   mu = mean(x) (0 for rms), rstd = 1 / sqrt(mean((x - mu)^2) + eps)
+//   xhat = (x - mu) rstd,     y = xhat w + b
+//   h = dy w,  dx = rstd (h - mean(h) - xhat mean(h xhat))   (rms: without mean(h))
+//   dw = sum over rows of dy xhat,   db = sum over rows of dy
+//
+// Everything is held in fp32; y and dx are rounded once to X's type, dw and db
+// once to the weight's type. All four are bound by memory: the forward reads
+// x and writes y, the backward reads dy and x and writes dx.
+//
+// * A row is held in the registers of TPR threads (16 lanes up to a whole
+//   workgroup), NV vectors of VEC elements each, so x (and dy) come from
+//   memory once: mean, centred squares and the output all use the held values.
+// * Rows that are not made of aligned 16-byte vectors (an odd width, an odd
+//   leading dimension, an unaligned base) take VEC = 1, one element per load,
+//   lanes along the row.
+// * Backward: a workgroup of 1024 threads walks the rows with a stride of the
+//   grid, every thread adding its columns' dy xhat and dy in registers. At the
+//   end the workgroup's row groups are added through LDS and one partial row
+//   per workgroup goes to the workspace; a second launch adds the partials.
+//   The grid is one workgroup per compute unit, which keeps the partials small
+//   beside the rows. All sums have a fixed order.
+// * Backward rows above 16384 elements do not fit the registers: one launch
+//   makes dx reading each row twice (the second time from cache), another the
+//   column sums.
+#include "rgc_internal.hpp"
+
+namespace rgc {
+namespace {
+
+constexpr int64_t kNormMaxWidth = 65536;
+constexpr int64_t kNormMaxRows = int64_t(1) << 31;
+constexpr int64_t kNormHeldBackward = 16384;  // widest backward row held in registers
+constexpr int kBwdThreads = 1024;
+constexpr int kPanel = 256;  // columns of a workgroup of the column-sum launch
+
+struct NormArgs {
+  const void* x;
+  const void* dy;   // backward
+  const void* w;    // null: ones
+  const void* b;    // null: none (forward)
+  void* out;        // y or dx
+  float* mean;      // forward: written unless null; backward: read (layer)
+  float* rstd;
+  float* part;      // backward: partial rows
+  int64_t ldx, lddy, ldo;
+  int64_t rows, n;
+  float eps;
+  int w_f32;
+  int centre;
+  int db;           // backward: db wanted
+};
+
+// One vector of VEC elements as loaded, and its values.
+template <typename XT, int VEC>
+struct Raw;
+template <>
+struct Raw<uint16_t, 8> {
+  uint4 v;
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+  static __device__ __forceinline__ void store(uint16_t* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(f32x2_to_bf16x2_rne(f[0], f[1]), f32x2_to_bf16x2_rne(f[2], f[3]),
+                                              f32x2_to_bf16x2_rne(f[4], f[5]), f32x2_to_bf16x2_rne(f[6], f[7]));
+  }
+};
+template <>
+struct Raw<float, 8> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const float4& q = i < 4 ? a : b;
+    return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+template <>
+struct Raw<uint16_t, 1> {
+  uint16_t v;
+  __device__ __forceinline__ void zero() { v = 0; }
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *p; }
+  __device__ __forceinline__ float get(int) const { return bf16_bits_to_f32(v); }
+  static __device__ __forceinline__ void store(uint16_t* p, const float (&f)[1]) { *p = (uint16_t)f32_to_bf16_rne(f[0]); }
+};
+template <>
+struct Raw<float, 1> {
+  float v;
+  __device__ __forceinline__ void zero() { v = 0.f; }
+  __device__ __forceinline__ void load(const float* p) { v = *p; }
+  __device__ __forceinline__ float get(int) const { return v; }
+  static __device__ __forceinline__ void store(float* p, const float (&f)[1]) { *p = f[0]; }
+};
+
+__device__ __forceinline__ float load_param(const void* p, int f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
+}
+template <int VEC>
+__device__ __forceinline__ void load_params(const void* p, int f32, int64_t i, float (&out)[VEC]) {
+  if constexpr (VEC == 8) {
+    if (f32) {
+      Raw<float, 8> r;
+      r.load(static_cast<const float*>(p) + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] = r.get(e);
+    } else {
+      Raw<uint16_t, 8> r;
+      r.load(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] = r.get(e);
+    }
+  } else {
+    out[0] = load_param(p, f32, i);
+  }
+}
+
+// Sums of two values over the TPR threads of a row group, in all of them.
+// Within a wave by a xor butterfly; across the waves of a wider group through
+// LDS, `slots` being two floats per wave of the workgroup, used by one call
+// between two barriers (the caller alternates two sets).
+template <int TPR>
+__device__ __forceinline__ void group_sum2(float& a, float& b, float* slots) {
+#pragma unroll
+  for (int off = (TPR < 64 ? TPR : 64) / 2; off >= 1; off >>= 1) {
+    a += __shfl_xor(a, off, 64);
+    b += __shfl_xor(b, off, 64);
+  }
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      slots[2 * wave] = a;
+      slots[2 * wave + 1] = b;
+    }
+    __syncthreads();
+    const int w0 = wave / W * W;
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      a += slots[2 * (w0 + i)];
+      b += slots[2 * (w0 + i) + 1];
+    }
+  }
+}
+
+// Forward: a workgroup of THREADS threads takes THREADS / TPR rows at a time.
+template <typename XT, int VEC, int NV, int TPR, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
+  constexpr int GROUPS = THREADS / TPR;
+  __shared__ float slots[3][2 * THREADS / 64];
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const float inv_n = 1.0f / (float)a.n;
+  for (int64_t row0 = (int64_t)blockIdx.x * GROUPS; row0 < a.rows; row0 += (int64_t)gridDim.x * GROUPS) {
+    const int64_t row = row0 + grp;
+    const bool live = row < a.rows;
+    const XT* x = static_cast<const XT*>(a.x) + (live ? row : row0) * a.ldx;
+    Raw<XT, VEC> raw[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t c = (int64_t)(j * TPR + t) * VEC;
+      raw[j].zero();
+      if (c < a.n) raw[j].load(x + c);
+    }
+    float s = 0.f, unused = 0.f;
+    float mu = 0.f;
+    if (a.centre) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s += raw[j].get(e);
+      group_sum2<TPR>(s, unused, slots[0]);
+      mu = s * inv_n;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = (int64_t)(j * TPR + t) * VEC < a.n;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = raw[j].get(e) - mu;
+        q += in ? d * d : 0.f;
+      }
+    }
+    unused = 0.f;
+    group_sum2<TPR>(q, unused, slots[1]);
+    const float rstd = 1.0f / sqrtf(q * inv_n + a.eps);
+    if (live && t == 0) {
+      if (a.mean) a.mean[row] = mu;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    XT* y = static_cast<XT*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t c = (int64_t)(j * TPR + t) * VEC;
+      if (c >= a.n || !live) continue;
+      float f[VEC], w[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) f[e] = (raw[j].get(e) - mu) * rstd;
+      if (a.w) {
+        load_params<VEC>(a.w, a.w_f32, c, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = f[e] * w[e];
+      }
+      if (a.b) {
+        load_params<VEC>(a.b, a.w_f32, c, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = f[e] + w[e];
+      }
+      Raw<XT, VEC>::store(y + c, f);
+    }
+    if constexpr (TPR > 64) __syncthreads();  // before the next rows' sums reuse the slots
+  }
+}
+
+// Backward with the row in registers; see the head of the file.
+template <typename XT, int VEC, int NV, int TPR>
+__global__ __launch_bounds__(kBwdThreads) void norm_backward_kernel(NormArgs a) {
+  constexpr int GROUPS = kBwdThreads / TPR, E = VEC * NV;
+  __shared__ float slots[2][2 * kBwdThreads / 64];
+  __shared__ float add[GROUPS > 1 ? kBwdThreads * E : 1];
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const float inv_n = 1.0f / (float)a.n;
+  float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int64_t c = (int64_t)(j * TPR + t) * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w[j][e] = 1.f, dw[j][e] = 0.f, db[j][e] = 0.f;
+    if (a.w && c < a.n) load_params<VEC>(a.w, a.w_f32, c, w[j]);
+  }
+  const int64_t stride = (int64_t)gridDim.x * GROUPS;
+  Raw<XT, VEC> rx[NV], rg[NV];
+  float mu = 0.f, rstd = 0.f;
+  auto load = [&](int64_t row) {
+    const bool live = row < a.rows;
+    const XT* x = static_cast<const XT*>(a.x) + (live ? row : 0) * a.ldx;
+    const XT* g = static_cast<const XT*>(a.dy) + (live ? row : 0) * a.lddy;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t c = (int64_t)(j * TPR + t) * VEC;
+      rx[j].zero();
+      rg[j].zero();
+      if (live && c < a.n) {
+        rx[j].load(x + c);
+        rg[j].load(g + c);
+      }
+    }
+    mu = live && a.centre ? a.mean[row] : 0.f;
+    rstd = live ? a.rstd[row] : 0.f;
+  };
+  int parity = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * GROUPS; row0 < a.rows; row0 += stride, parity ^= 1) {
+    const int64_t row = row0 + grp;
+    load(row);
+    const bool live = row < a.rows;
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = live && (int64_t)(j * TPR + t) * VEC < a.n;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float g = rg[j].get(e);
+        const float xhat = in ? (rx[j].get(e) - mu) * rstd : 0.f;
+        const float h = g * w[j][e];
+        s1 += h;
+        s2 += h * xhat;
+        dw[j][e] += g * xhat;
+        db[j][e] += g;
+      }
+    }
+    group_sum2<TPR>(s1, s2, slots[parity]);
+    const float c1 = a.centre ? s1 * inv_n : 0.f, c2 = s2 * inv_n;
+    XT* dx = static_cast<XT*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t c = (int64_t)(j * TPR + t) * VEC;
+      if (c >= a.n || !live) continue;
+      float f[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float xhat = (rx[j].get(e) - mu) * rstd;
+        f[e] = (rg[j].get(e) * w[j][e] - c1 - xhat * c2) * rstd;
+      }
+      Raw<XT, VEC>::store(dx + c, f);
+    }
+  }
+  // the workgroup's partial rows: dw, then db
+  for (int which = 0; which < 1 + a.db; ++which) {
+    float* part = a.part + ((int64_t)which * gridDim.x + blockIdx.x) * a.n;
+    if constexpr (GROUPS > 1) {
+      if (which) __syncthreads();
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) add[grp * TPR * E + (j * TPR + t) * VEC + e] = which ? db[j][e] : dw[j][e];
+      __syncthreads();
+      for (int64_t c = threadIdx.x; c < a.n; c += kBwdThreads) {
+        float s = 0.f;
+#pragma unroll 4
+        for (int q = 0; q < GROUPS; ++q) s += add[q * TPR * E + c];
+        part[c] = s;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int64_t c = (int64_t)(j * TPR + t) * VEC;
+        if (c >= a.n) continue;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) part[c + e] = which ? db[j][e] : dw[j][e];
+      }
+    }
+  }
+}
+
+// Wide rows, first launch: dx, one row per workgroup, each row read twice.
+template <typename XT>
+__global__ __launch_bounds__(kBwdThreads) void norm_wide_dx_kernel(NormArgs a) {
+  __shared__ float slots[2 * kBwdThreads / 64];
+  const float inv_n = 1.0f / (float)a.n;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const XT* x = static_cast<const XT*>(a.x) + row * a.ldx;
+    const XT* g = static_cast<const XT*>(a.dy) + row * a.lddy;
+    XT* dx = static_cast<XT*>(a.out) + row * a.ldo;
+    const float mu = a.centre ? a.mean[row] : 0.f, rstd = a.rstd[row];
+    float s1 = 0.f, s2 = 0.f;
+    for (int64_t c = threadIdx.x; c < a.n; c += kBwdThreads) {
+      Raw<XT, 1> rx, rg;
+      rx.load(x + c);
+      rg.load(g + c);
+      const float h = rg.get(0) * (a.w ? load_param(a.w, a.w_f32, c) : 1.f);
+      s1 += h;
+      s2 += h * ((rx.get(0) - mu) * rstd);
+    }
+    group_sum2<kBwdThreads>(s1, s2, slots);
+    const float c1 = a.centre ? s1 * inv_n : 0.f, c2 = s2 * inv_n;
+    for (int64_t c = threadIdx.x; c < a.n; c += kBwdThreads) {
+      Raw<XT, 1> rx, rg;
+      rx.load(x + c);
+      rg.load(g + c);
+      const float h = rg.get(0) * (a.w ? load_param(a.w, a.w_f32, c) : 1.f);
+      const float f[1] = {(h - c1 - (rx.get(0) - mu) * rstd * c2) * rstd};
+      Raw<XT, 1>::store(dx + c, f);
+    }
+    __syncthreads();
+  }
+}
+
+// Wide rows, second launch: partial column sums, a workgroup per panel of 256
+// columns (blockIdx.x) and slice of the rows (blockIdx.y).
+template <typename XT>
+__global__ __launch_bounds__(kPanel) void norm_wide_columns_kernel(NormArgs a) {
+  const int64_t c = (int64_t)blockIdx.x * kPanel + threadIdx.x;
+  if (c >= a.n) return;
+  float dw = 0.f, db = 0.f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    Raw<XT, 1> rx, rg;
+    rx.load(static_cast<const XT*>(a.x) + row * a.ldx + c);
+    rg.load(static_cast<const XT*>(a.dy) + row * a.lddy + c);
+    const float mu = a.centre ? a.mean[row] : 0.f;
+    dw += rg.get(0) * ((rx.get(0) - mu) * a.rstd[row]);
+    db += rg.get(0);
+  }
+  a.part[(int64_t)blockIdx.y * a.n + c] = dw;
+  if (a.db) a.part[((int64_t)gridDim.y + blockIdx.y) * a.n + c] = db;
+}
+
+// dw (blockIdx.y = 0) and db (1): the G partial rows added, 64 columns per
+// workgroup, sixteen waves each taking every sixteenth row, then in wave order.
+__global__ __launch_bounds__(1024) void norm_params_kernel(const float* part, int64_t G, int64_t n, int f32, void* dw,
+                                                           void* db) {
+  __shared__ float sums[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const float* p = part + (int64_t)blockIdx.y * G * n + c;
+  float s = 0.f;
+  if (c < n) {
+#pragma unroll 8
+    for (int64_t g = wave; g < G; g += 16) s += p[g * n];
+  }
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < n) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += sums[i][lane];
+    void* out = blockIdx.y ? db : dw;
+    if (f32)
+      static_cast<float*>(out)[c] = s;
+    else
+      static_cast<uint16_t*>(out)[c] = (uint16_t)f32_to_bf16_rne(s);
+  }
+}
+
+size_t elem(rgc_dtype_t t) { return t == RGC_F32 ? 4 : 2; }
+bool dtype_ok(rgc_dtype_t t) { return t == RGC_BF16 || t == RGC_F32; }
+
+// Rows of 16-byte vectors: base, leading dimension and width all multiples.
+bool vectors(const void* p, int64_t ld, int64_t n, rgc_dtype_t t) {
+  return aligned16(p) && (ld * (int64_t)elem(t)) % 16 == 0 && n % 8 == 0;
+}
+
+rgc_status_t check_rows(const void* p, int64_t ld, int64_t n, rgc_dtype_t t) {
+  if (!p) return RGC_ERR_NULL;
+  if (ld < n) return RGC_ERR_SHAPE;
+  if (ld > int64_t(1) << 31) return RGC_ERR_UNSUPPORTED;
+  if (!aligned_to(p, elem(t))) return RGC_ERR_ALIGN;
+  return RGC_OK;
+}
+
+rgc_status_t check_shape(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, int64_t rows, int64_t n) {
+  if (kind != RGC_NORM_LAYER && kind != RGC_NORM_RMS) return RGC_ERR_UNSUPPORTED;
+  if (!dtype_ok(xt) || !dtype_ok(wt)) return RGC_ERR_UNSUPPORTED;
+  if (rows < 0 || n <= 0) return RGC_ERR_SHAPE;
+  if (rows > kNormMaxRows || n > kNormMaxWidth) return RGC_ERR_UNSUPPORTED;
+  return RGC_OK;
+}
+
+rgc_status_t launched() { return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP; }
+
+template <typename XT, int VEC, int NV, int TPR, int THREADS>
+void forward_launch(const NormArgs& a, hipStream_t s) {
+  const int64_t groups = (a.rows + THREADS / TPR - 1) / (THREADS / TPR);
+  const int64_t most = (int64_t)device_compute_units() * (2048 / THREADS) * 4;
+  hipLaunchKernelGGL((norm_forward_kernel<XT, VEC, NV, TPR, THREADS>), dim3((unsigned)(groups < most ? groups : most)),
+                     dim3(THREADS), 0, s, a);
+}
+
+template <typename XT>
+void forward_pick(const NormArgs& a, bool vec, hipStream_t s) {
+  if (vec) {
+    if (a.n <= 128) forward_launch<XT, 8, 1, 16, 256>(a, s);
+    else if (a.n <= 512) forward_launch<XT, 8, 1, 64, 256>(a, s);
+    else if (a.n <= 1024) forward_launch<XT, 8, 2, 64, 256>(a, s);
+    else if (a.n <= 2048) forward_launch<XT, 8, 4, 64, 256>(a, s);
+    else if (a.n <= 4096) forward_launch<XT, 8, 2, 256, 256>(a, s);
+    else if (a.n <= 8192) forward_launch<XT, 8, 4, 256, 256>(a, s);
+    else if (a.n <= 16384) forward_launch<XT, 8, 2, 1024, 1024>(a, s);
+    else forward_launch<XT, 8, 8, 1024, 1024>(a, s);
+  } else {
+    if (a.n <= 64) forward_launch<XT, 1, 1, 64, 256>(a, s);
+    else if (a.n <= 256) forward_launch<XT, 1, 4, 64, 256>(a, s);
+    else if (a.n <= 1024) forward_launch<XT, 1, 4, 256, 256>(a, s);
+    else if (a.n <= 4096) forward_launch<XT, 1, 16, 256, 256>(a, s);
+    else if (a.n <= 16384) forward_launch<XT, 1, 16, 1024, 1024>(a, s);
+    else forward_launch<XT, 1, 64, 1024, 1024>(a, s);
+  }
+}
+
+// Threads of a row in the backward (1024 / this: rows a workgroup holds).
+int backward_threads_per_row(int64_t n, bool vec) {
+  if (vec) return n <= 128 ? 16 : n <= 1024 ? 64 : n <= 4096 ? 256 : n <= 8192 ? 512 : 1024;
+  return n <= 256 ? 64 : n <= 4096 ? 256 : 1024;
+}
+
+// Workgroups of the backward, and so partial rows: one per compute unit, or
+// fewer where the rows do not fill them.
+int64_t backward_groups(int64_t rows, int64_t n, bool vec) {
+  const int64_t cus = device_compute_units();
+  if (n > kNormHeldBackward) return rows < 64 ? rows : 64;
+  const int64_t per = kBwdThreads / backward_threads_per_row(n, vec);
+  const int64_t need = (rows + per - 1) / per;
+  return need < cus ? need : cus;
+}
+
+template <typename XT, int VEC, int NV, int TPR>
+void backward_launch(const NormArgs& a, int64_t G, hipStream_t s) {
+  hipLaunchKernelGGL((norm_backward_kernel<XT, VEC, NV, TPR>), dim3((unsigned)G), dim3(kBwdThreads), 0, s, a);
+}
+
+template <typename XT>
+void backward_pick(const NormArgs& a, bool vec, int64_t G, hipStream_t s) {
+  if (a.n > kNormHeldBackward) {
+    const int64_t most = (int64_t)device_compute_units() * 4;
+    hipLaunchKernelGGL(norm_wide_dx_kernel<XT>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(kBwdThreads), 0, s,
+                       a);
+    hipLaunchKernelGGL(norm_wide_columns_kernel<XT>, dim3((unsigned)((a.n + kPanel - 1) / kPanel), (unsigned)G),
+                       dim3(kPanel), 0, s, a);
+  } else if (vec) {
+    if (a.n <= 128) backward_launch<XT, 8, 1, 16>(a, G, s);
+    else if (a.n <= 512) backward_launch<XT, 8, 1, 64>(a, G, s);
+    else if (a.n <= 1024) backward_launch<XT, 8, 2, 64>(a, G, s);
+    else if (a.n <= 2048) backward_launch<XT, 8, 1, 256>(a, G, s);
+    else if (a.n <= 4096) backward_launch<XT, 8, 2, 256>(a, G, s);
+    else if (a.n <= 8192) backward_launch<XT, 8, 2, 512>(a, G, s);
+    else backward_launch<XT, 8, 2, 1024>(a, G, s);
+  } else {
+    if (a.n <= 64) backward_launch<XT, 1, 1, 64>(a, G, s);
+    else if (a.n <= 256) backward_launch<XT, 1, 4, 64>(a, G, s);
+    else if (a.n <= 1024) backward_launch<XT, 1, 4, 256>(a, G, s);
+    else if (a.n <= 4096) backward_launch<XT, 1, 16, 256>(a, G, s);
+    else backward_launch<XT, 1, 16, 1024>(a, G, s);
+  }
+}
+
+}  // namespace
+}  // namespace rgc
+
+using namespace rgc;
+
+extern "C" rgc_status_t rgc_layer_norm_forward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* X,
+                                               int64_t ldx, const void* weight, const void* bias, double eps, void* Y,
+                                               int64_t ldy, float* mean, float* rstd, int64_t rows, int64_t n,
+                                               void* stream) {
+  rgc_status_t st = check_shape(kind, xt, wt, rows, n);
+  if (st != RGC_OK) return st;
+  if (!(eps >= 0) || !((float)eps <= 3e38f)) return RGC_ERR_VALUE;
+  if (rows == 0) return RGC_OK;
+  if ((st = check_rows(X, ldx, n, xt)) != RGC_OK) return st;
+  if ((st = check_rows(Y, ldy, n, xt)) != RGC_OK) return st;
+  if (!aligned_to(weight, elem(wt)) || !aligned_to(bias, elem(wt)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return RGC_ERR_ALIGN;
+  NormArgs a{};
+  a.x = X, a.w = weight, a.b = bias, a.out = Y, a.mean = mean, a.rstd = rstd;
+  a.ldx = ldx, a.ldo = ldy, a.rows = rows, a.n = n, a.eps = (float)eps;
+  a.w_f32 = wt == RGC_F32, a.centre = kind == RGC_NORM_LAYER;
+  const bool vec = vectors(X, ldx, n, xt) && vectors(Y, ldy, n, xt) && aligned16(weight) && aligned16(bias);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (xt == RGC_F32) forward_pick<float>(a, vec, s);
+  else forward_pick<uint16_t>(a, vec, s);
+  return launched();
+}
+
+// The partial rows of either path (the element path never has more workgroups
+// than the vector path has rows to give, but may have more than it).
+extern "C" size_t rgc_layer_norm_backward_workspace_size(int64_t rows, int64_t n) {
+  if (rows <= 0 || n <= 0 || rows > kNormMaxRows || n > kNormMaxWidth) return 0;
+  const int64_t a = backward_groups(rows, n, true), b = backward_groups(rows, n, false);
+  return (size_t)(a > b ? a : b) * 2 * (size_t)n * 4;
+}
+
+extern "C" rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* dY,
+                                                int64_t lddy, const void* X, int64_t ldx, const void* weight,
+                                                const float* mean, const float* rstd, void* dX, int64_t lddx,
+                                                void* dweight, void* dbias, int64_t rows, int64_t n, void* ws,
+                                                size_t ws_bytes, void* stream) {
+  rgc_status_t st = check_shape(kind, xt, wt, rows, n);
+  if (st != RGC_OK) return st;
+  if (!dweight) return RGC_ERR_NULL;
+  if (!aligned_to(dweight, elem(wt)) || !aligned_to(dbias, elem(wt))) return RGC_ERR_ALIGN;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const dim3 params((unsigned)((n + 63) / 64), dbias ? 2 : 1);
+  if (rows == 0) {  // sums over no rows
+    hipLaunchKernelGGL(norm_params_kernel, params, dim3(1024), 0, s, nullptr, (int64_t)0, n, (int)(wt == RGC_F32),
+                       dweight, dbias);
+    return launched();
+  }
+  if ((st = check_rows(dY, lddy, n, xt)) != RGC_OK) return st;
+  if ((st = check_rows(X, ldx, n, xt)) != RGC_OK) return st;
+  if ((st = check_rows(dX, lddx, n, xt)) != RGC_OK) return st;
+  if (!rstd || (kind == RGC_NORM_LAYER && !mean)) return RGC_ERR_NULL;
+  if (!aligned_to(weight, elem(wt)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4)) return RGC_ERR_ALIGN;
+  if (!ws || ws_bytes < rgc_layer_norm_backward_workspace_size(rows, n)) return RGC_ERR_WORKSPACE;
+  if (!aligned_to(ws, 256)) return RGC_ERR_ALIGN;
+  NormArgs a{};
+  a.x = X, a.dy = dY, a.w = weight, a.out = dX, a.part = static_cast<float*>(ws);
+  a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
+  a.ldx = ldx, a.lddy = lddy, a.ldo = lddx, a.rows = rows, a.n = n;
+  a.w_f32 = wt == RGC_F32, a.centre = kind == RGC_NORM_LAYER, a.db = dbias != nullptr;
+  const bool vec = vectors(X, ldx, n, xt) && vectors(dY, lddy, n, xt) && vectors(dX, lddx, n, xt) && aligned16(weight);
+  const int64_t G = backward_groups(rows, n, vec);
+  if (xt == RGC_F32) backward_pick<float>(a, vec, G, s);
+  else backward_pick<uint16_t>(a, vec, G, s);
+  if ((st = launched()) != RGC_OK) return st;
+  hipLaunchKernelGGL(norm_params_kernel, params, dim3(1024), 0, s, a.part, G, n, a.w_f32, dweight, dbias);
+  return launched();
+}

@@ -16,6 +16,14 @@ Names mirror the C ABI in include/rgc.h:
                                             P regenerated from its seed, then one of the two
   rgc_linear_forward(X, W, P)               (Y, XP) = (bf16(X W^T), bf16(X P)), one tile grid
   rgc_linear_backward(D, W, XP, C)          dX = bf16(D W), then C += D^T XP
+  rgc_linear_cross_entropy_forward(X, W, targets, P)
+                                            (loss, lse, XP) of the softmax of X W^T, which is not kept
+  rgc_linear_cross_entropy_backward(X, W, targets, lse, grad, XP, C)
+                                            dX, and C += D^T XP of the same
+  rgc_layer_norm_forward(X, weight, bias)   (Y, mean, rstd) of a layer or root-mean-square norm
+  rgc_layer_norm_backward(dY, X, weight, mean, rstd)
+                                            (dX, dweight, dbias)
+  rgc_adamw_batch(Ps, Gs, Ms, Vs, lr, step) one AdamW step over many tensors (in place)
 """
 from __future__ import annotations
 
@@ -34,12 +42,20 @@ _KINDS = {"rademacher": RGC_PROJ_RADEMACHER, "qr": RGC_PROJ_QR_GAUSSIAN}
 RGC_UPDATE_NORMALIZED = 0
 RGC_UPDATE_SCALED = 1
 _MODES = {"normalized": RGC_UPDATE_NORMALIZED, "scaled": RGC_UPDATE_SCALED}
+RGC_BF16 = 0
+RGC_F32 = 1
+_DTYPES = {torch.bfloat16: RGC_BF16, torch.float32: RGC_F32}
+RGC_NORM_LAYER = 0
+RGC_NORM_RMS = 1
+_NORMS = {"layer": RGC_NORM_LAYER, "rms": RGC_NORM_RMS}
+ADAMW_BLOCK = 128  # elements of an 8-bit state that share a scale
 
 _i64 = ctypes.c_int64
 _u64 = ctypes.c_uint64
 _sz = ctypes.c_size_t
 _vp = ctypes.c_void_p
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 
 # (name, restype, argtypes) for every exported function of include/rgc.h
 SIGNATURES = {
@@ -95,6 +111,21 @@ SIGNATURES = {
     "rgc_linear_backward_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
     "rgc_linear_backward": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _sz,
                                            _vp]),
+    "rgc_linear_cross_entropy_forward_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
+    "rgc_linear_cross_entropy_forward": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                                                        _i64, _vp, _sz, _vp]),
+    "rgc_linear_cross_entropy_backward_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
+    "rgc_linear_cross_entropy_backward": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                                                         _i64, _i64, _i64, _vp, _sz, _vp]),
+    "rgc_layer_norm_forward": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _i64, _vp, _vp, _f64, _vp,
+                                              _i64, _vp, _vp, _i64, _i64, _vp]),
+    "rgc_layer_norm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "rgc_layer_norm_backward": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _vp,
+                                               _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "rgc_adamw_batch": (ctypes.c_int, [_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(_vp),
+                                       ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_vp),
+                                       ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_i64), _f64, _f64, _f64,
+                                       _f64, _f64, _i64, _vp, _u64, _vp]),
     "rgc_test_philox": (ctypes.c_int, [_u64, _i64, _vp, _vp, _vp]),
     "rgc_test_stochastic_round": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _i64, _i64, _u64, _vp]),
     "rgc_test_round_nearest": (ctypes.c_int, [_vp, _vp, _i64, _vp]),
@@ -630,6 +661,238 @@ def rgc_apply_from_seed(mode: str, kind: str, proj_seed: int, W: torch.Tensor, C
                                    C.data_ptr(), d, k, r, float(step), seed & 0xFFFFFFFFFFFFFFFF, sp, wp, wn,
                                    _stream(dev)))
     return W
+
+
+# ---- the head's loss, norms and AdamW ----------------------------------------
+
+def _on(dev: torch.device):
+    """Makes dev the current device for a call (its tensors may live on another than the current one)."""
+    return torch.cuda.device(dev)
+
+
+def _scratch(workspace: Workspace | None, nbytes: int, dev: torch.device):
+    """(pointer, size, owner) of a call's workspace: the given Workspace's, or a
+    buffer of the call's own from torch's allocator, which orders its reuse on
+    the stream and keeps it for a graph that captured the call."""
+    if workspace is not None:
+        return (*workspace.get(nbytes), workspace.buf)
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return ctypes.c_void_p(buf.data_ptr()), nbytes, buf
+
+
+def _head_args(X, W, targets):
+    ldx = _rows(X, torch.bfloat16, "X")
+    ldw = _rows(W, torch.bfloat16, "W")
+    _dense(targets, torch.int64, "targets")
+    T, k = X.shape
+    if W.shape[1] != k or tuple(targets.shape) != (T,):
+        raise RgcError("shapes must be X: T x k, W: V x k, targets: T")
+    return ldx, ldw, T, W.shape[0], k
+
+
+def rgc_linear_cross_entropy_forward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
+                                     P: torch.Tensor | None = None, workspace: Workspace | None = None):
+    """(loss, lse, XP): per token t the softmax cross entropy of X W^T against
+    targets[t] (0 where the target lies outside 0 .. V-1) and the logits' log
+    sum of exponentials, both float32, with the logits never stored; XP =
+    bf16(X P), or None without P. X: T x k, W: V x k bf16, targets: int64."""
+    lib = load_library()
+    dev = _need_gpu(X, W, targets, *([P] if P is not None else []))
+    ldx, ldw, T, V, k = _head_args(X, W, targets)
+    r, XP = 0, None
+    if P is not None:
+        _dense(P, torch.bfloat16, "P")
+        if P.dim() != 2 or P.shape[0] != k or P.shape[1] == 0:
+            raise RgcError("P must be k x r with k = X.shape[1]")
+        r = P.shape[1]
+        XP = torch.empty((T, r), dtype=torch.bfloat16, device=dev)
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    with _on(dev):
+        wp, wn, _keep = _scratch(workspace, lib.rgc_linear_cross_entropy_forward_workspace_size(T, V, k, r), dev)
+        _check(lib.rgc_linear_cross_entropy_forward(X.data_ptr(), ldx, W.data_ptr(), ldw, P.data_ptr() if r else None,
+                                                    targets.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                                                    XP.data_ptr() if r else None, T, V, k, r, wp, wn, _stream(dev)))
+    return loss, lse, XP
+
+
+def rgc_linear_cross_entropy_backward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                                      grad: torch.Tensor, XP: torch.Tensor | None = None, C: torch.Tensor | None = None,
+                                      dX: torch.Tensor | None = None, workspace: Workspace | None = None) -> torch.Tensor:
+    """dX = bf16(D W) with D_tv = grad[t] (softmax(X W^T)_tv - [v = targets[t]]),
+    and, with XP and C, C += D^T XP (V x r float32). lse is the forward's; grad:
+    float32, the gradient of each token's loss. D exists a piece of the
+    vocabulary at a time."""
+    lib = load_library()
+    dev = _need_gpu(X, W, targets, lse, grad, *[t for t in (XP, C, dX) if t is not None])
+    ldx, ldw, T, V, k = _head_args(X, W, targets)
+    _dense(lse, torch.float32, "lse")
+    _dense(grad, torch.float32, "grad")
+    if tuple(lse.shape) != (T,) or tuple(grad.shape) != (T,):
+        raise RgcError("lse and grad must have one value per token")
+    if (XP is None) != (C is None):
+        raise RgcError("XP and C go together")
+    r = 0
+    if C is not None:
+        _dense(XP, torch.bfloat16, "XP")
+        _dense(C, torch.float32, "C")
+        r = C.shape[-1]
+        if r == 0 or tuple(C.shape) != (V, r) or tuple(XP.shape) != (T, r):
+            raise RgcError("shapes must be XP: T x r, C: V x r")
+    if dX is None:
+        dX = torch.empty((T, k), dtype=torch.bfloat16, device=dev)
+    lddx = _rows(dX, torch.bfloat16, "dX")
+    if tuple(dX.shape) != (T, k):
+        raise RgcError("dX must be T x k")
+    with _on(dev):
+        wp, wn, _keep = _scratch(workspace, lib.rgc_linear_cross_entropy_backward_workspace_size(T, V, k, r), dev)
+        _check(lib.rgc_linear_cross_entropy_backward(X.data_ptr(), ldx, W.data_ptr(), ldw, targets.data_ptr(),
+                                                     lse.data_ptr(), grad.data_ptr(), XP.data_ptr() if r else None,
+                                                     C.data_ptr() if r else None, dX.data_ptr(), lddx, T, V, k, r, wp, wn,
+                                                     _stream(dev)))
+    return dX
+
+
+def _norm_rows(t: torch.Tensor, like: torch.Tensor, name: str) -> int:
+    if t.dtype not in _DTYPES or t.dtype != like.dtype:
+        raise RgcError(f"{name} must be bf16 or float32, and of X's type")
+    if t.shape != like.shape:
+        raise RgcError(f"{name} must have X's shape")
+    return _rows(t, t.dtype, name)
+
+
+def _norm_params(n: int, weight, bias):
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            if t.dtype not in _DTYPES or not t.is_contiguous() or tuple(t.shape) != (n,):
+                raise RgcError(f"{name} must be a contiguous bf16 or float32 tensor of X.shape[1] elements")
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise RgcError("weight and bias must have one type")
+    return _DTYPES[(weight if weight is not None else bias).dtype] if weight is not None or bias is not None else RGC_F32
+
+
+def _norm_kind(kind: str) -> int:
+    if kind not in _NORMS:
+        raise RgcError('kind must be "layer" or "rms"')
+    return _NORMS[kind]
+
+
+def rgc_layer_norm_forward(X: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                           eps: float = 1e-5, kind: str = "layer", Y: torch.Tensor | None = None):
+    """(Y, mean, rstd) of the norm of X's rows (kind "layer"), or of their
+    root-mean-square norm (kind "rms", mean None). X: rows x n, bf16 or float32;
+    weight, bias: n elements, bf16 or float32, or None."""
+    lib = load_library()
+    dev = _need_gpu(X, *[t for t in (weight, bias, Y) if t is not None])
+    ldx = _norm_rows(X, X, "X")
+    rows, n = X.shape
+    kid = _norm_kind(kind)
+    wt = _norm_params(n, weight, bias)
+    if Y is None:
+        Y = torch.empty((rows, n), dtype=X.dtype, device=dev)
+    ldy = _norm_rows(Y, X, "Y")
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if kid == RGC_NORM_LAYER else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    with _on(dev):
+        _check(lib.rgc_layer_norm_forward(kid, _DTYPES[X.dtype], wt, X.data_ptr(), ldx,
+                                          weight.data_ptr() if weight is not None else None,
+                                          bias.data_ptr() if bias is not None else None, eps, Y.data_ptr(), ldy,
+                                          mean.data_ptr() if mean is not None else None, rstd.data_ptr(), rows, n,
+                                          _stream(dev)))
+    return Y, mean, rstd
+
+
+def rgc_layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor | None,
+                            rstd: torch.Tensor, bias: bool = True, kind: str = "layer", dX: torch.Tensor | None = None,
+                            workspace: Workspace | None = None):
+    """(dX, dweight, dbias) from dY and the forward's mean and rstd; dweight and
+    dbias have the weight's type (float32 without a weight), dbias is None with
+    bias False."""
+    lib = load_library()
+    dev = _need_gpu(dY, X, rstd, *[t for t in (weight, mean, dX) if t is not None])
+    ldx, lddy = _norm_rows(X, X, "X"), _norm_rows(dY, X, "dY")
+    rows, n = X.shape
+    kid = _norm_kind(kind)
+    wt = _norm_params(n, weight, None)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t is None:
+            if kid == RGC_NORM_LAYER:
+                raise RgcError("a layer norm's backward needs the forward's mean")
+            continue
+        _dense(t, torch.float32, name)
+        if tuple(t.shape) != (rows,):
+            raise RgcError(f"{name} must have one value per row")
+    if dX is None:
+        dX = torch.empty((rows, n), dtype=X.dtype, device=dev)
+    lddx = _norm_rows(dX, X, "dX")
+    pt = torch.float32 if weight is None else weight.dtype
+    dweight = torch.empty(n, dtype=pt, device=dev)
+    dbias = torch.empty(n, dtype=pt, device=dev) if bias else None
+    with _on(dev):
+        wp, wn, _keep = _scratch(workspace, lib.rgc_layer_norm_backward_workspace_size(rows, n), dev)
+        _check(lib.rgc_layer_norm_backward(kid, _DTYPES[X.dtype], wt, dY.data_ptr(), lddy, X.data_ptr(), ldx,
+                                           weight.data_ptr() if weight is not None else None,
+                                           mean.data_ptr() if mean is not None else None, rstd.data_ptr(),
+                                           dX.data_ptr(), lddx, dweight.data_ptr(),
+                                           dbias.data_ptr() if bias else None, rows, n, wp, wn, _stream(dev)))
+    return dX, dweight, dbias
+
+
+def _adamw_list(ts, name: str, dev, dtypes, sizes):
+    """The pointers of a list of dense tensors of one of `dtypes`, of the given element counts."""
+    dtype = ts[0].dtype
+    if dtype not in dtypes:
+        raise RgcError(f"{name} must be " + " or ".join(str(d) for d in dtypes))
+    for t, n in zip(ts, sizes):
+        if t.dtype != dtype or t.device != dev or t.numel() != n or not t.is_contiguous():
+            raise RgcError(f"{name} must be contiguous tensors of one type, on one device, of the parameters' sizes")
+    return _ptrs(ts)
+
+
+def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: float = 0.9, beta2: float = 0.999,
+                    eps: float = 1e-8, weight_decay: float = 0.0, M_scales=None, V_scales=None,
+                    grad_scale: torch.Tensor | None = None):
+    """One AdamW step, in place, over lists of parameters Ps and gradients Gs
+    (each list bf16 or float32) with moments Ms and Vs: float32, or
+    float8_e4m3fn with M_scales and V_scales (float32, one per 128 elements; Vs
+    then holds square roots). `step` counts from 1; bf16 parameters and 8-bit
+    second moments are rounded stochastically from `seed`. grad_scale: a device
+    float32 that multiplies every gradient; one that is not finite skips the step."""
+    lib = load_library()
+    n = len(Ps)
+    eight = M_scales is not None or V_scales is not None
+    lists = [Gs, Ms, Vs] + ([M_scales, V_scales] if eight else [])
+    if any(x is None or len(x) != n for x in lists):
+        raise RgcError("Ps, Gs, Ms, Vs (and the scales) must be lists of one length")
+    if n == 0:
+        return Ps
+    dev = _need_gpu(Ps[0], *([grad_scale] if grad_scale is not None else []))
+    sizes = [p.numel() for p in Ps]
+    state = (torch.float8_e4m3fn,) if eight else (torch.float32,)
+    pp = _adamw_list(Ps, "Ps", dev, _DTYPES, sizes)
+    gp = _adamw_list(Gs, "Gs", dev, _DTYPES, sizes)
+    mp = _adamw_list(Ms, "Ms", dev, state, sizes)
+    vp = _adamw_list(Vs, "Vs", dev, state, sizes)
+    msp = vsp = None
+    if eight:
+        blocks = [(s + ADAMW_BLOCK - 1) // ADAMW_BLOCK for s in sizes]
+        msp = _adamw_list(M_scales, "M_scales", dev, (torch.float32,), blocks)
+        vsp = _adamw_list(V_scales, "V_scales", dev, (torch.float32,), blocks)
+    if n > 1:
+        for ptrs in (pp, mp, vp):
+            given = [p for p, s in zip(ptrs, sizes) if s]
+            if len(set(given)) != len(given):
+                raise RgcError("a tensor is listed twice")
+    if grad_scale is not None:
+        _dense(grad_scale, torch.float32, "grad_scale")
+        if grad_scale.numel() != 1:
+            raise RgcError("grad_scale must be one float32")
+    with _on(dev):
+        _check(lib.rgc_adamw_batch(n, _DTYPES[Ps[0].dtype], _DTYPES[Gs[0].dtype], 8 if eight else 32, pp, gp, mp, vp,
+                                   msp, vsp, _i64s(sizes), lr, beta1, beta2, eps, weight_decay, step,
+                                   grad_scale.data_ptr() if grad_scale is not None else None,
+                                   seed & 0xFFFFFFFFFFFFFFFF, _stream(dev)))
+    return Ps
 
 
 # ---- test hooks -------------------------------------------------------------
