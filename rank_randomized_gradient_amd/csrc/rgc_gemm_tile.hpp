@@ -16,9 +16,10 @@
 // * One barrier a step, before the last phase: every wave has read all of the
 //   step's stage by then, so it is refilled for the step after next, and the
 //   next step's copies, issued a step ago, have been waited for.
-// * LDS rows of 128 bytes: 16-byte chunk q of row t sits at slot
-//   q ^ (t % 8) ^ (t / 8 % 2), so that 8 consecutive rows at one chunk touch 8
-//   slots and 16 rows touch each half of the 64 banks alike. K-major slabs
+// * LDS rows of 128 bytes: 16-byte chunk q of row t sits at slot q ^ (t % 8),
+//   which reads sixteen lanes a clock without a bank conflict (counted: none).
+//   With q ^ (t % 8) ^ (t / 8 % 2), which would suit sixteen consecutive
+//   lanes, half of the LDS cycles were conflicts. K-major slabs
 //   are blocks of 4 K rows x 16 columns read with transposing reads, block
 //   (kq, b) at place b ^ (kq / 2 % 2) of its row of sixteen.
 // * The MFMA takes B's fragment on its M side, so a lane ends with four
@@ -37,14 +38,6 @@ constexpr int kGtThreads = 512;
 constexpr int kGtSlab = 32768;
 constexpr int kGtStage = 2 * kGtSlab;
 constexpr int kGtLds = 2 * kGtStage;
-
-// Source of the 16-byte chunks behind the end of K.
-__device__ const uint32_t kGtZeros[4] = {0u, 0u, 0u, 0u};
-
-// As dma_16b_cached, every lane with an address of its own.
-__device__ __forceinline__ void dma_16b_lanes(const void* p, uint32_t lds_addr) {
-  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds_addr) : "memory");
-}
 
 struct GtFrag {
   uint32_t r[4];
@@ -83,23 +76,24 @@ struct GtTile {
         const int64_t last = (v < 4 ? m_rem : n_rem) - 1;
         int64_t row = 8 * c + (lane >> 3);
         row = row < last ? row : last;
-        voff[v] = (uint32_t)((row * (v < 4 ? lda : ldb) + 8 * chunk(c)) * 2);
+        voff[v] = (uint32_t)((row * (v < 4 ? lda : ldb) + 8 * chunk()) * 2);
       } else {
         int64_t col = column(c);
         col = col + 8 <= n_rem ? col : n_rem - 8;
         voff[v] = (uint32_t)((krow(c) * ldb + col) * 2);
       }
     }
-    const int swz = (li & 7) ^ (li >> 3);
+    const int swz = li & 7;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       fa[kk] = (uint32_t)(128 * (128 * (wave & 1) + li) + 16 * ((4 * kk + g) ^ swz));
       if constexpr (!BKM) fb[kk] = (uint32_t)(kGtSlab + 128 * (64 * (wave >> 1) + li) + 16 * ((4 * kk + g) ^ swz));
     }
     if constexpr (BKM) {
-      // block rows kq = 8 kk + 2 g + h: kq / 2 % 2 = g % 2, so columns 4 wn + b sit at (4 wn + b) ^ (g % 2)
-      fb[0] = (uint32_t)(kGtSlab + 128 * (32 * g + 4 * (wave >> 1)) + 8 * li);
-      fb[1] = (uint32_t)(g & 1);
+      // block rows kq = 8 kk + 2 g + h: kq / 2 % 2 = g % 2, so even and odd blocks change places where g is odd
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+        fb[nt] = (uint32_t)(kGtSlab + 128 * (32 * g + 4 * (wave >> 1) + (nt ^ (g & 1))) + 8 * li);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -107,41 +101,51 @@ struct GtTile {
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
 
-  // chunk of the row that lane l of copy c fetches (K-contiguous slabs)
-  __device__ __forceinline__ int chunk(int c) const { return (lane & 7) ^ (lane >> 3) ^ (c & 1); }
+  // chunk of its row that a lane fetches (K-contiguous slabs)
+  __device__ __forceinline__ int chunk() const { return (lane & 7) ^ (lane >> 3); }
   // K row and column that lane l of copy c fetches (K-major slabs): blocks 8 c .. 8 c + 7
-  __device__ __forceinline__ int64_t krow(int c) const { return 4 * (c >> 1) + ((lane & 7) >> 1); }
+  __device__ __forceinline__ int krow(int c) const { return 4 * (c >> 1) + ((lane & 7) >> 1); }
   __device__ __forceinline__ int64_t column(int c) const {
     const int place = 8 * (c & 1) + (lane >> 3);
     return 16 * (place ^ ((c >> 2) & 1)) + 8 * (lane & 1);
   }
 
+  // Copy v of this wave, from the step's bases. `left`: elements of K from the
+  // step on; where they are fewer than a step, the lanes behind the end fetch
+  // the last chunk (or K row) instead, which settle() clears or A's zeros cancel.
+  __device__ __forceinline__ void copy(int v, const uint16_t* Ab, const uint16_t* Bb, uint32_t st, int left) const {
+    const int c = wave + 8 * (v & 3);
+    int over;
+    if (v < 4 || !BKM) {
+      over = chunk() - (left - 1) / 8;
+      over = 16 * (over > 0 ? over : 0);
+    } else {
+      over = krow(c) - (left - 1);
+      over = (over > 0 ? over : 0) * (int)(2 * ldb);
+    }
+    dma_16b_cached(v < 4 ? Ab : Bb, voff[v] - (uint32_t)over, st + (v < 4 ? 0 : kGtSlab) + 1024 * c);
+  }
+  __device__ __forceinline__ int left_of(int64_t step) const {
+    const int64_t left = K - step * kGtStep;
+    return left < kGtStep ? (int)left : kGtStep;
+  }
   __device__ __forceinline__ void issue(int64_t step, uint32_t stage) const {
     const int64_t k0 = step * kGtStep;
     const uint16_t* Ab = uniform_ptr(A + k0);
     const uint16_t* Bb = uniform_ptr(BKM ? B + k0 * ldb : B + k0);
-    const uint32_t st = lds0 + stage * kGtStage;
-    if (k0 + kGtStep <= K) {
 #pragma unroll
-      for (int v = 0; v < 8; ++v)
-        dma_16b_cached(v < 4 ? Ab : Bb, voff[v], st + (v < 4 ? 0 : kGtSlab) + 1024 * (wave + 8 * (v & 3)));
-    } else {
-      // the last step of a K that is no multiple of 64: chunks behind the end
-      // come from zeros (K rows of a K-major B, whose products with A's zeros
-      // vanish, from the last row)
-#pragma unroll
-      for (int v = 0; v < 8; ++v) {
-        const int c = wave + 8 * (v & 3);
-        const char* p = reinterpret_cast<const char*>(v < 4 ? Ab : Bb) + voff[v];
-        if (v < 4 || !BKM) {
-          if (k0 + 8 * chunk(c) >= K) p = reinterpret_cast<const char*>(kGtZeros);
-        } else {
-          const int64_t kr = krow(c), over = k0 + kr - (K - 1);
-          if (over > 0) p -= over * ldb * 2;
-        }
-        dma_16b_lanes(p, st + (v < 4 ? 0 : kGtSlab) + 1024 * c);
-      }
+    for (int v = 0; v < 8; ++v) copy(v, Ab, Bb, lds0 + stage * kGtStage, left_of(step));
+  }
+  // After the barrier that ends a step's copies: clears the chunks behind the
+  // end of K in the last step.
+  __device__ __forceinline__ void settle(int64_t step, uint32_t stage) const {
+    const int64_t left = K - step * kGtStep;
+    if (left >= kGtStep) return;
+    for (int p = threadIdx.x; p < (BKM ? 1 : 2) * kGtSlab / 16; p += kGtThreads) {
+      const int row = (p >> 3) & 255, q = (p & 7) ^ (row & 7);
+      if (8 * q >= left) *(RGC_LDS u32x4v_t*)(lds + stage * kGtStage + 16 * p) = u32x4v_t{0u, 0u, 0u, 0u};
     }
+    lds_barrier();
   }
 
   __device__ __forceinline__ GtFrag read16(uint32_t off) const {
@@ -164,8 +168,7 @@ struct GtTile {
         if constexpr (BKM) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const u32x2v_t v = lds_read_tr16(lds + fb[0] + stage * kGtStage + 128 * (16 * (8 * kk + h)) +
-                                             128 * ((2 * H + nt) ^ fb[1]));
+            const u32x2v_t v = lds_read_tr16(lds + fb[nt] + stage * kGtStage + 2048 * (8 * kk + h) + 256 * H);
             b[nt][kk].r[2 * h] = v.x;
             b[nt][kk].r[2 * h + 1] = v.y;
           }
@@ -198,11 +201,14 @@ struct GtTile {
     if (s + 1 < nsteps) {
       wait_vmcnt<0>();
       lds_barrier();
-      if (s + 2 < nsteps) issue(s + 2, STAGE);
+      settle(s + 1, STAGE ^ 1);
       read_a<0>(a0, STAGE ^ 1);
       read_b<0>(y, STAGE ^ 1);
     }
+    __builtin_amdgcn_s_setprio(1);
+    if (s + 2 < nsteps) issue(s + 2, STAGE);
     multiply<1, 0>(a1, x);
+    __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -216,6 +222,7 @@ struct GtTile {
       wait_vmcnt<0>();
     }
     lds_barrier();
+    settle(0, 0);
     read_a<0>(a0, 0);
     read_b<0>(b0, 0);
     for (int64_t s = 0; s < nsteps; s += 2) {

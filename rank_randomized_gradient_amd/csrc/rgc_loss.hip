@@ -19,9 +19,11 @@
 //
 // The sketch is fp32, and a D rounded once to bf16 would put an error of 2^-9
 // into each of its terms. So with a sketch D is kept as two bf16 terms,
-// D = hi + lo (error 2^-17), stacked along the tokens: C += [hi; lo]^T [XP; XP]
-// is one accumulation over 2 T tokens. dX is rounded to bf16 itself and takes
-// hi alone.
+// D = hi + lo (error 2^-18), stacked along the tokens: C += [hi; lo]^T [XP; XP]
+// is one accumulation over 2 T tokens. What two terms still leave of the
+// targets' entries, by far the largest of D (of the order of g, the others of
+// g / V), is kept in fp32, one value a token, and added in a last launch. dX is
+// rounded to bf16 itself and takes hi alone.
 //
 // Bound by MFMA: 2 T V k operations for the loss, 6 T V k + 4 T V r for the
 // gradient. Where dX has few tiles (few tokens), each is split over K among
@@ -51,44 +53,70 @@ struct CeArgs {
   const float* lse;    // backward
   const float* grad;
   uint16_t* hi;        // backward: T x ldd, bf16
-  uint16_t* lo;        // or null
+  uint16_t* lo;        // or null: no sketch
+  float* rest;         // with lo: D - hi - lo at each token's target
   int64_t ldd;
 };
 
-// The target's column counted from a lane's first one (the lane holds columns
-// 16 nt + e from there), or a number that is none of them.
-__device__ __forceinline__ int target_column(int64_t y, int64_t v0, int64_t V, int64_t first) {
-  const int64_t c = y - v0, at = c - first;
-  return c >= 0 && c < V && at >= 0 && at < 64 ? (int)at : -1;
+// What an epilogue needs of a tile's rows, fetched before the product.
+struct CeRows {
+  float lse[kGtTile], grad[kGtTile];
+  int at[kGtTile];  // the target's column in the tile; -1: elsewhere; -2: an ignored token
+};
+
+__device__ __forceinline__ void load_rows(const CeArgs& a, int64_t m0, int64_t n0, bool backward, CeRows* r) {
+  const int row = threadIdx.x;
+  if (row >= kGtTile) return;
+  const bool live = m0 + row < a.T;
+  const int64_t y = live ? a.targets[m0 + row] : -1, c = y - a.v0 - n0;
+  r->at[row] = y < 0 || y >= a.vocab ? -2 : c >= 0 && c < kGtTile ? (int)c : -1;
+  if (backward) {
+    r->lse[row] = live ? a.lse[m0 + row] : 0.f;
+    r->grad[row] = live ? a.grad[m0 + row] : 0.f;
+  }
 }
+
+// exp(x); below 2^-126 it is zero.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 __global__ __launch_bounds__(kGtThreads, 1) void ce_forward_kernel(CeArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[kGtLds];
+  __shared__ CeRows rows;
   int64_t i, j;
   gt_place(gt_logical(blockIdx.x, gridDim.x), a.mtiles, a.ntiles, kCeDown, &i, &j);
   const int64_t m0 = i * kGtTile, n0 = j * kGtTile;
+  load_rows(a, m0, n0, false, &rows);
   GtTile<false> t;
   t.init(a.X + m0 * a.ldx, a.ldx, a.W + n0 * a.ldw, a.ldw, a.T - m0, a.V - n0, a.k, smem);
   t.run();
 
   const int g = t.lane >> 4, li = t.lane & 15, wm = t.wave & 1, wn = t.wave >> 1;
-  float* rows = reinterpret_cast<float*>(smem);  // [row][wn]: maximum, sum
-  const int64_t first = n0 + 64 * wn + 4 * g;
+  float* sums = reinterpret_cast<float*>(smem);  // [row][wn]: maximum, sum
+  const int first = 64 * wn + 4 * g;
+  const int width = (int)(a.V - n0 < kGtTile ? a.V - n0 : kGtTile);
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) {
     const int row = 128 * wm + 16 * mt + li;
-    const bool live = m0 + row < a.T;
-    const int64_t y = live ? a.targets[m0 + row] : -1;
-    const int at = target_column(y, a.v0, a.V, first);
-    float z[4][4], top = -INFINITY;
+    const int at = rows.at[row] - first;
+    if (__builtin_expect(width < kGtTile, 0)) {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (first + 16 * nt + e >= width) t.acc[mt][nt][e] = -INFINITY;
+    }
+    if (__any(at >= 0 && at < 64)) {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (16 * nt + e == at) a.zt[m0 + row] = t.acc[mt][nt][e];
+    }
+    float top = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        z[nt][e] = first + 16 * nt + e < a.V ? t.acc[mt][nt][e] : -INFINITY;
-        top = fmaxf(top, z[nt][e]);
-        if (16 * nt + e == at) a.zt[m0 + row] = z[nt][e];
-      }
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, t.acc[mt][nt][e]);
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const float base = top == -INFINITY ? 0.f : top;
@@ -96,23 +124,23 @@ __global__ __launch_bounds__(kGtThreads, 1) void ce_forward_kernel(CeArgs a) {
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s += exp2f((z[nt][e] - base) * kLog2e);
+      for (int e = 0; e < 4; ++e) s += fast_exp(t.acc[mt][nt][e] - base);
     s += __shfl_xor(s, 16, 64);
     s += __shfl_xor(s, 32, 64);
     if (g == 0) {
-      rows[8 * row + 2 * wn] = top;
-      rows[8 * row + 2 * wn + 1] = s;
+      sums[8 * row + 2 * wn] = top;
+      sums[8 * row + 2 * wn + 1] = s;
     }
   }
   __syncthreads();
   const int row = threadIdx.x;
   if (row < kGtTile && m0 + row < a.T) {
-    float top = rows[8 * row], s = 0.f;
+    float top = sums[8 * row], s = 0.f;
 #pragma unroll
-    for (int w = 1; w < 4; ++w) top = fmaxf(top, rows[8 * row + 2 * w]);
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, sums[8 * row + 2 * w]);
     const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) s += rows[8 * row + 2 * w + 1] * exp2f((rows[8 * row + 2 * w] - base) * kLog2e);
+    for (int w = 0; w < 4; ++w) s += sums[8 * row + 2 * w + 1] * fast_exp(sums[8 * row + 2 * w] - base);
     a.part[j * a.T + m0 + row] = make_float2(top, s);
   }
 }
@@ -129,7 +157,7 @@ __global__ __launch_bounds__(1024) void ce_finish_kernel(CeArgs a, float* loss, 
     for (int64_t j = wave; j < a.ntiles; j += 16) {
       const float2 p = a.part[j * a.T + t];
       const float m = fmaxf(top, p.x), base = m == -INFINITY ? 0.f : m;
-      s = s * exp2f((top - base) * kLog2e) + p.y * exp2f((p.x - base) * kLog2e);
+      s = s * fast_exp(top - base) + p.y * fast_exp(p.x - base);
       top = m;
     }
   }
@@ -140,7 +168,7 @@ __global__ __launch_bounds__(1024) void ce_finish_kernel(CeArgs a, float* loss, 
     for (int w = 1; w < 16; ++w) top = fmaxf(top, tops[w][lane]);
     const float base = top == -INFINITY ? 0.f : top;
     s = 0.f;
-    for (int w = 0; w < 16; ++w) s += sums[w][lane] * exp2f((tops[w][lane] - base) * kLog2e);
+    for (int w = 0; w < 16; ++w) s += sums[w][lane] * fast_exp(tops[w][lane] - base);
     const float l = top + logf(s);
     const int64_t y = a.targets[t];
     lse[t] = l;
@@ -149,41 +177,116 @@ __global__ __launch_bounds__(1024) void ce_finish_kernel(CeArgs a, float* loss, 
 }
 
 // A piece's D, hi (and lo): T x ldd, zero in the columns behind the piece.
+// The tile's bf16 values are laid out in LDS first, so that they are stored in
+// whole 512-byte rows (16-byte chunk q of row t at place q ^ (t % 16)). The
+// lo pass forms D - hi from the fp32 values, which stay in the registers.
 __global__ __launch_bounds__(kGtThreads, 1) void ce_d_kernel(CeArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[kGtLds];
+  __shared__ CeRows rows;
   int64_t i, j;
   gt_place(gt_logical(blockIdx.x, gridDim.x), a.mtiles, a.ntiles, kCeDown, &i, &j);
   const int64_t m0 = i * kGtTile, n0 = j * kGtTile;
+  load_rows(a, m0, n0, true, &rows);
   GtTile<false> t;
   t.init(a.X + m0 * a.ldx, a.ldx, a.W + n0 * a.ldw, a.ldw, a.T - m0, a.V - n0, a.k, smem);
   t.run();
 
   const int g = t.lane >> 4, li = t.lane & 15, wm = t.wave & 1, wn = t.wave >> 1;
-  const int64_t first = n0 + 64 * wn + 4 * g;
+  const int first = 64 * wn + 4 * g;
+  const int width = (int)(a.V - n0 < kGtTile ? a.V - n0 : kGtTile);
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) {
-    const int64_t row = m0 + 128 * wm + 16 * mt + li;
-    if (row >= a.T) continue;
-    const int64_t y = a.targets[row];
-    const bool kept = y >= 0 && y < a.vocab;
-    const int at = target_column(y, a.v0, a.V, first);
-    const float lse = a.lse[row], gr = a.grad[row];
+    const int row = 128 * wm + 16 * mt + li;
+    const int target = rows.at[row], at = target - first;
+    const float lse = rows.lse[row], gr = rows.grad[row];
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      float d[4];
+    for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float p = exp2f((t.acc[mt][nt][e] - lse) * kLog2e);
-        d[e] = kept && first + 16 * nt + e < a.V ? (16 * nt + e == at ? p - 1.f : p) * gr : 0.f;
+        const float p = fast_exp(t.acc[mt][nt][e] - lse) * gr;
+        t.acc[mt][nt][e] = target == -2 ? 0.f : p;
       }
-      const uint2 h = make_uint2(f32x2_to_bf16x2_rne(d[0], d[1]), f32x2_to_bf16x2_rne(d[2], d[3]));
-      *reinterpret_cast<uint2*>(a.hi + row * a.ldd + first + 16 * nt) = h;
-      if (a.lo)
-        *reinterpret_cast<uint2*>(a.lo + row * a.ldd + first + 16 * nt) =
-            make_uint2(f32x2_to_bf16x2_rne(d[0] - __uint_as_float(h.x << 16), d[1] - __uint_as_float(h.x & 0xFFFF0000u)),
-                       f32x2_to_bf16x2_rne(d[2] - __uint_as_float(h.y << 16), d[3] - __uint_as_float(h.y & 0xFFFF0000u)));
+    if (__any(at >= 0 && at < 64)) {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (16 * nt + e == at) t.acc[mt][nt][e] -= gr;
+    }
+    if (__builtin_expect(width < kGtTile, 0)) {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (first + 16 * nt + e >= width) t.acc[mt][nt][e] = 0.f;
     }
   }
+  for (int term = 0; term < (a.lo ? 2 : 1); ++term) {
+    if (term) __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      const int row = 128 * wm + 16 * mt + li;
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const f32x4_t d = t.acc[mt][nt];
+        uint2 h = make_uint2(f32x2_to_bf16x2_rne(d[0], d[1]), f32x2_to_bf16x2_rne(d[2], d[3]));
+        // D - hi, exact: hi is D's leading bits
+        t.acc[mt][nt] = d - f32x4_t{__uint_as_float(h.x << 16), __uint_as_float(h.x & 0xFFFF0000u),
+                                    __uint_as_float(h.y << 16), __uint_as_float(h.y & 0xFFFF0000u)};
+        const int q = 8 * wn + 2 * nt + (g >> 1);
+        *reinterpret_cast<uint2*>(smem + 512 * row + 16 * (q ^ (row & 15)) + 8 * (g & 1)) = h;
+      }
+    }
+    __syncthreads();
+    uint16_t* out = term ? a.lo : a.hi;
+#pragma unroll 4
+    for (int it = 0; it < kGtTile * 32 / kGtThreads; ++it) {
+      const int p = it * kGtThreads + threadIdx.x, row = p >> 5, q = (p & 31) ^ (row & 15);
+      if (m0 + row < a.T)
+        *reinterpret_cast<uint4*>(out + (m0 + row) * a.ldd + n0 + 8 * q) = *reinterpret_cast<const uint4*>(smem + 16 * p);
+    }
+  }
+  if (a.lo) {  // the registers now hold D - hi - lo
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      const int row = 128 * wm + 16 * mt + li, at = rows.at[row] - first;
+      if (__any(at >= 0 && at < 64)) {
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * nt + e == at) a.rest[m0 + row] = t.acc[mt][nt][e];
+      }
+    }
+  }
+}
+
+// C_y += sum of rest_t XP_t over the tokens with target y, in token order. A
+// wave per token; the one with a target's first token adds for all of them.
+__global__ __launch_bounds__(256) void ce_rest_kernel(const int64_t* targets, const float* rest, const uint16_t* XP,
+                                                      float* C, int64_t T, int64_t V, int r) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  const int64_t y = targets[t];
+  if (y < 0 || y >= V) return;
+  for (int64_t j0 = 0; j0 < t; j0 += 64)
+    if (__any(j0 + lane < t && targets[j0 + lane] == y)) return;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t j0 = t; j0 < T; j0 += 64) {
+    uint64_t same = __ballot(j0 + lane < T && targets[j0 + lane] == y);
+    while (same) {
+      const int64_t j = j0 + __builtin_ctzll(same);
+      same &= same - 1;
+      const float w = rest[j];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (lane + 64 * q < r) sum[q] += w * bf16_bits_to_f32(XP[j * r + lane + 64 * q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (lane + 64 * q < r) C[y * r + lane + 64 * q] += sum[q];
 }
 
 struct DxArgs {
@@ -267,14 +370,15 @@ struct Plan {
   int64_t pieces;
   int64_t splits;  // of dX's sums within a piece
   bool stacked;    // hi and lo in one accumulation of 2 T tokens
-  size_t d, xp, slab, acc;  // bytes of the workspace's parts
+  size_t d, xp, rest, slab, acc;  // bytes of the workspace's parts
+  size_t total() const { return d + xp + rest + slab + acc; }
 };
 
 Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
   Plan p{};
   const int64_t terms = r > 0 ? 2 : 1;
-  // a piece's D stays within half of the 256 MB last-level cache
-  int64_t piece = (int64_t(128) << 20) / (T * 2 * terms) / kGtTile * kGtTile;
+  // a piece's D fills the 256 MB last-level cache at most
+  int64_t piece = (int64_t(256) << 20) / (T * 2 * terms) / kGtTile * kGtTile;
   if (piece < 1024) piece = 1024;
   if (piece > kMaxTiledDim) piece = kMaxTiledDim;
   p.pieces = (V + piece - 1) / piece;
@@ -293,6 +397,7 @@ Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
   p.stacked = 2 * T <= kMaxTiledDim;
   p.d = up256((size_t)(terms * T * p.piece) * 2);
   p.xp = r > 0 && p.stacked ? up256((size_t)(2 * T * r) * 2) : 0;
+  p.rest = r > 0 ? up256((size_t)T * 4) : 0;
   p.slab = p.pieces > 1 || p.splits > 1 ? up256((size_t)(p.splits * T * k) * 4) : 0;
   if (r > 0) {
     // every width the pieces have: the whole ones and the last
@@ -372,8 +477,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int6
 
 extern "C" size_t rgc_linear_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r) {
   if (!shape_ok(T, V, k, r)) return 0;
-  const Plan p = plan_of(T, V, k, r);
-  return p.d + p.xp + p.slab + p.acc;
+  return plan_of(T, V, k, r).total();
 }
 
 extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
@@ -392,13 +496,13 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
       (r > 0 && (!aligned16(XP) || !aligned16(C))))
     return RGC_ERR_ALIGN;
   const Plan p = plan_of(T, V, k, r);
-  if (!ws || ws_bytes < p.d + p.xp + p.slab + p.acc) return RGC_ERR_WORKSPACE;
+  if (!ws || ws_bytes < p.total()) return RGC_ERR_WORKSPACE;
   if (!aligned_to(ws, 256)) return RGC_ERR_ALIGN;
   char* at = static_cast<char*>(ws);
   uint16_t* D = reinterpret_cast<uint16_t*>(at);
   uint16_t* twice = reinterpret_cast<uint16_t*>(at + p.d);
-  float* slab = p.slab ? reinterpret_cast<float*>(at + p.d + p.xp) : nullptr;
-  char* acc = at + p.d + p.xp + p.slab;
+  float* slab = p.slab ? reinterpret_cast<float*>(at + p.d + p.xp + p.rest) : nullptr;
+  char* acc = at + p.d + p.xp + p.rest + p.slab;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (r > 0 && p.stacked) {
     const int64_t n = T * r / 4;
@@ -409,6 +513,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
   CeArgs a{};
   a.X = X, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = T, a.vocab = V, a.k = k;
   a.lse = lse, a.grad = grad, a.mtiles = tiles_of(T);
+  a.rest = reinterpret_cast<float*>(at + p.d + p.xp);
   DxArgs x{};
   x.ldw = ldw, x.T = T, x.k = k, x.mtiles = tiles_of(T), x.ntiles = tiles_of(k), x.slab = slab, x.lddx = lddx;
   for (int64_t q = 0; q < p.pieces; ++q) {
@@ -433,6 +538,10 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
       }
       if (st != RGC_OK) return st;
     }
+  }
+  if (r > 0) {
+    hipLaunchKernelGGL(ce_rest_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, targets, a.rest, XP, C, T, V, (int)r);
+    if ((st = launched()) != RGC_OK) return st;
   }
   if (p.splits > 1) {
     const int64_t n = (T * k / 8 + 255) / 256;
