@@ -48,7 +48,7 @@ struct GtTile {
   f32x4_t acc[8][4];
   // 64-row and 32-column halves of the fragments, each for the two 32-K halves of a step
   GtFrag a0[4][2], a1[4][2], b0[2][2], b1[2][2];
-  uint32_t voff[8];  // this lane's byte offsets of the wave's copies: four of A, four of B
+  uint32_t voff[8];  // this lane's byte offsets of the wave's copies: four of A, four of B (K-major: one)
   uint32_t fa[2], fb[2];
   const uint16_t* A;
   const uint16_t* B;
@@ -77,7 +77,7 @@ struct GtTile {
         int64_t row = 8 * c + (lane >> 3);
         row = row < last ? row : last;
         voff[v] = (uint32_t)((row * (v < 4 ? lda : ldb) + 8 * chunk()) * 2);
-      } else {
+      } else if (v == 4) {
         int64_t col = column(c);
         col = col + 8 <= n_rem ? col : n_rem - 8;
         voff[v] = (uint32_t)((krow(c) * ldb + col) * 2);
@@ -115,15 +115,19 @@ struct GtTile {
   // the last chunk (or K row) instead, which settle() clears or A's zeros cancel.
   __device__ __forceinline__ void copy(int v, const uint16_t* Ab, const uint16_t* Bb, uint32_t st, int left) const {
     const int c = wave + 8 * (v & 3);
-    int over;
     if (v < 4 || !BKM) {
-      over = chunk() - (left - 1) / 8;
-      over = 16 * (over > 0 ? over : 0);
+      const int over = chunk() - (left - 1) / 8;
+      dma_16b_cached(v < 4 ? Ab : Bb, voff[v] - (uint32_t)(16 * (over > 0 ? over : 0)),
+                     st + (v < 4 ? 0 : kGtSlab) + 1024 * c);
     } else {
-      over = krow(c) - (left - 1);
-      over = (over > 0 ? over : 0) * (int)(2 * ldb);
+      // a K-major slab's copies are sixteen K rows apart, so one offset (of a
+      // row from 0 to 15) serves the four; base and lane are clamped to the
+      // last row each, and the offset never falls below the base
+      const int last = left - 1, row0 = 16 * (v - 4) < last ? 16 * (v - 4) : last;
+      const int over = krow(wave) - (last - row0);
+      dma_16b_cached(Bb + row0 * ldb, voff[4] - (uint32_t)(over > 0 ? over : 0) * (uint32_t)(2 * ldb),
+                     st + kGtSlab + 1024 * c);
     }
-    dma_16b_cached(v < 4 ? Ab : Bb, voff[v] - (uint32_t)over, st + (v < 4 ? 0 : kGtSlab) + 1024 * c);
   }
   __device__ __forceinline__ int left_of(int64_t step) const {
     const int64_t left = K - step * kGtStep;

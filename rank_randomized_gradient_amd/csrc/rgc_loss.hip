@@ -354,11 +354,16 @@ __global__ __launch_bounds__(256) void ce_join_kernel(const float* slab, int spl
                  f32x2_to_bf16x2_rne(v[2], v[3]));
 }
 
-// XP twice over, for the two terms of D (16-byte vectors; 8-byte ones end a
-// rank-4 XP of an odd token count).
-__global__ __launch_bounds__(256) void ce_twice_kernel(const uint2* XP, int64_t n, uint2* out) {
+// XP for the accumulation, `copies` times over (for the two terms of D), with
+// zeros for the ignored tokens: D's zeros would not cancel an Inf or NaN there.
+// Four values to a thread.
+__global__ __launch_bounds__(256) void ce_xp_kernel(const uint2* XP, const int64_t* targets, int64_t V, int64_t T, int quads,
+                                                    int copies, uint2* out) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) out[i] = out[n + i] = XP[i];
+  if (i >= T * quads) return;
+  const int64_t y = targets[i / quads];
+  const uint2 v = y >= 0 && y < V ? XP[i] : make_uint2(0u, 0u);
+  for (int c = 0; c < copies; ++c) out[c * T * quads + i] = v;
 }
 
 int64_t tiles_of(int64_t n) { return (n + kGtTile - 1) / kGtTile; }
@@ -396,7 +401,7 @@ Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
   p.splits = best < steps ? best : steps;
   p.stacked = 2 * T <= kMaxTiledDim;
   p.d = up256((size_t)(terms * T * p.piece) * 2);
-  p.xp = r > 0 && p.stacked ? up256((size_t)(2 * T * r) * 2) : 0;
+  p.xp = r > 0 ? up256((size_t)((p.stacked ? 2 : 1) * T * r) * 2) : 0;
   p.rest = r > 0 ? up256((size_t)T * 4) : 0;
   p.slab = p.pieces > 1 || p.splits > 1 ? up256((size_t)(p.splits * T * k) * 4) : 0;
   if (r > 0) {
@@ -500,14 +505,14 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
   if (!aligned_to(ws, 256)) return RGC_ERR_ALIGN;
   char* at = static_cast<char*>(ws);
   uint16_t* D = reinterpret_cast<uint16_t*>(at);
-  uint16_t* twice = reinterpret_cast<uint16_t*>(at + p.d);
+  uint16_t* xp = reinterpret_cast<uint16_t*>(at + p.d);
   float* slab = p.slab ? reinterpret_cast<float*>(at + p.d + p.xp + p.rest) : nullptr;
   char* acc = at + p.d + p.xp + p.rest + p.slab;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (r > 0 && p.stacked) {
+  if (r > 0) {
     const int64_t n = T * r / 4;
-    hipLaunchKernelGGL(ce_twice_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
-                       reinterpret_cast<const uint2*>(XP), n, reinterpret_cast<uint2*>(twice));
+    hipLaunchKernelGGL(ce_xp_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, reinterpret_cast<const uint2*>(XP),
+                       targets, V, T, (int)(r / 4), p.stacked ? 2 : 1, reinterpret_cast<uint2*>(xp));
     if ((st = launched()) != RGC_OK) return st;
   }
   CeArgs a{};
@@ -531,10 +536,10 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
     if (r > 0) {
       float* c = C + v0 * r;
       if (p.stacked) {
-        st = rgc_accumulate(D, a.ldd, twice, c, 2 * T, rows, r, acc, p.acc, stream);
+        st = rgc_accumulate(D, a.ldd, xp, c, 2 * T, rows, r, acc, p.acc, stream);
       } else {
-        st = rgc_accumulate(a.hi, a.ldd, XP, c, T, rows, r, acc, p.acc, stream);
-        if (st == RGC_OK) st = rgc_accumulate(a.lo, a.ldd, XP, c, T, rows, r, acc, p.acc, stream);
+        st = rgc_accumulate(a.hi, a.ldd, xp, c, T, rows, r, acc, p.acc, stream);
+        if (st == RGC_OK) st = rgc_accumulate(a.lo, a.ldd, xp, c, T, rows, r, acc, p.acc, stream);
       }
       if (st != RGC_OK) return st;
     }
