@@ -33,7 +33,7 @@ namespace {
 constexpr int64_t kNormMaxWidth = 65536;
 constexpr int64_t kNormMaxRows = int64_t(1) << 31;
 constexpr int64_t kNormHeldBackward = 16384;  // widest backward row held in registers
-constexpr int kBwdThreads = 1024;
+constexpr int kBwdThreads = 1024;           // of the wide rows' dx launch
 constexpr int kPanel = 256;  // columns of a workgroup of the column-sum launch
 
 struct NormArgs {
@@ -53,14 +53,17 @@ struct NormArgs {
   int db;           // backward: db wanted
 };
 
-// One vector of VEC elements as loaded, and its values.
+// One vector of VEC elements as loaded, and its values. again() hides from the
+// compiler that the values are those of before, so that it unpacks them anew
+// instead of keeping them in registers in between.
 template <typename XT, int VEC>
 struct Raw;
 template <>
 struct Raw<uint16_t, 8> {
-  uint4 v;
-  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  u32x4v_t v;
+  __device__ __forceinline__ void zero() { v = u32x4v_t{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void again() { asm volatile("" : "+v"(v)); }
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4v_t*>(p); }
   __device__ __forceinline__ float get(int i) const {
     const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
     return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
@@ -73,6 +76,7 @@ struct Raw<uint16_t, 8> {
 template <>
 struct Raw<float, 8> {
   float4 a, b;
+  __device__ __forceinline__ void again() {}
   __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
   __device__ __forceinline__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
@@ -90,6 +94,7 @@ struct Raw<float, 8> {
 template <>
 struct Raw<uint16_t, 1> {
   uint16_t v;
+  __device__ __forceinline__ void again() {}
   __device__ __forceinline__ void zero() { v = 0; }
   __device__ __forceinline__ void load(const uint16_t* p) { v = *p; }
   __device__ __forceinline__ float get(int) const { return bf16_bits_to_f32(v); }
@@ -98,6 +103,7 @@ struct Raw<uint16_t, 1> {
 template <>
 struct Raw<float, 1> {
   float v;
+  __device__ __forceinline__ void again() {}
   __device__ __forceinline__ void zero() { v = 0.f; }
   __device__ __forceinline__ void load(const float* p) { v = *p; }
   __device__ __forceinline__ float get(int) const { return v; }
@@ -126,31 +132,45 @@ __device__ __forceinline__ void load_params(const void* p, int f32, int64_t i, f
   }
 }
 
-// Sums of two values over the TPR threads of a row group, in all of them.
-// Within a wave by a xor butterfly; across the waves of a wider group through
-// LDS, `slots` being two floats per wave of the workgroup, used by one call
-// between two barriers (the caller alternates two sets).
-template <int TPR>
-__device__ __forceinline__ void group_sum2(float& a, float& b, float* slots) {
-#pragma unroll
-  for (int off = (TPR < 64 ? TPR : 64) / 2; off >= 1; off >>= 1) {
-    a += __shfl_xor(a, off, 64);
-    b += __shfl_xor(b, off, 64);
+// v plus its value R lanes further round a row of sixteen. Every step of a
+// halving sequence pairs the same two partial sums in both lanes.
+template <int R>
+__device__ __forceinline__ float add_rotated(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + R, 0xF, 0xF, false));
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+  static_assert(LANES == 16 || LANES == 64, "row or wave");
+  v = add_rotated<1>(add_rotated<2>(add_rotated<4>(add_rotated<8>(v))));
+  if constexpr (LANES == 64) {
+    v += __shfl_xor(v, 16, 64);
+    v += __shfl_xor(v, 32, 64);
   }
+  return v;
+}
+
+// Sums of N values over the TPR threads of a row group, in all of them: within
+// a wave across lanes, across the waves of a wider group through LDS, `slots`
+// being N floats per wave of the workgroup, used by one call between two
+// barriers (the caller alternates two sets).
+template <int TPR, int N>
+__device__ __forceinline__ void group_sum(float (&a)[N], float* slots) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = lanes_sum<(TPR < 64 ? 16 : 64)>(a[i]);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
-      slots[2 * wave] = a;
-      slots[2 * wave + 1] = b;
+#pragma unroll
+      for (int i = 0; i < N; ++i) slots[N * wave + i] = a[i];
     }
     __syncthreads();
     const int w0 = wave / W * W;
-    a = b = 0.f;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      a += slots[2 * (w0 + i)];
-      b += slots[2 * (w0 + i) + 1];
+    for (int i = 0; i < N; ++i) {
+      a[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) a[i] += slots[N * (w0 + w) + i];
     }
   }
 }
@@ -159,7 +179,7 @@ __device__ __forceinline__ void group_sum2(float& a, float& b, float* slots) {
 template <typename XT, int VEC, int NV, int TPR, int THREADS>
 __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
   constexpr int GROUPS = THREADS / TPR;
-  __shared__ float slots[3][2 * THREADS / 64];
+  __shared__ float slots[2][THREADS / 64];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const float inv_n = 1.0f / (float)a.n;
   for (int64_t row0 = (int64_t)blockIdx.x * GROUPS; row0 < a.rows; row0 += (int64_t)gridDim.x * GROUPS) {
@@ -173,29 +193,28 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
       raw[j].zero();
       if (c < a.n) raw[j].load(x + c);
     }
-    float s = 0.f, unused = 0.f;
     float mu = 0.f;
     if (a.centre) {
+      float s[1] = {0.f};
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += raw[j].get(e);
-      group_sum2<TPR>(s, unused, slots[0]);
-      mu = s * inv_n;
+        for (int e = 0; e < VEC; ++e) s[0] += raw[j].get(e);
+      group_sum<TPR>(s, slots[0]);
+      mu = s[0] * inv_n;
     }
-    float q = 0.f;
+    float q[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const bool in = (int64_t)(j * TPR + t) * VEC < a.n;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float d = raw[j].get(e) - mu;
-        q += in ? d * d : 0.f;
+        q[0] += in ? d * d : 0.f;
       }
     }
-    unused = 0.f;
-    group_sum2<TPR>(q, unused, slots[1]);
-    const float rstd = 1.0f / sqrtf(q * inv_n + a.eps);
+    group_sum<TPR>(q, slots[1]);
+    const float rstd = 1.0f / sqrtf(q[0] * inv_n + a.eps);
     if (live && t == 0) {
       if (a.mean) a.mean[row] = mu;
       if (a.rstd) a.rstd[row] = rstd;
@@ -224,32 +243,36 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
   }
 }
 
-// Backward with the row in registers; see the head of the file.
-template <typename XT, int VEC, int NV, int TPR>
-__global__ __launch_bounds__(kBwdThreads) void norm_backward_kernel(NormArgs a) {
-  constexpr int GROUPS = kBwdThreads / TPR, E = VEC * NV;
-  __shared__ float slots[2][2 * kBwdThreads / 64];
-  __shared__ float add[GROUPS > 1 ? kBwdThreads * E : 1];
+// Backward with the row in registers; see the head of the file. The weight is
+// kept in LDS. With c = x - mu: dw += (g rstd) c, and dx = rstd h - rstd c1 -
+// c (rstd^2 c2), c1 = mean(h) and c2 = mean(h c).
+template <typename XT, int VEC, int NV, int TPR, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
+  constexpr int GROUPS = THREADS / TPR, E = VEC * NV, COLS = TPR * E;
+  __shared__ float slots[2][2 * THREADS / 64];
+  __shared__ __attribute__((aligned(16))) float mem[GROUPS * COLS];  // the weight; at the end the groups' sums
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const float inv_n = 1.0f / (float)a.n;
-  float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+  for (int c = threadIdx.x; c < COLS; c += THREADS)
+    mem[c] = c >= a.n ? 0.f : a.w ? load_param(a.w, a.w_f32, c) : 1.f;
+  float dw[NV][VEC], db[NV][VEC];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int64_t c = (int64_t)(j * TPR + t) * VEC;
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) w[j][e] = 1.f, dw[j][e] = 0.f, db[j][e] = 0.f;
-    if (a.w && c < a.n) load_params<VEC>(a.w, a.w_f32, c, w[j]);
-  }
+    for (int e = 0; e < VEC; ++e) dw[j][e] = 0.f, db[j][e] = 0.f;
+  __syncthreads();
   const int64_t stride = (int64_t)gridDim.x * GROUPS;
-  Raw<XT, VEC> rx[NV], rg[NV];
-  float mu = 0.f, rstd = 0.f;
-  auto load = [&](int64_t row) {
+  int parity = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * GROUPS; row0 < a.rows; row0 += stride, parity ^= 1) {
+    const int64_t row = row0 + grp;
     const bool live = row < a.rows;
+    if (TPR <= 64 && !live) break;  // (wider groups meet at the barriers)
+    Raw<XT, VEC> rx[NV], rg[NV];
     const XT* x = static_cast<const XT*>(a.x) + (live ? row : 0) * a.ldx;
     const XT* g = static_cast<const XT*>(a.dy) + (live ? row : 0) * a.lddy;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = (int64_t)(j * TPR + t) * VEC;
+      const int c = (j * TPR + t) * VEC;
       rx[j].zero();
       rg[j].zero();
       if (live && c < a.n) {
@@ -257,69 +280,55 @@ __global__ __launch_bounds__(kBwdThreads) void norm_backward_kernel(NormArgs a) 
         rg[j].load(g + c);
       }
     }
-    mu = live && a.centre ? a.mean[row] : 0.f;
-    rstd = live ? a.rstd[row] : 0.f;
-  };
-  int parity = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * GROUPS; row0 < a.rows; row0 += stride, parity ^= 1) {
-    const int64_t row = row0 + grp;
-    load(row);
-    const bool live = row < a.rows;
-    float s1 = 0.f, s2 = 0.f;
+    const float mu = live && a.centre ? a.mean[row] : 0.f, rstd = live ? a.rstd[row] : 0.f;
+    float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool in = live && (int64_t)(j * TPR + t) * VEC < a.n;
+      const float* w = mem + (j * TPR + t) * VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float g = rg[j].get(e);
-        const float xhat = in ? (rx[j].get(e) - mu) * rstd : 0.f;
-        const float h = g * w[j][e];
-        s1 += h;
-        s2 += h * xhat;
-        dw[j][e] += g * xhat;
-        db[j][e] += g;
+        // columns behind the row's end have g = 0
+        const float gv = rg[j].get(e), c = rx[j].get(e) - mu, h = gv * w[e];
+        sum[0] += h;
+        sum[1] = __builtin_fmaf(h, c, sum[1]);
+        dw[j][e] = __builtin_fmaf(gv * rstd, c, dw[j][e]);
+        db[j][e] += gv;
       }
+      // the sums here and not behind the stores, where the compiler would take them with all they need
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) asm volatile("" : "+v"(dw[j][e]), "+v"(db[j][e]));
     }
-    group_sum2<TPR>(s1, s2, slots[parity]);
-    const float c1 = a.centre ? s1 * inv_n : 0.f, c2 = s2 * inv_n;
+    group_sum<TPR>(sum, slots[parity]);
+    const float k1 = a.centre ? sum[0] * inv_n * rstd : 0.f, k2 = sum[1] * inv_n * rstd * rstd * rstd;
     XT* dx = static_cast<XT*>(a.out) + row * a.ldo;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = (int64_t)(j * TPR + t) * VEC;
+      const int c = (j * TPR + t) * VEC;
       if (c >= a.n || !live) continue;
+      rx[j].again();
+      rg[j].again();
+      const float* w = mem + c;
       float f[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float xhat = (rx[j].get(e) - mu) * rstd;
-        f[e] = (rg[j].get(e) * w[j][e] - c1 - xhat * c2) * rstd;
-      }
+      for (int e = 0; e < VEC; ++e)
+        f[e] = __builtin_fmaf(rg[j].get(e) * w[e], rstd, -__builtin_fmaf(rx[j].get(e) - mu, k2, k1));
       Raw<XT, VEC>::store(dx + c, f);
     }
   }
   // the workgroup's partial rows: dw, then db
   for (int which = 0; which < 1 + a.db; ++which) {
     float* part = a.part + ((int64_t)which * gridDim.x + blockIdx.x) * a.n;
-    if constexpr (GROUPS > 1) {
-      if (which) __syncthreads();
+    __syncthreads();
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) add[grp * TPR * E + (j * TPR + t) * VEC + e] = which ? db[j][e] : dw[j][e];
-      __syncthreads();
-      for (int64_t c = threadIdx.x; c < a.n; c += kBwdThreads) {
-        float s = 0.f;
+      for (int e = 0; e < VEC; ++e) mem[grp * COLS + (j * TPR + t) * VEC + e] = which ? db[j][e] : dw[j][e];
+    __syncthreads();
+    for (int64_t c = threadIdx.x; c < a.n; c += THREADS) {
+      float s = 0.f;
 #pragma unroll 4
-        for (int q = 0; q < GROUPS; ++q) s += add[q * TPR * E + c];
-        part[c] = s;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int64_t c = (int64_t)(j * TPR + t) * VEC;
-        if (c >= a.n) continue;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) part[c + e] = which ? db[j][e] : dw[j][e];
-      }
+      for (int q = 0; q < GROUPS; ++q) s += mem[q * COLS + c];
+      part[c] = s;
     }
   }
 }
@@ -334,17 +343,17 @@ __global__ __launch_bounds__(kBwdThreads) void norm_wide_dx_kernel(NormArgs a) {
     const XT* g = static_cast<const XT*>(a.dy) + row * a.lddy;
     XT* dx = static_cast<XT*>(a.out) + row * a.ldo;
     const float mu = a.centre ? a.mean[row] : 0.f, rstd = a.rstd[row];
-    float s1 = 0.f, s2 = 0.f;
+    float sum[2] = {0.f, 0.f};
     for (int64_t c = threadIdx.x; c < a.n; c += kBwdThreads) {
       Raw<XT, 1> rx, rg;
       rx.load(x + c);
       rg.load(g + c);
       const float h = rg.get(0) * (a.w ? load_param(a.w, a.w_f32, c) : 1.f);
-      s1 += h;
-      s2 += h * ((rx.get(0) - mu) * rstd);
+      sum[0] += h;
+      sum[1] += h * ((rx.get(0) - mu) * rstd);
     }
-    group_sum2<kBwdThreads>(s1, s2, slots);
-    const float c1 = a.centre ? s1 * inv_n : 0.f, c2 = s2 * inv_n;
+    group_sum<kBwdThreads>(sum, slots);
+    const float c1 = a.centre ? sum[0] * inv_n : 0.f, c2 = sum[1] * inv_n;
     for (int64_t c = threadIdx.x; c < a.n; c += kBwdThreads) {
       Raw<XT, 1> rx, rg;
       rx.load(x + c);
@@ -458,25 +467,27 @@ void forward_pick(const NormArgs& a, bool vec, hipStream_t s) {
   }
 }
 
-// Threads of a row in the backward (1024 / this: rows a workgroup holds).
-int backward_threads_per_row(int64_t n, bool vec) {
-  if (vec) return n <= 128 ? 16 : n <= 1024 ? 64 : n <= 4096 ? 256 : n <= 8192 ? 512 : 1024;
-  return n <= 256 ? 64 : n <= 4096 ? 256 : 1024;
+// Rows a workgroup of the backward holds at a time (as backward_pick).
+int backward_rows(int64_t n, bool vec, rgc_dtype_t xt) {
+  const bool f32 = xt == RGC_F32;
+  if (vec && n <= 1024) return n <= 128 ? 64 : 16;
+  if (vec) return (n <= 2048 ? 16 : n <= 4096 ? 8 : n <= 8192 ? 4 : 2) / (f32 ? 2 : 1);
+  return n <= 1024 ? 16 : n <= 4096 ? 4 : 1;
 }
 
 // Workgroups of the backward, and so partial rows: one per compute unit, or
 // fewer where the rows do not fill them.
-int64_t backward_groups(int64_t rows, int64_t n, bool vec) {
+int64_t backward_groups(int64_t rows, int64_t n, bool vec, rgc_dtype_t xt) {
   const int64_t cus = device_compute_units();
   if (n > kNormHeldBackward) return rows < 64 ? rows : 64;
-  const int64_t per = kBwdThreads / backward_threads_per_row(n, vec);
+  const int64_t per = backward_rows(n, vec, xt);
   const int64_t need = (rows + per - 1) / per;
   return need < cus ? need : cus;
 }
 
-template <typename XT, int VEC, int NV, int TPR>
+template <typename XT, int VEC, int NV, int TPR, int THREADS>
 void backward_launch(const NormArgs& a, int64_t G, hipStream_t s) {
-  hipLaunchKernelGGL((norm_backward_kernel<XT, VEC, NV, TPR>), dim3((unsigned)G), dim3(kBwdThreads), 0, s, a);
+  hipLaunchKernelGGL((norm_backward_kernel<XT, VEC, NV, TPR, THREADS>), dim3((unsigned)G), dim3(THREADS), 0, s, a);
 }
 
 template <typename XT>
@@ -488,19 +499,25 @@ void backward_pick(const NormArgs& a, bool vec, int64_t G, hipStream_t s) {
     hipLaunchKernelGGL(norm_wide_columns_kernel<XT>, dim3((unsigned)((a.n + kPanel - 1) / kPanel), (unsigned)G),
                        dim3(kPanel), 0, s, a);
   } else if (vec) {
-    if (a.n <= 128) backward_launch<XT, 8, 1, 16>(a, G, s);
-    else if (a.n <= 512) backward_launch<XT, 8, 1, 64>(a, G, s);
-    else if (a.n <= 1024) backward_launch<XT, 8, 2, 64>(a, G, s);
-    else if (a.n <= 2048) backward_launch<XT, 8, 1, 256>(a, G, s);
-    else if (a.n <= 4096) backward_launch<XT, 8, 2, 256>(a, G, s);
-    else if (a.n <= 8192) backward_launch<XT, 8, 2, 512>(a, G, s);
-    else backward_launch<XT, 8, 2, 1024>(a, G, s);
+    if (a.n <= 128) return backward_launch<XT, 8, 1, 16, 1024>(a, G, s);
+    if (a.n <= 512) return backward_launch<XT, 8, 1, 64, 1024>(a, G, s);
+    if (a.n <= 1024) return backward_launch<XT, 8, 2, 64, 1024>(a, G, s);
+    if (a.n <= 2048) return backward_launch<XT, 8, 4, 64, sizeof(XT) == 2 ? 1024 : 512>(a, G, s);
+    if constexpr (sizeof(XT) == 2) {  // a row of 4096 in one wave, 64 elements to a lane
+      if (a.n <= 4096) return backward_launch<XT, 8, 8, 64, 512>(a, G, s);
+      if (a.n <= 8192) return backward_launch<XT, 8, 8, 128, 512>(a, G, s);
+      backward_launch<XT, 8, 8, 256, 512>(a, G, s);
+    } else {
+      if (a.n <= 4096) return backward_launch<XT, 8, 4, 128, 512>(a, G, s);
+      if (a.n <= 8192) return backward_launch<XT, 8, 4, 256, 512>(a, G, s);
+      backward_launch<XT, 8, 4, 512, 512>(a, G, s);
+    }
   } else {
-    if (a.n <= 64) backward_launch<XT, 1, 1, 64>(a, G, s);
-    else if (a.n <= 256) backward_launch<XT, 1, 4, 64>(a, G, s);
-    else if (a.n <= 1024) backward_launch<XT, 1, 4, 256>(a, G, s);
-    else if (a.n <= 4096) backward_launch<XT, 1, 16, 256>(a, G, s);
-    else backward_launch<XT, 1, 16, 1024>(a, G, s);
+    if (a.n <= 64) return backward_launch<XT, 1, 1, 64, 1024>(a, G, s);
+    if (a.n <= 256) return backward_launch<XT, 1, 4, 64, 1024>(a, G, s);
+    if (a.n <= 1024) return backward_launch<XT, 1, 16, 64, 1024>(a, G, s);
+    if (a.n <= 4096) return backward_launch<XT, 1, 16, 256, 1024>(a, G, s);
+    backward_launch<XT, 1, 32, 512, 512>(a, G, s);
   }
 }
 
@@ -532,12 +549,15 @@ extern "C" rgc_status_t rgc_layer_norm_forward(rgc_norm_kind_t kind, rgc_dtype_t
   return launched();
 }
 
-// The partial rows of either path (the element path never has more workgroups
-// than the vector path has rows to give, but may have more than it).
+// The partial rows of whichever path the call will take.
 extern "C" size_t rgc_layer_norm_backward_workspace_size(int64_t rows, int64_t n) {
   if (rows <= 0 || n <= 0 || rows > kNormMaxRows || n > kNormMaxWidth) return 0;
-  const int64_t a = backward_groups(rows, n, true), b = backward_groups(rows, n, false);
-  return (size_t)(a > b ? a : b) * 2 * (size_t)n * 4;
+  int64_t most = 0;
+  for (int path = 0; path < 4; ++path) {
+    const int64_t G = backward_groups(rows, n, path & 1, path & 2 ? RGC_F32 : RGC_BF16);
+    most = G > most ? G : most;
+  }
+  return (size_t)most * 2 * (size_t)n * 4;
 }
 
 extern "C" rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* dY,
@@ -569,7 +589,7 @@ extern "C" rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_
   a.ldx = ldx, a.lddy = lddy, a.ldo = lddx, a.rows = rows, a.n = n;
   a.w_f32 = wt == RGC_F32, a.centre = kind == RGC_NORM_LAYER, a.db = dbias != nullptr;
   const bool vec = vectors(X, ldx, n, xt) && vectors(dY, lddy, n, xt) && vectors(dX, lddx, n, xt) && aligned16(weight);
-  const int64_t G = backward_groups(rows, n, vec);
+  const int64_t G = backward_groups(rows, n, vec, xt);
   if (xt == RGC_F32) backward_pick<float>(a, vec, G, s);
   else backward_pick<uint16_t>(a, vec, G, s);
   if ((st = launched()) != RGC_OK) return st;
