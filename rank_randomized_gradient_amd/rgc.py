@@ -27,6 +27,7 @@ Names mirror the C ABI in include/rgc.h:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -665,9 +666,12 @@ def rgc_apply_from_seed(mode: str, kind: str, proj_seed: int, W: torch.Tensor, C
 
 # ---- the head's loss, norms and AdamW ----------------------------------------
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(dev: torch.device):
     """Makes dev the current device for a call (its tensors may live on another than the current one)."""
-    return torch.cuda.device(dev)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _scratch(workspace: Workspace | None, nbytes: int, dev: torch.device):
