@@ -27,6 +27,7 @@ Names mirror the C ABI in include/rgc.h:
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -182,7 +183,7 @@ def _check(status: int) -> None:
 
 
 def _stream(dev: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev.index))
 
 
 def _need_gpu(*tensors: torch.Tensor) -> torch.device:
@@ -844,13 +845,12 @@ def rgc_layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Ten
 
 def _adamw_list(ts, name: str, dev, dtypes, sizes):
     """The pointers of a list of dense tensors of one of `dtypes`, of the given element counts."""
-    dtype = ts[0].dtype
-    if dtype not in dtypes:
-        raise RgcError(f"{name} must be " + " or ".join(str(d) for d in dtypes))
-    for t, n in zip(ts, sizes):
-        if t.dtype != dtype or t.device != dev or t.numel() != n or not t.is_contiguous():
-            raise RgcError(f"{name} must be contiguous tensors of one type, on one device, of the parameters' sizes")
-    return _ptrs(ts)
+    T = torch.Tensor  # whole lists through the unbound methods: a step over many small tensors is bound by this
+    if (ts[0].dtype not in dtypes or {t.dtype for t in ts} != {ts[0].dtype} or set(map(T.get_device, ts)) != {dev.index}
+            or list(map(T.numel, ts)) != sizes or not all(map(T.is_contiguous, ts))):
+        raise RgcError(f"{name} must be contiguous tensors of one type ({' or '.join(map(str, dtypes))}), on one device, "
+                       "of the parameters' sizes")
+    return (_vp * len(ts)).from_buffer(array.array("Q", map(T.data_ptr, ts)))
 
 
 def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: float = 0.9, beta2: float = 0.999,
@@ -871,7 +871,7 @@ def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: 
     if n == 0:
         return Ps
     dev = _need_gpu(Ps[0], *([grad_scale] if grad_scale is not None else []))
-    sizes = [p.numel() for p in Ps]
+    sizes = list(map(torch.Tensor.numel, Ps))
     state = (torch.float8_e4m3fn,) if eight else (torch.float32,)
     pp = _adamw_list(Ps, "Ps", dev, _DTYPES, sizes)
     gp = _adamw_list(Gs, "Gs", dev, _DTYPES, sizes)
@@ -884,7 +884,7 @@ def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: 
         vsp = _adamw_list(V_scales, "V_scales", dev, (torch.float32,), blocks)
     if n > 1:
         for ptrs in (pp, mp, vp):
-            given = [p for p, s in zip(ptrs, sizes) if s]
+            given = [p for p in ptrs if p]
             if len(set(given)) != len(given):
                 raise RgcError("a tensor is listed twice")
     if grad_scale is not None:
