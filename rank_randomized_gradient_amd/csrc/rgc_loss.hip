@@ -36,8 +36,16 @@ namespace {
 
 constexpr int64_t kCeMaxVocab = int64_t(1) << 24;
 constexpr int kCeDown = 8;        // tile rows walked together
-constexpr int kCeMaxSplit = 16;
+constexpr int kCeMaxSplit = 128;
+constexpr double kCeSmallRate = 0.6;  // a small tile's rate beside a large one's
 constexpr float kLog2e = 1.4426950408889634f;
+
+// The logits' tiles of a launch: `large` 256 x 256 ones, which cover the first
+// `split` rows of the piece, then small ones for the rest.
+struct CeGrid {
+  int64_t large, split;
+  int64_t ntiles;  // columns of tiles, large and small
+};
 
 struct CeArgs {
   const uint16_t* X;
@@ -47,8 +55,8 @@ struct CeArgs {
   int64_t T, V, k;     // V: rows of the piece
   int64_t v0;          // vocabulary index of the piece's first row
   int64_t vocab;       // rows of the whole vocabulary
-  int64_t mtiles, ntiles;
-  float2* part;        // forward: (maximum, sum) of each tile row, [tile][token]
+  CeGrid grid;
+  float2* part;        // forward: (maximum, sum) of each tile row, [tile column][token]
   float* zt;           // forward: the target's logit
   const float* lse;    // backward
   const float* grad;
@@ -58,18 +66,25 @@ struct CeArgs {
   int64_t ldd;
 };
 
+typedef GtTile<8, 4, 2, false> LargeTile;   // 256 x 256
+typedef GtTile<4, 2, 4, false> SmallTile;   // 128 x 128
+typedef GtTile<2, 2, 5, false> FlatTile;    // 64 x 128, for few tokens
+constexpr int kCeLds = LargeTile::kLds;
+static_assert(SmallTile::kLds <= kCeLds && FlatTile::kLds <= kCeLds, "one LDS array serves the tiles");
+
 // What an epilogue needs of a tile's rows, fetched before the product.
 struct CeRows {
   float lse[kGtTile], grad[kGtTile];
   int at[kGtTile];  // the target's column in the tile; -1: elsewhere; -2: an ignored token
 };
 
+template <typename Tile>
 __device__ __forceinline__ void load_rows(const CeArgs& a, int64_t m0, int64_t n0, bool backward, CeRows* r) {
   const int row = threadIdx.x;
-  if (row >= kGtTile) return;
+  if (row >= Tile::kRows) return;
   const bool live = m0 + row < a.T;
   const int64_t y = live ? a.targets[m0 + row] : -1, c = y - a.v0 - n0;
-  r->at[row] = y < 0 || y >= a.vocab ? -2 : c >= 0 && c < kGtTile ? (int)c : -1;
+  r->at[row] = y < 0 || y >= a.vocab ? -2 : c >= 0 && c < Tile::kCols ? (int)c : -1;
   if (backward) {
     r->lse[row] = live ? a.lse[m0 + row] : 0.f;
     r->grad[row] = live ? a.grad[m0 + row] : 0.f;
@@ -79,42 +94,40 @@ __device__ __forceinline__ void load_rows(const CeArgs& a, int64_t m0, int64_t n
 // exp(x); below 2^-126 it is zero.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
-__global__ __launch_bounds__(kGtThreads, 1) void ce_forward_kernel(CeArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[kGtLds];
-  __shared__ CeRows rows;
-  int64_t i, j;
-  gt_place(gt_logical(blockIdx.x, gridDim.x), a.mtiles, a.ntiles, kCeDown, &i, &j);
-  const int64_t m0 = i * kGtTile, n0 = j * kGtTile;
-  load_rows(a, m0, n0, false, &rows);
-  GtTile<false> t;
+// The tile of rows m0 .. and columns n0 .. of z, reduced to slot `column` of its rows.
+template <int MI, int NI, int STAGES>
+__device__ __forceinline__ void forward_tile(const CeArgs& a, int64_t m0, int64_t n0, int64_t column, char* smem, CeRows* rows) {
+  typedef GtTile<MI, NI, STAGES, false> Tile;
+  load_rows<Tile>(a, m0, n0, false, rows);
+  Tile t;
   t.init(a.X + m0 * a.ldx, a.ldx, a.W + n0 * a.ldw, a.ldw, a.T - m0, a.V - n0, a.k, smem);
   t.run();
 
   const int g = t.lane >> 4, li = t.lane & 15, wm = t.wave & 1, wn = t.wave >> 1;
   float* sums = reinterpret_cast<float*>(smem);  // [row][wn]: maximum, sum
-  const int first = 64 * wn + 4 * g;
-  const int width = (int)(a.V - n0 < kGtTile ? a.V - n0 : kGtTile);
+  const int first = 16 * NI * wn + 4 * g;
+  const int width = (int)(a.V - n0 < Tile::kCols ? a.V - n0 : Tile::kCols);
 #pragma unroll
-  for (int mt = 0; mt < 8; ++mt) {
-    const int row = 128 * wm + 16 * mt + li;
-    const int at = rows.at[row] - first;
-    if (__builtin_expect(width < kGtTile, 0)) {
+  for (int mt = 0; mt < MI; ++mt) {
+    const int row = 16 * MI * wm + 16 * mt + li;
+    const int at = rows->at[row] - first;
+    if (__builtin_expect(width < Tile::kCols, 0)) {
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+      for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (first + 16 * nt + e >= width) t.acc[mt][nt][e] = -INFINITY;
     }
-    if (__any(at >= 0 && at < 64)) {
+    if (__any(at >= 0 && at < 16 * NI)) {
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+      for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (16 * nt + e == at) a.zt[m0 + row] = t.acc[mt][nt][e];
     }
     float top = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = fmaxf(top, t.acc[mt][nt][e]);
     top = fmaxf(top, __shfl_xor(top, 16, 64));
@@ -122,7 +135,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void ce_forward_kernel(CeArgs a) {
     const float base = top == -INFINITY ? 0.f : top;
     float s = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s += fast_exp(t.acc[mt][nt][e] - base);
     s += __shfl_xor(s, 16, 64);
@@ -134,14 +147,14 @@ __global__ __launch_bounds__(kGtThreads, 1) void ce_forward_kernel(CeArgs a) {
   }
   __syncthreads();
   const int row = threadIdx.x;
-  if (row < kGtTile && m0 + row < a.T) {
+  if (row < Tile::kRows && m0 + row < a.T) {
     float top = sums[8 * row], s = 0.f;
 #pragma unroll
     for (int w = 1; w < 4; ++w) top = fmaxf(top, sums[8 * row + 2 * w]);
     const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int w = 0; w < 4; ++w) s += sums[8 * row + 2 * w + 1] * fast_exp(sums[8 * row + 2 * w] - base);
-    a.part[j * a.T + m0 + row] = make_float2(top, s);
+    a.part[column * a.T + m0 + row] = make_float2(top, s);
   }
 }
 
@@ -154,7 +167,7 @@ __global__ __launch_bounds__(1024) void ce_finish_kernel(CeArgs a, float* loss, 
   float top = -INFINITY, s = 0.f;
   if (t < a.T) {
 #pragma unroll 4
-    for (int64_t j = wave; j < a.ntiles; j += 16) {
+    for (int64_t j = wave; j < a.grid.ntiles; j += 16) {
       const float2 p = a.part[j * a.T + t];
       const float m = fmaxf(top, p.x), base = m == -INFINITY ? 0.f : m;
       s = s * fast_exp(top - base) + p.y * fast_exp(p.x - base);
@@ -178,44 +191,42 @@ __global__ __launch_bounds__(1024) void ce_finish_kernel(CeArgs a, float* loss, 
 
 // A piece's D, hi (and lo): T x ldd, zero in the columns behind the piece.
 // The tile's bf16 values are laid out in LDS first, so that they are stored in
-// whole 512-byte rows (16-byte chunk q of row t at place q ^ (t % 16)). The
+// whole rows (16-byte chunk q of row t at place q ^ (t % 16)). The
 // lo pass forms D - hi from the fp32 values, which stay in the registers.
-__global__ __launch_bounds__(kGtThreads, 1) void ce_d_kernel(CeArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[kGtLds];
-  __shared__ CeRows rows;
-  int64_t i, j;
-  gt_place(gt_logical(blockIdx.x, gridDim.x), a.mtiles, a.ntiles, kCeDown, &i, &j);
-  const int64_t m0 = i * kGtTile, n0 = j * kGtTile;
-  load_rows(a, m0, n0, true, &rows);
-  GtTile<false> t;
+template <int MI, int NI, int STAGES>
+__device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, char* smem, CeRows* rows) {
+  typedef GtTile<MI, NI, STAGES, false> Tile;
+  constexpr int kRowChunks = Tile::kCols / 8;  // 16-byte chunks of a row
+  load_rows<Tile>(a, m0, n0, true, rows);
+  Tile t;
   t.init(a.X + m0 * a.ldx, a.ldx, a.W + n0 * a.ldw, a.ldw, a.T - m0, a.V - n0, a.k, smem);
   t.run();
 
   const int g = t.lane >> 4, li = t.lane & 15, wm = t.wave & 1, wn = t.wave >> 1;
-  const int first = 64 * wn + 4 * g;
-  const int width = (int)(a.V - n0 < kGtTile ? a.V - n0 : kGtTile);
+  const int first = 16 * NI * wn + 4 * g;
+  const int width = (int)(a.V - n0 < Tile::kCols ? a.V - n0 : Tile::kCols);
 #pragma unroll
-  for (int mt = 0; mt < 8; ++mt) {
-    const int row = 128 * wm + 16 * mt + li;
-    const int target = rows.at[row], at = target - first;
-    const float lse = rows.lse[row], gr = rows.grad[row];
+  for (int mt = 0; mt < MI; ++mt) {
+    const int row = 16 * MI * wm + 16 * mt + li;
+    const int target = rows->at[row], at = target - first;
+    const float lse = rows->lse[row], gr = rows->grad[row];
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float p = fast_exp(t.acc[mt][nt][e] - lse) * gr;
         t.acc[mt][nt][e] = target == -2 ? 0.f : p;
       }
-    if (__any(at >= 0 && at < 64)) {
+    if (__any(at >= 0 && at < 16 * NI)) {
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+      for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (16 * nt + e == at) t.acc[mt][nt][e] -= gr;
     }
-    if (__builtin_expect(width < kGtTile, 0)) {
+    if (__builtin_expect(width < Tile::kCols, 0)) {
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+      for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (first + 16 * nt + e >= width) t.acc[mt][nt][e] = 0.f;
@@ -224,40 +235,67 @@ __global__ __launch_bounds__(kGtThreads, 1) void ce_d_kernel(CeArgs a) {
   for (int term = 0; term < (a.lo ? 2 : 1); ++term) {
     if (term) __syncthreads();
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
-      const int row = 128 * wm + 16 * mt + li;
+    for (int mt = 0; mt < MI; ++mt) {
+      const int row = 16 * MI * wm + 16 * mt + li;
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int nt = 0; nt < NI; ++nt) {
         const f32x4_t d = t.acc[mt][nt];
         uint2 h = make_uint2(f32x2_to_bf16x2_rne(d[0], d[1]), f32x2_to_bf16x2_rne(d[2], d[3]));
         // D - hi, exact: hi is D's leading bits
         t.acc[mt][nt] = d - f32x4_t{__uint_as_float(h.x << 16), __uint_as_float(h.x & 0xFFFF0000u),
                                     __uint_as_float(h.y << 16), __uint_as_float(h.y & 0xFFFF0000u)};
-        const int q = 8 * wn + 2 * nt + (g >> 1);
-        *reinterpret_cast<uint2*>(smem + 512 * row + 16 * (q ^ (row & 15)) + 8 * (g & 1)) = h;
+        const int q = 2 * NI * wn + 2 * nt + (g >> 1);
+        *reinterpret_cast<uint2*>(smem + 16 * (kRowChunks * row + (q ^ (row & 15))) + 8 * (g & 1)) = h;
       }
     }
     __syncthreads();
     uint16_t* out = term ? a.lo : a.hi;
 #pragma unroll 4
-    for (int it = 0; it < kGtTile * 32 / kGtThreads; ++it) {
-      const int p = it * kGtThreads + threadIdx.x, row = p >> 5, q = (p & 31) ^ (row & 15);
+    for (int it = 0; it < Tile::kRows * kRowChunks / kGtThreads; ++it) {
+      const int p = it * kGtThreads + threadIdx.x, row = p / kRowChunks, q = (p % kRowChunks) ^ (row & 15);
       if (m0 + row < a.T)
         *reinterpret_cast<uint4*>(out + (m0 + row) * a.ldd + n0 + 8 * q) = *reinterpret_cast<const uint4*>(smem + 16 * p);
     }
   }
   if (a.lo) {  // the registers now hold D - hi - lo
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
-      const int row = 128 * wm + 16 * mt + li, at = rows.at[row] - first;
-      if (__any(at >= 0 && at < 64)) {
+    for (int mt = 0; mt < MI; ++mt) {
+      const int row = 16 * MI * wm + 16 * mt + li, at = rows->at[row] - first;
+      if (__any(at >= 0 && at < 16 * NI)) {
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (16 * nt + e == at) a.rest[m0 + row] = t.acc[mt][nt][e];
       }
     }
+  }
+}
+
+// The logits' kernel of both directions: the tile of this workgroup.
+template <bool BACKWARD, bool FEW>
+__global__ __launch_bounds__(kGtThreads, 1) void ce_logits_kernel(CeArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[kCeLds];
+  __shared__ CeRows rows;
+  int64_t i, j;
+  if (!FEW && (int64_t)blockIdx.x < a.grid.large) {
+    const int64_t columns = a.grid.split / kGtTile + (a.grid.split % kGtTile != 0);
+    gt_place(gt_logical(blockIdx.x, a.grid.large), (a.T + kGtTile - 1) / kGtTile, columns, kCeDown, &i, &j);
+    if constexpr (BACKWARD) d_tile<8, 4, 2>(a, i * kGtTile, j * kGtTile, smem, &rows);
+    else forward_tile<8, 4, 2>(a, i * kGtTile, j * kGtTile, j, smem, &rows);
+    return;
+  }
+  typedef std::conditional_t<FEW, FlatTile, SmallTile> Tile;
+  const int64_t before = a.grid.split / kGtTile;  // columns of large tiles (whole ones where small tiles follow)
+  gt_place(gt_logical(blockIdx.x - a.grid.large, gridDim.x - a.grid.large), (a.T + Tile::kRows - 1) / Tile::kRows,
+           a.grid.ntiles - before, 2 * kCeDown, &i, &j);
+  const int64_t m0 = i * Tile::kRows, n0 = a.grid.split + j * Tile::kCols;
+  if constexpr (BACKWARD) {
+    if constexpr (FEW) d_tile<2, 2, 5>(a, m0, n0, smem, &rows);
+    else d_tile<4, 2, 4>(a, m0, n0, smem, &rows);
+  } else {
+    if constexpr (FEW) forward_tile<2, 2, 5>(a, m0, n0, before + j, smem, &rows);
+    else forward_tile<4, 2, 4>(a, m0, n0, before + j, smem, &rows);
   }
 }
 
@@ -303,7 +341,7 @@ struct DxArgs {
 };
 
 __global__ __launch_bounds__(kGtThreads, 1) void ce_dx_kernel(DxArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[kGtLds];
+  __shared__ __attribute__((aligned(1024))) char smem[GtTile<8, 4, 2, true>::kLds];
   const int64_t tiles = a.mtiles * a.ntiles;
   const int64_t place = gt_logical(blockIdx.x, gridDim.x);
   const int64_t split = place / tiles;
@@ -312,7 +350,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void ce_dx_kernel(DxArgs a) {
   const int64_t m0 = i * kGtTile, n0 = j * kGtTile;
   const int64_t k0 = split * a.steps * kGtStep;
   const int64_t K = a.K - k0 < a.steps * kGtStep ? a.K - k0 : a.steps * kGtStep;
-  GtTile<true> t;
+  GtTile<8, 4, 2, true> t;
   t.init(a.D + m0 * a.ldd + k0, a.ldd, a.W + k0 * a.ldw + n0, a.ldw, a.T - m0, a.k - n0, K, smem);
   if (K > 0) t.run();
 
@@ -369,6 +407,48 @@ __global__ __launch_bounds__(256) void ce_xp_kernel(const uint2* XP, const int64
 int64_t tiles_of(int64_t n) { return (n + kGtTile - 1) / kGtTile; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Divides T x V logits into tiles. Large tiles run at the highest rate, but a
+// last round of them that fills few compute units costs as much as a full one:
+// then the columns of whole rounds stay large and the rest is cut into small
+// tiles, which do a quarter of a large one's work at kCeSmallRate of its rate.
+// 1001 x 50001 x 2048 (784 large tiles are 3.06 rounds): 221 us with large tiles
+// alone, 191 us so; 100 x 12000 x 2048 (47 large tiles): 58 and 28 us.
+CeGrid grid_of(int64_t T, int64_t V, bool few) {
+  const int64_t cus = device_compute_units(), m = tiles_of(T), n = tiles_of(V);
+  CeGrid g{};
+  if (few) {
+    g.ntiles = (V + FlatTile::kCols - 1) / FlatTile::kCols;
+    return g;
+  }
+  const auto small_columns = [&](int64_t from) { return V > from ? (V - from + SmallTile::kCols - 1) / SmallTile::kCols : 0; };
+  const int64_t small_rows = (T + SmallTile::kRows - 1) / SmallTile::kRows;
+  const int64_t rounds = m * n / cus;
+  double best = (double)((m * n + cus - 1) / cus);
+  int64_t columns = n;  // of large tiles
+  for (int64_t keep = rounds; keep >= 0 && keep >= rounds - 1; --keep) {
+    const int64_t c = keep * cus / m < n ? keep * cus / m : n;
+    const int64_t small = small_rows * small_columns(c * kGtTile);
+    const double cost = (double)((m * c + cus - 1) / cus) + (double)((small + cus - 1) / cus) * 0.25 / kCeSmallRate;
+    if (cost < 0.97 * best) best = cost, columns = c;
+  }
+  g.large = m * columns;
+  g.split = columns == n ? V : columns * kGtTile;
+  g.ntiles = columns + (columns == n ? 0 : small_columns(g.split));
+  return g;
+}
+
+template <bool BACKWARD>
+rgc_status_t logits_launch(CeArgs& a, hipStream_t s) {
+  const bool few = a.T <= FlatTile::kRows;
+  a.grid = grid_of(a.T, a.V, few);
+  const int64_t before = few ? 0 : a.grid.split == a.V ? a.grid.ntiles : a.grid.split / kGtTile;
+  const int64_t rows = few ? 1 : (a.T + SmallTile::kRows - 1) / SmallTile::kRows;
+  const int64_t blocks = a.grid.large + rows * (a.grid.ntiles - before);
+  if (few) hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, true>), dim3((unsigned)blocks), dim3(kGtThreads), 0, s, a);
+  else hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, false>), dim3((unsigned)blocks), dim3(kGtThreads), 0, s, a);
+  return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP;
+}
+
 // How the backward goes through the vocabulary and divides dX's sums.
 struct Plan {
   int64_t piece;   // vocabulary rows of a piece
@@ -389,16 +469,19 @@ Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
   p.pieces = (V + piece - 1) / piece;
   p.piece = tiles_of((V + p.pieces - 1) / p.pieces) * kGtTile;
   p.pieces = (V + p.piece - 1) / p.piece;
-  // as many splits as keep the compute units busy with the fewest rounds of tiles a split
+  // as many splits as take the least time: rounds of tiles on the compute units
+  // (4.7 TFLOP/s each with all at work), and the slabs' way to memory and back
+  // at 4 TB/s. At least four steps to a split.
   const int64_t tiles = tiles_of(T) * tiles_of(k), cus = device_compute_units();
-  int64_t best = 1;
-  double cost = 1e30;
-  for (int64_t s = 1; s <= kCeMaxSplit; ++s) {
-    const double c = (double)((tiles * s + cus - 1) / cus) / (double)s + 0.004 * (double)s;
-    if (c < cost) cost = c, best = s;
-  }
   const int64_t steps = (p.piece + kGtStep - 1) / kGtStep;
-  p.splits = best < steps ? best : steps;
+  double best = 1e30;
+  p.splits = 1;
+  for (int64_t s = 1; s <= kCeMaxSplit && (s == 1 || 4 * s <= steps); ++s) {
+    const int64_t own = (steps + s - 1) / s;
+    const double cost = (double)((tiles * s + cus - 1) / cus) * (double)own * (2.0 * kGtTile * kGtTile * kGtStep / 4.7e12) +
+                        (s > 1 ? (double)(s * T * k) * 8 / 4e12 : 0.0);
+    if (cost < best) best = cost, p.splits = s;
+  }
   p.stacked = 2 * T <= kMaxTiledDim;
   p.d = up256((size_t)(terms * T * p.piece) * 2);
   p.xp = r > 0 ? up256((size_t)((p.stacked ? 2 : 1) * T * r) * 2) : 0;
@@ -434,7 +517,8 @@ rgc_status_t check_shape(int64_t T, int64_t V, int64_t k, int64_t r) {
 
 rgc_status_t launched() { return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP; }
 
-size_t part_bytes(int64_t T, int64_t V) { return up256((size_t)(tiles_of(V) * T) * 8); }
+// Slots of a token's partial sums: at most one for every 128 entries and one for a rest on either side.
+size_t part_bytes(int64_t T, int64_t V) { return up256((size_t)((V + 127) / 128 + 2) * (size_t)T * 8); }
 
 }  // namespace
 }  // namespace rgc
@@ -463,19 +547,17 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int6
   char* at = static_cast<char*>(ws);
   CeArgs a{};
   a.X = X, a.W = W, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = T, a.V = a.vocab = V, a.k = k;
-  a.mtiles = tiles_of(T), a.ntiles = tiles_of(V);
   a.part = reinterpret_cast<float2*>(at);
   at += part_bytes(T, V);
   a.zt = reinterpret_cast<float*>(at);
   at += up256((size_t)T * 4);
-  if (a.mtiles * a.ntiles >= int64_t(1) << 23) return RGC_ERR_UNSUPPORTED;  // threads of a launch
+  if (((T + 63) / 64) * ((V + 127) / 128) >= int64_t(1) << 23) return RGC_ERR_UNSUPPORTED;  // threads of a launch
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (r > 0) {  // the layer's X P, as rgc_project makes it
     st = rgc_project(X, ldx, P, XP, T, k, r, at, ws_bytes - (size_t)(at - static_cast<char*>(ws)), stream);
     if (st != RGC_OK) return st;
   }
-  hipLaunchKernelGGL(ce_forward_kernel, dim3((unsigned)(a.mtiles * a.ntiles)), dim3(kGtThreads), 0, s, a);
-  if ((st = launched()) != RGC_OK) return st;
+  if ((st = logits_launch<false>(a, s)) != RGC_OK) return st;
   hipLaunchKernelGGL(ce_finish_kernel, dim3((unsigned)((T + 63) / 64)), dim3(1024), 0, s, a, loss, lse);
   return launched();
 }
@@ -517,17 +599,16 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
   }
   CeArgs a{};
   a.X = X, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = T, a.vocab = V, a.k = k;
-  a.lse = lse, a.grad = grad, a.mtiles = tiles_of(T);
+  a.lse = lse, a.grad = grad;
   a.rest = reinterpret_cast<float*>(at + p.d + p.xp);
   DxArgs x{};
   x.ldw = ldw, x.T = T, x.k = k, x.mtiles = tiles_of(T), x.ntiles = tiles_of(k), x.slab = slab, x.lddx = lddx;
   for (int64_t q = 0; q < p.pieces; ++q) {
     const int64_t v0 = q * p.piece, rows = V - v0 < p.piece ? V - v0 : p.piece;
-    a.W = W + v0 * ldw, a.V = rows, a.v0 = v0, a.ntiles = tiles_of(rows);
-    a.ldd = a.ntiles * kGtTile;
+    a.W = W + v0 * ldw, a.V = rows, a.v0 = v0;
+    a.ldd = tiles_of(rows) * kGtTile;
     a.hi = D, a.lo = r > 0 ? D + T * a.ldd : nullptr;
-    hipLaunchKernelGGL(ce_d_kernel, dim3((unsigned)(a.mtiles * a.ntiles)), dim3(kGtThreads), 0, s, a);
-    if ((st = launched()) != RGC_OK) return st;
+    if ((st = logits_launch<true>(a, s)) != RGC_OK) return st;
     x.D = a.hi, x.W = a.W, x.ldd = a.ldd, x.K = rows, x.first = q == 0;
     x.steps = ((rows + kGtStep - 1) / kGtStep + p.splits - 1) / p.splits;
     x.dX = p.splits == 1 && q == p.pieces - 1 ? dX : nullptr;
