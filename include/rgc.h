@@ -401,7 +401,8 @@ rgc_status_t rgc_linear_backward(const uint16_t* D, int64_t ldd, const uint16_t*
  *   C += D^T XP with r > 0: V x r fp32, as rgc_accumulate adds, D as two bf16
  *   terms (hi + lo, 2^-17 relative), so that C's error is that of fp32 sums.
  *   C is what rgc_apply turns into the head's update. r = 0 (XP and C may then
- *   be NULL) is a frozen head: dX alone.
+ *   be NULL) is a frozen head: dX alone. With r > 0 dX may be NULL (an input
+ *   that needs no gradient): C alone.
  * Limits: T and k at most 65536, V at most 2^24 and, with r > 0, a multiple of
  * 8 in the backward (as every layer's d); k, ldx, ldw and lddx multiples of 8,
  * leading dimensions at most 2^23; X, W, P, XP, C and dX 16-byte aligned; r 0 or a

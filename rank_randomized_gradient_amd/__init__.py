@@ -39,3 +39,6 @@ from .rgc import (  # noqa: F401
     rgc_test_stochastic_round,
 )
 from .sketched_linear import SketchedLinear, SketchedLinearFunction  # noqa: F401,E402
+from .sketched_head import SketchedCrossEntropy, SketchedCrossEntropyFunction  # noqa: F401,E402
+from .layer_norm import LayerNorm, LayerNormFunction  # noqa: F401,E402
+from .adamw import AdamW  # noqa: F401,E402

@@ -577,7 +577,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
   if (r > 0 && V % 8 != 0) return RGC_ERR_UNSUPPORTED;  // the sketch has a layer's widths
   if ((st = check_rows(X, ldx, k)) != RGC_OK) return st;
   if ((st = check_rows(W, ldw, k)) != RGC_OK) return st;
-  if ((st = check_rows(dX, lddx, k)) != RGC_OK) return st;
+  if ((dX || r == 0) && (st = check_rows(dX, lddx, k)) != RGC_OK) return st;
   if (!targets || !lse || !grad || (r > 0 && (!XP || !C))) return RGC_ERR_NULL;
   if (!aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(grad, 4) ||
       (r > 0 && (!aligned16(XP) || !aligned16(C))))
@@ -609,11 +609,13 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
     a.ldd = tiles_of(rows) * kGtTile;
     a.hi = D, a.lo = r > 0 ? D + T * a.ldd : nullptr;
     if ((st = logits_launch<true>(a, s)) != RGC_OK) return st;
-    x.D = a.hi, x.W = a.W, x.ldd = a.ldd, x.K = rows, x.first = q == 0;
-    x.steps = ((rows + kGtStep - 1) / kGtStep + p.splits - 1) / p.splits;
-    x.dX = p.splits == 1 && q == p.pieces - 1 ? dX : nullptr;
-    hipLaunchKernelGGL(ce_dx_kernel, dim3((unsigned)(x.mtiles * x.ntiles * p.splits)), dim3(kGtThreads), 0, s, x);
-    if ((st = launched()) != RGC_OK) return st;
+    if (dX) {
+      x.D = a.hi, x.W = a.W, x.ldd = a.ldd, x.K = rows, x.first = q == 0;
+      x.steps = ((rows + kGtStep - 1) / kGtStep + p.splits - 1) / p.splits;
+      x.dX = p.splits == 1 && q == p.pieces - 1 ? dX : nullptr;
+      hipLaunchKernelGGL(ce_dx_kernel, dim3((unsigned)(x.mtiles * x.ntiles * p.splits)), dim3(kGtThreads), 0, s, x);
+      if ((st = launched()) != RGC_OK) return st;
+    }
     if (r > 0) {
       float* c = C + v0 * r;
       if (p.stacked) {
@@ -629,7 +631,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
     hipLaunchKernelGGL(ce_rest_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, targets, a.rest, XP, C, T, V, (int)r);
     if ((st = launched()) != RGC_OK) return st;
   }
-  if (p.splits > 1) {
+  if (dX && p.splits > 1) {
     const int64_t n = (T * k / 8 + 255) / 256;
     hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)n), dim3(256), 0, s, slab, (int)p.splits, T, k, dX, lddx);
     st = launched();

@@ -723,11 +723,12 @@ def rgc_linear_cross_entropy_forward(X: torch.Tensor, W: torch.Tensor, targets: 
 
 def rgc_linear_cross_entropy_backward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
                                       grad: torch.Tensor, XP: torch.Tensor | None = None, C: torch.Tensor | None = None,
-                                      dX: torch.Tensor | None = None, workspace: Workspace | None = None) -> torch.Tensor:
+                                      dX: torch.Tensor | None = None, input_grad: bool = True,
+                                      workspace: Workspace | None = None) -> torch.Tensor | None:
     """dX = bf16(D W) with D_tv = grad[t] (softmax(X W^T)_tv - [v = targets[t]]),
     and, with XP and C, C += D^T XP (V x r float32). lse is the forward's; grad:
     float32, the gradient of each token's loss. D exists a piece of the
-    vocabulary at a time."""
+    vocabulary at a time. input_grad False leaves dX out (C alone; returns None)."""
     lib = load_library()
     dev = _need_gpu(X, W, targets, lse, grad, *[t for t in (XP, C, dX) if t is not None])
     ldx, ldw, T, V, k = _head_args(X, W, targets)
@@ -744,16 +745,20 @@ def rgc_linear_cross_entropy_backward(X: torch.Tensor, W: torch.Tensor, targets:
         r = C.shape[-1]
         if r == 0 or tuple(C.shape) != (V, r) or tuple(XP.shape) != (T, r):
             raise RgcError("shapes must be XP: T x r, C: V x r")
-    if dX is None:
-        dX = torch.empty((T, k), dtype=torch.bfloat16, device=dev)
-    lddx = _rows(dX, torch.bfloat16, "dX")
-    if tuple(dX.shape) != (T, k):
-        raise RgcError("dX must be T x k")
+    if input_grad:
+        if dX is None:
+            dX = torch.empty((T, k), dtype=torch.bfloat16, device=dev)
+        if tuple(dX.shape) != (T, k):
+            raise RgcError("dX must be T x k")
+    elif dX is not None or C is None:
+        raise RgcError("without the input's gradient there must be a sketch, and no dX")
+    lddx = _rows(dX, torch.bfloat16, "dX") if input_grad else k
     with _on(dev):
         wp, wn, _keep = _scratch(workspace, lib.rgc_linear_cross_entropy_backward_workspace_size(T, V, k, r), dev)
         _check(lib.rgc_linear_cross_entropy_backward(X.data_ptr(), ldx, W.data_ptr(), ldw, targets.data_ptr(),
                                                      lse.data_ptr(), grad.data_ptr(), XP.data_ptr() if r else None,
-                                                     C.data_ptr() if r else None, dX.data_ptr(), lddx, T, V, k, r, wp, wn,
+                                                     C.data_ptr() if r else None, dX.data_ptr() if input_grad else None,
+                                                     lddx, T, V, k, r, wp, wn,
                                                      _stream(dev)))
     return dX
 
