@@ -20,10 +20,11 @@
 // The sketch is fp32, and a D rounded once to bf16 would put an error of 2^-9
 // into each of its terms. So with a sketch D is kept as two bf16 terms,
 // D = hi + lo (error 2^-18), stacked along the tokens: C += [hi; lo]^T [XP; XP]
-// is one accumulation over 2 T tokens. What two terms still leave of the
-// targets' entries, by far the largest of D (of the order of g, the others of
-// g / V), is kept in fp32, one value a token, and added in a last launch. dX is
-// rounded to bf16 itself and takes hi alone.
+// is one accumulation over 2 T tokens. dX is rounded to bf16 itself and takes
+// hi alone. The targets' entries are by far the largest of D (of the order of
+// g, the others of g / V), so what the terms leave of them is kept in fp32, one
+// value a token, and added where it costs little: rest_t W_y(t) to dX when it is
+// rounded, and rest_t XP_t to C's row y(t) in a last launch.
 //
 // Bound by MFMA: 2 T V k operations for the loss, 6 T V k + 4 T V r for the
 // gradient. Where dX has few tiles (few tokens), each is split over K among
@@ -62,7 +63,8 @@ struct CeArgs {
   const float* grad;
   uint16_t* hi;        // backward: T x ldd, bf16
   uint16_t* lo;        // or null: no sketch
-  float* rest;         // with lo: D - hi - lo at each token's target
+  float* rest;         // D - hi at each token's target
+  float* rest_sketch;  // with lo: D - hi - lo there
   int64_t ldd;
 };
 
@@ -232,32 +234,31 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
           if (first + 16 * nt + e >= width) t.acc[mt][nt][e] = 0.f;
     }
   }
-  for (int term = 0; term < (a.lo ? 2 : 1); ++term) {
+  RGC_LDS char* lds = (RGC_LDS char*)smem;
+  uint32_t to[NI];  // this lane's places in the row of mt = 0
+#pragma unroll
+  for (int nt = 0; nt < NI; ++nt)
+    to[nt] = (uint32_t)(16 * (kRowChunks * (16 * MI * wm + li) + ((2 * NI * wn + 2 * nt + (g >> 1)) ^ li)) + 8 * (g & 1));
+  const int row0 = threadIdx.x / kRowChunks, q = (threadIdx.x % kRowChunks) ^ (row0 & 15);
+  constexpr int kRowsAtOnce = kGtThreads / kRowChunks;  // a multiple of 16: q holds for every pass
+  static_assert(kRowsAtOnce % 16 == 0, "rows of a pass");
+  const int terms = a.lo ? 2 : 1;
+#pragma unroll 1
+  for (int term = 0; term < terms; ++term) {
     if (term) __syncthreads();
 #pragma unroll
-    for (int mt = 0; mt < MI; ++mt) {
-      const int row = 16 * MI * wm + 16 * mt + li;
+    for (int mt = 0; mt < MI; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NI; ++nt) {
         const f32x4_t d = t.acc[mt][nt];
-        uint2 h = make_uint2(f32x2_to_bf16x2_rne(d[0], d[1]), f32x2_to_bf16x2_rne(d[2], d[3]));
+        const u32x2v_t h = {f32x2_to_bf16x2_rne(d[0], d[1]), f32x2_to_bf16x2_rne(d[2], d[3])};
         // D - hi, exact: hi is D's leading bits
         t.acc[mt][nt] = d - f32x4_t{__uint_as_float(h.x << 16), __uint_as_float(h.x & 0xFFFF0000u),
                                     __uint_as_float(h.y << 16), __uint_as_float(h.y & 0xFFFF0000u)};
-        const int q = 2 * NI * wn + 2 * nt + (g >> 1);
-        *reinterpret_cast<uint2*>(smem + 16 * (kRowChunks * row + (q ^ (row & 15))) + 8 * (g & 1)) = h;
+        *(RGC_LDS u32x2v_t*)(lds + to[nt] + 256 * kRowChunks * mt) = h;
       }
-    }
-    __syncthreads();
-    uint16_t* out = term ? a.lo : a.hi;
-#pragma unroll 4
-    for (int it = 0; it < Tile::kRows * kRowChunks / kGtThreads; ++it) {
-      const int p = it * kGtThreads + threadIdx.x, row = p / kRowChunks, q = (p % kRowChunks) ^ (row & 15);
-      if (m0 + row < a.T)
-        *reinterpret_cast<uint4*>(out + (m0 + row) * a.ldd + n0 + 8 * q) = *reinterpret_cast<const uint4*>(smem + 16 * p);
-    }
-  }
-  if (a.lo) {  // the registers now hold D - hi - lo
+    // what is left of the targets' entries: after hi for dX, after lo for the sketch
+    float* rest = term ? a.rest_sketch : a.rest;
 #pragma unroll
     for (int mt = 0; mt < MI; ++mt) {
       const int row = 16 * MI * wm + 16 * mt + li, at = rows->at[row] - first;
@@ -266,9 +267,15 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
         for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (16 * nt + e == at) a.rest[m0 + row] = t.acc[mt][nt][e];
+            if (16 * nt + e == at) rest[m0 + row] = t.acc[mt][nt][e];
       }
     }
+    __syncthreads();
+    uint16_t* out = (term ? a.lo : a.hi) + (m0 + row0) * a.ldd + n0 + 8 * q;
+#pragma unroll 4
+    for (int it = 0; it < Tile::kRows / kRowsAtOnce; ++it, out += kRowsAtOnce * a.ldd)
+      if (m0 + row0 + it * kRowsAtOnce < a.T)
+        *reinterpret_cast<u32x4v_t*>(out) = *(const RGC_LDS u32x4v_t*)(lds + 16 * (threadIdx.x + it * kGtThreads));
   }
 }
 
@@ -308,19 +315,33 @@ __global__ __launch_bounds__(256) void ce_rest_kernel(const int64_t* targets, co
   if (t >= T) return;
   const int64_t y = targets[t];
   if (y < 0 || y >= V) return;
-  for (int64_t j0 = 0; j0 < t; j0 += 64)
-    if (__any(j0 + lane < t && targets[j0 + lane] == y)) return;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t j0 = t; j0 < T; j0 += 64) {
-    uint64_t same = __ballot(j0 + lane < T && targets[j0 + lane] == y);
-    while (same) {
-      const int64_t j = j0 + __builtin_ctzll(same);
-      same &= same - 1;
-      const float w = rest[j];
+  // 512 targets at a time, so that their loads are in flight together
+  for (int64_t j0 = 0; j0 < t; j0 += 512) {
+    bool same = false;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (lane + 64 * q < r) sum[q] += w * bf16_bits_to_f32(XP[j * r + lane + 64 * q]);
+    for (int c = 0; c < 8; ++c) {
+      const int64_t j = j0 + 64 * c + lane;
+      same |= j < t && targets[j] == y;
     }
+    if (__any(same)) return;
+  }
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t j0 = t; j0 < T; j0 += 512) {
+    uint64_t same[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int64_t j = j0 + 64 * c + lane;
+      same[c] = __ballot(j < T && targets[j] == y);
+    }
+    for (int c = 0; c < 8; ++c)
+      while (same[c]) {
+        const int64_t j = j0 + 64 * c + __builtin_ctzll(same[c]);
+        same[c] &= same[c] - 1;
+        const float w = rest[j];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (lane + 64 * q < r) sum[q] = __builtin_fmaf(w, bf16_bits_to_f32(XP[j * r + lane + 64 * q]), sum[q]);
+      }
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q)
@@ -338,7 +359,19 @@ struct DxArgs {
   int first;          // the first piece: the slab is written, not added to
   uint16_t* dX;       // the last piece of an unsplit product: rounded here; else null
   int64_t lddx;
+  const uint16_t* V0;  // W's first row
+  const int64_t* targets;
+  const float* rest;
+  int64_t vocab;
 };
+
+// rest_t and the row of W it multiplies; 0 and W's first row for an ignored token.
+__device__ __forceinline__ float rest_of(const DxArgs& a, int64_t t, const uint16_t** row) {
+  const int64_t y = a.targets[t];
+  const bool live = y >= 0 && y < a.vocab;
+  *row = a.V0 + (live ? y : 0) * a.ldw;
+  return live ? a.rest[t] : 0.f;
+}
 
 __global__ __launch_bounds__(kGtThreads, 1) void ce_dx_kernel(DxArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[GtTile<8, 4, 2, true>::kLds];
@@ -360,34 +393,53 @@ __global__ __launch_bounds__(kGtThreads, 1) void ce_dx_kernel(DxArgs a) {
   for (int mt = 0; mt < 8; ++mt) {
     const int64_t row = m0 + 128 * wm + 16 * mt + li;
     if (row >= a.T) continue;
+    const uint16_t* wy = nullptr;
+    const float rest = a.dX ? rest_of(a, row, &wy) : 0.f;
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
       const int64_t col = n0 + 64 * wn + 16 * nt + 4 * g;
       if (col >= a.k) continue;  // k is a multiple of 8: four columns are all in or all out
       f32x4_t v = t.acc[mt][nt];
       if (!a.first) v += *reinterpret_cast<const f32x4_t*>(slab + row * a.k + col);
-      if (a.dX)
+      if (a.dX) {
+        if (rest != 0.f) {
+          float w[4];
+          load_bf16_row<4>(wy + col, w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(rest, w[e], v[e]);
+        }
         *reinterpret_cast<uint2*>(a.dX + row * a.lddx + col) =
             make_uint2(f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3]));
-      else
+      } else {
         *reinterpret_cast<f32x4_t*>(slab + row * a.k + col) = v;
+      }
     }
   }
 }
 
-// dX = bf16(sum of the slabs), eight columns to a thread.
-__global__ __launch_bounds__(256) void ce_join_kernel(const float* slab, int splits, int64_t T, int64_t k, uint16_t* dX,
-                                                      int64_t lddx) {
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (at >= T * k) return;
-  f32x4_t u = *reinterpret_cast<const f32x4_t*>(slab + at), v = *reinterpret_cast<const f32x4_t*>(slab + at + 4);
+// dX = bf16(sum of the slabs + rest W_y), eight columns to a thread.
+__global__ __launch_bounds__(256) void ce_join_kernel(DxArgs a, int splits) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, all = a.T * a.k;
+  if (at >= all) return;
+  f32x4_t u = *reinterpret_cast<const f32x4_t*>(a.slab + at), v = *reinterpret_cast<const f32x4_t*>(a.slab + at + 4);
 #pragma unroll 4
   for (int s = 1; s < splits; ++s) {
-    u += *reinterpret_cast<const f32x4_t*>(slab + s * T * k + at);
-    v += *reinterpret_cast<const f32x4_t*>(slab + s * T * k + at + 4);
+    u += *reinterpret_cast<const f32x4_t*>(a.slab + s * all + at);
+    v += *reinterpret_cast<const f32x4_t*>(a.slab + s * all + at + 4);
   }
-  const int64_t row = at / k, col = at - row * k;
-  *reinterpret_cast<uint4*>(dX + row * lddx + col) =
+  const int64_t row = at / a.k, col = at - row * a.k;
+  const uint16_t* wy;
+  const float rest = rest_of(a, row, &wy);
+  if (rest != 0.f) {
+    float w[8];
+    load_bf16_row<8>(wy + col, w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      u[e] = __builtin_fmaf(rest, w[e], u[e]);
+      v[e] = __builtin_fmaf(rest, w[e + 4], v[e]);
+    }
+  }
+  *reinterpret_cast<uint4*>(a.dX + row * a.lddx + col) =
       make_uint4(f32x2_to_bf16x2_rne(u[0], u[1]), f32x2_to_bf16x2_rne(u[2], u[3]), f32x2_to_bf16x2_rne(v[0], v[1]),
                  f32x2_to_bf16x2_rne(v[2], v[3]));
 }
@@ -485,7 +537,7 @@ Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
   p.stacked = 2 * T <= kMaxTiledDim;
   p.d = up256((size_t)(terms * T * p.piece) * 2);
   p.xp = r > 0 ? up256((size_t)((p.stacked ? 2 : 1) * T * r) * 2) : 0;
-  p.rest = r > 0 ? up256((size_t)T * 4) : 0;
+  p.rest = up256((size_t)T * 4) * (r > 0 ? 2 : 1);
   p.slab = p.pieces > 1 || p.splits > 1 ? up256((size_t)(p.splits * T * k) * 4) : 0;
   if (r > 0) {
     // every width the pieces have: the whole ones and the last
@@ -601,8 +653,10 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
   a.X = X, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = T, a.vocab = V, a.k = k;
   a.lse = lse, a.grad = grad;
   a.rest = reinterpret_cast<float*>(at + p.d + p.xp);
+  a.rest_sketch = a.rest + up256((size_t)T * 4) / 4;
   DxArgs x{};
   x.ldw = ldw, x.T = T, x.k = k, x.mtiles = tiles_of(T), x.ntiles = tiles_of(k), x.slab = slab, x.lddx = lddx;
+  x.V0 = W, x.targets = targets, x.rest = a.rest, x.vocab = V;
   for (int64_t q = 0; q < p.pieces; ++q) {
     const int64_t v0 = q * p.piece, rows = V - v0 < p.piece ? V - v0 : p.piece;
     a.W = W + v0 * ldw, a.V = rows, a.v0 = v0;
@@ -628,12 +682,14 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
     }
   }
   if (r > 0) {
-    hipLaunchKernelGGL(ce_rest_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, targets, a.rest, XP, C, T, V, (int)r);
+    hipLaunchKernelGGL(ce_rest_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, targets, a.rest_sketch, XP, C, T, V,
+                       (int)r);
     if ((st = launched()) != RGC_OK) return st;
   }
   if (dX && p.splits > 1) {
     const int64_t n = (T * k / 8 + 255) / 256;
-    hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)n), dim3(256), 0, s, slab, (int)p.splits, T, k, dX, lddx);
+    x.dX = dX;
+    hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)n), dim3(256), 0, s, x, (int)p.splits);
     st = launched();
   }
   return st;

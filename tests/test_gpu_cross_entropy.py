@@ -6,9 +6,9 @@ it is off by at most 2^-20 of A = sum |x w| (as for the layer products). lse
 inherits the largest logit error of its row (it is a weighted mean of them),
 plus a few fp32 roundings of values of the size of lse; loss is lse minus one
 logit. D = g (p - [v = y]) then is off by p |g| times the two logit errors in
-its exponent, and rounded to bf16 for dX (half a step, 2^-8 of D); dX adds
-its own rounding (2^-8) and the fp32 sum (2^-20 of sum |D W|). For C, D's two
-bf16 terms leave 2^-16 of D.
+its exponent, and rounded to bf16 for dX (half a step, 2^-8 of D) except at the
+targets, whose rest is added in fp32; dX adds its own rounding (2^-8) and the
+fp32 sum (2^-20 of sum |D W|). For C, D's two bf16 terms leave 2^-16 of D.
 """
 import pytest
 import torch
@@ -52,10 +52,12 @@ def _reference(x, w, y, gr, xp, c):
     gl = torch.where(live, gr, torch.zeros(()).double())
     d = d * gl[:, None]
     off = (2 * dz + 2.0 ** -20)[:, None] * p * gl.abs()[:, None]  # of D, before any rounding to bf16
+    rounded = d.abs()  # entries that dX takes rounded to bf16: all but the targets'
+    rounded[torch.arange(len(y)), at] = 0
     out = {"lse": lse, "loss": loss, "dX": d @ w}
     few = 2.0 ** -21 * (lse.abs() + z.abs().amax(1) + 1)
     bound = {"lse": dz + few, "loss": 2 * dz + 2 * few,
-             "dX": (off + (2.0 ** -8 + 2.0 ** -20) * d.abs()) @ w.abs() + 2.0 ** -8 * (d @ w).abs()}
+             "dX": (off + 2.0 ** -8 * rounded + 2.0 ** -20 * d.abs()) @ w.abs() + 2.0 ** -8 * (d @ w).abs()}
     if c is not None:
         xa = xp.double()
         xa = torch.where(live[:, None], xa, torch.zeros(()).double())
