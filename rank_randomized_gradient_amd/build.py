@@ -1,15 +1,18 @@
-"""Builds librgc.so (the HIP kernels + C ABI) in-tree for gfx950 with hipcc."""
+"""Builds librgc.so (the HIP kernels + C ABI) in-tree for gfx950 with hipcc, and the
+small CPython module beside it that unpacks lists of tensors."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "librgc.so")
+LISTS_PATH = os.path.join(PKG_DIR, "_rgc_lists.so")
 SOURCES = ["rgc_sketch.hip", "rgc_apply.hip", "rgc_projection.hip", "rgc_linear.hip", "rgc_loss.hip", "rgc_norm.hip", "rgc_adamw.hip",
            "rgc_abi.cpp"]
 
@@ -29,11 +32,25 @@ def hipcc() -> str:
     return cand
 
 
+def lists_command(out: str) -> list:
+    """g++'s command for the CPython module that unpacks lists of tensors (host code only)."""
+    from torch.utils import cpp_extension
+
+    inc = [f"-I{p}" for p in [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]]
+    lib = [f"-L{p}" for p in cpp_extension.library_paths()]
+    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", *inc,
+            os.path.join(CSRC, "rgc_lists.cpp"), "-o", out, *lib, "-lc10", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = hipcc()
     procs = []
     objs = []
+    lists = lists_command(LISTS_PATH + ".tmp")
+    if verbose:
+        print(" ".join(lists), flush=True)
+    procs.append(("rgc_lists.cpp", subprocess.Popen(lists, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
@@ -51,7 +68,8 @@ def build(verbose: bool = False) -> str:
         elif verbose and lines:
             print("\n".join(lines))
     if failed:
-        raise RuntimeError(f"hipcc failed on {failed}")
+        raise RuntimeError(f"the build failed on {failed}")
+    os.replace(LISTS_PATH + ".tmp", LISTS_PATH)
     tmp = LIB_PATH + ".tmp"
     cmd = [cc, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:

@@ -459,16 +459,19 @@ __global__ __launch_bounds__(256) void ce_xp_kernel(const uint2* XP, const int64
 int64_t tiles_of(int64_t n) { return (n + kGtTile - 1) / kGtTile; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Whether the logits take 64-row tiles.
+bool few_tokens(int64_t T) { return T <= FlatTile::kRows; }
+
 // Divides T x V logits into tiles. Large tiles run at the highest rate, but a
 // last round of them that fills few compute units costs as much as a full one:
 // then the columns of whole rounds stay large and the rest is cut into small
 // tiles, which do a quarter of a large one's work at kCeSmallRate of its rate.
 // 1001 x 50001 x 2048 (784 large tiles are 3.06 rounds): 221 us with large tiles
 // alone, 191 us so; 100 x 12000 x 2048 (47 large tiles): 58 and 28 us.
-CeGrid grid_of(int64_t T, int64_t V, bool few) {
+CeGrid grid_of(int64_t T, int64_t V) {
   const int64_t cus = device_compute_units(), m = tiles_of(T), n = tiles_of(V);
   CeGrid g{};
-  if (few) {
+  if (few_tokens(T)) {
     g.ntiles = (V + FlatTile::kCols - 1) / FlatTile::kCols;
     return g;
   }
@@ -491,8 +494,8 @@ CeGrid grid_of(int64_t T, int64_t V, bool few) {
 
 template <bool BACKWARD>
 rgc_status_t logits_launch(CeArgs& a, hipStream_t s) {
-  const bool few = a.T <= FlatTile::kRows;
-  a.grid = grid_of(a.T, a.V, few);
+  const bool few = few_tokens(a.T);
+  a.grid = grid_of(a.T, a.V);
   const int64_t before = few ? 0 : a.grid.split == a.V ? a.grid.ntiles : a.grid.split / kGtTile;
   const int64_t rows = few ? 1 : (a.T + SmallTile::kRows - 1) / SmallTile::kRows;
   const int64_t blocks = a.grid.large + rows * (a.grid.ntiles - before);
@@ -569,8 +572,8 @@ rgc_status_t check_shape(int64_t T, int64_t V, int64_t k, int64_t r) {
 
 rgc_status_t launched() { return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP; }
 
-// Slots of a token's partial sums: at most one for every 128 entries and one for a rest on either side.
-size_t part_bytes(int64_t T, int64_t V) { return up256((size_t)((V + 127) / 128 + 2) * (size_t)T * 8); }
+// A token's partial sums, one for each column of tiles.
+size_t part_bytes(int64_t T, int64_t V) { return up256((size_t)grid_of(T, V).ntiles * (size_t)T * 8); }
 
 }  // namespace
 }  // namespace rgc

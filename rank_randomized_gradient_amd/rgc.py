@@ -27,7 +27,6 @@ Names mirror the C ABI in include/rgc.h:
 """
 from __future__ import annotations
 
-import array
 import contextlib
 import ctypes
 import os
@@ -47,6 +46,7 @@ _MODES = {"normalized": RGC_UPDATE_NORMALIZED, "scaled": RGC_UPDATE_SCALED}
 RGC_BF16 = 0
 RGC_F32 = 1
 _DTYPES = {torch.bfloat16: RGC_BF16, torch.float32: RGC_F32}
+_TYPE_NAMES = {"BFloat16": RGC_BF16, "Float": RGC_F32}
 RGC_NORM_LAYER = 0
 RGC_NORM_RMS = 1
 _NORMS = {"layer": RGC_NORM_LAYER, "rms": RGC_NORM_RMS}
@@ -848,14 +848,23 @@ def rgc_layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Ten
     return dX, dweight, dbias
 
 
-def _adamw_list(ts, name: str, dev, dtypes, sizes):
-    """The pointers of a list of dense tensors of one of `dtypes`, of the given element counts."""
-    T = torch.Tensor  # whole lists through the unbound methods: a step over many small tensors is bound by this
-    if (ts[0].dtype not in dtypes or {t.dtype for t in ts} != {ts[0].dtype} or set(map(T.get_device, ts)) != {dev.index}
-            or list(map(T.numel, ts)) != sizes or not all(map(T.is_contiguous, ts))):
-        raise RgcError(f"{name} must be contiguous tensors of one type ({' or '.join(map(str, dtypes))}), on one device, "
-                       "of the parameters' sizes")
-    return (_vp * len(ts)).from_buffer(array.array("Q", map(T.data_ptr, ts)))
+def _lists():
+    """The compiled module that checks and unpacks lists of tensors."""
+    try:
+        from . import _rgc_lists
+    except ImportError as e:
+        raise RgcError("_rgc_lists.so is not built; run `python -c 'import __graft_entry__ as g; g.build()'`") from e
+    return _rgc_lists
+
+
+def _adamw_list(ts, name: str, types, sizes, block: int = 1):
+    """(pointers, sizes, type, device index) of a list of dense tensors of one of `types`, on one
+    device, with ceil(size / block) elements each."""
+    got = _lists().pack(ts, sizes, block)
+    if got is None or got[2] not in types:
+        raise RgcError(f"{name} must be contiguous tensors of one type ({' or '.join(types)}), on one device, of the "
+                       "parameters' sizes")
+    return got
 
 
 def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: float = 0.9, beta2: float = 0.999,
@@ -876,29 +885,27 @@ def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: 
     if n == 0:
         return Ps
     dev = _need_gpu(Ps[0], *([grad_scale] if grad_scale is not None else []))
-    sizes = list(map(torch.Tensor.numel, Ps))
-    state = (torch.float8_e4m3fn,) if eight else (torch.float32,)
-    pp = _adamw_list(Ps, "Ps", dev, _DTYPES, sizes)
-    gp = _adamw_list(Gs, "Gs", dev, _DTYPES, sizes)
-    mp = _adamw_list(Ms, "Ms", dev, state, sizes)
-    vp = _adamw_list(Vs, "Vs", dev, state, sizes)
-    msp = vsp = None
+    state = ("Float8_e4m3fn",) if eight else ("Float",)
+    given = [_adamw_list(Ps, "Ps", tuple(_TYPE_NAMES), None)]
+    sizes = given[0][1]
+    given.append(_adamw_list(Gs, "Gs", tuple(_TYPE_NAMES), sizes))
+    given += [_adamw_list(ts, name, state, sizes) for ts, name in ((Ms, "Ms"), (Vs, "Vs"))]
     if eight:
-        blocks = [(s + ADAMW_BLOCK - 1) // ADAMW_BLOCK for s in sizes]
-        msp = _adamw_list(M_scales, "M_scales", dev, (torch.float32,), blocks)
-        vsp = _adamw_list(V_scales, "V_scales", dev, (torch.float32,), blocks)
-    if n > 1:
-        for ptrs in (pp, mp, vp):
-            given = [p for p in ptrs if p]
-            if len(set(given)) != len(given):
-                raise RgcError("a tensor is listed twice")
+        given += [_adamw_list(ts, name, ("Float",), sizes, ADAMW_BLOCK)
+                  for ts, name in ((M_scales, "M_scales"), (V_scales, "V_scales"))]
+    if any(x[3] != dev.index for x in given):
+        raise RgcError("all tensors must be on the same device")
+    if n > 1 and not all(_lists().distinct(given[i][0]) for i in (0, 2, 3)):
+        raise RgcError("a tensor is listed twice")
+    pp, gp, mp, vp, *scales = [(_vp * n).from_buffer_copy(x[0]) for x in given]
+    msp, vsp = scales if eight else (None, None)
     if grad_scale is not None:
         _dense(grad_scale, torch.float32, "grad_scale")
         if grad_scale.numel() != 1:
             raise RgcError("grad_scale must be one float32")
     with _on(dev):
-        _check(lib.rgc_adamw_batch(n, _DTYPES[Ps[0].dtype], _DTYPES[Gs[0].dtype], 8 if eight else 32, pp, gp, mp, vp,
-                                   msp, vsp, _i64s(sizes), lr, beta1, beta2, eps, weight_decay, step,
+        _check(lib.rgc_adamw_batch(n, _TYPE_NAMES[given[0][2]], _TYPE_NAMES[given[1][2]], 8 if eight else 32, pp, gp, mp,
+                                   vp, msp, vsp, (_i64 * n).from_buffer_copy(sizes), lr, beta1, beta2, eps, weight_decay, step,
                                    grad_scale.data_ptr() if grad_scale is not None else None,
                                    seed & 0xFFFFFFFFFFFFFFFF, _stream(dev)))
     return Ps

@@ -48,7 +48,7 @@ def test_cross_entropy_forward(lib, kw, want):
     (dict(T=-1), SHAPE), (dict(V=0), SHAPE), (dict(r=128), SHAPE), (dict(lddx=56), SHAPE),
     (dict(V=100), UNSUP),  # a sketched head's V is a multiple of 8
     (dict(r=24), UNSUP), (dict(T=65537), UNSUP), (dict(lddx=(1 << 23) + 8), UNSUP),
-    (dict(dX=None), NULL), (dict(lse=None), NULL), (dict(grad=None), NULL), (dict(XP=None), NULL), (dict(C=None), NULL),
+    (dict(dX=None, r=0, XP=None, C=None), NULL), (dict(lse=None), NULL), (dict(grad=None), NULL), (dict(XP=None), NULL), (dict(C=None), NULL),
     (dict(dX=FAKE + 8), ALIGN), (dict(lddx=68), ALIGN), (dict(C=FAKE + 4), ALIGN), (dict(grad=FAKE + 1), ALIGN),
     (dict(ws=FAKE + 64), ALIGN), (dict(ws=None), WS), (dict(n=1000), WS),
 ])
