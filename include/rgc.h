@@ -475,7 +475,7 @@ rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_d
  * Arrays are HOST arrays of n entries, n without limit (48 tensors a launch);
  * parameters, gradients and moments 16-byte aligned, at most 2^34 elements. A
  * tensor may be listed once only. RGC_ERR_VALUE: step < 1, a beta outside
- * [0, 1), eps <= 0 (as fp32), or a scalar that is not finite. */
+ * [0, 1), eps below 2^-126 (as fp32), or a scalar that is not finite. */
 rgc_status_t rgc_adamw_batch(int64_t n, rgc_dtype_t pt, rgc_dtype_t gt, int state_bits, void* const* Ps,
                              const void* const* Gs, void* const* Ms, void* const* Vs, float* const* Mscales,
                              float* const* Vscales, const int64_t* numels, double lr, double beta1, double beta2,

@@ -125,7 +125,7 @@ def test_adamw(lib):
         assert _adam(lib, **kw) == UNSUP, kw
     assert _adam(lib, numels=(-1,)) == SHAPE
     for kw in (dict(lr=nan), dict(lr=inf), dict(b1=1.0), dict(b1=-0.1), dict(b2=1.0), dict(b2=nan), dict(eps=0.0),
-               dict(eps=-1e-8), dict(eps=1e-60), dict(eps=inf), dict(wd=nan), dict(step=0)):
+               dict(eps=-1e-8), dict(eps=1e-60), dict(eps=1e-39), dict(eps=inf), dict(wd=nan), dict(step=0)):
         assert _adam(lib, **kw) == VALUE, kw
     for kw in (dict(P=None), dict(G=None), dict(M=None), dict(V=None), dict(Ms=None), dict(Vs=None), dict(P="none"),
                dict(Ms="none")):
