@@ -252,7 +252,7 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
       for (int nt = 0; nt < NI; ++nt) {
         const f32x4_t d = t.acc[mt][nt];
         const u32x2v_t h = {f32x2_to_bf16x2_rne(d[0], d[1]), f32x2_to_bf16x2_rne(d[2], d[3])};
-        // D - hi, exact: hi is D's leading bits
+        // what the term leaves, exact: it is the value's leading bits
         t.acc[mt][nt] = d - f32x4_t{__uint_as_float(h.x << 16), __uint_as_float(h.x & 0xFFFF0000u),
                                     __uint_as_float(h.y << 16), __uint_as_float(h.y & 0xFFFF0000u)};
         *(RGC_LDS u32x2v_t*)(lds + to[nt] + 256 * kRowChunks * mt) = h;
@@ -492,14 +492,18 @@ CeGrid grid_of(int64_t T, int64_t V) {
   return g;
 }
 
+// Workgroups of the grid.
+int64_t blocks_of(int64_t T, int64_t V, const CeGrid& g) {
+  if (few_tokens(T)) return g.ntiles;
+  const int64_t before = g.split == V ? g.ntiles : g.split / kGtTile;  // columns of large tiles
+  return g.large + (T + SmallTile::kRows - 1) / SmallTile::kRows * (g.ntiles - before);
+}
+
 template <bool BACKWARD>
 rgc_status_t logits_launch(CeArgs& a, hipStream_t s) {
-  const bool few = few_tokens(a.T);
   a.grid = grid_of(a.T, a.V);
-  const int64_t before = few ? 0 : a.grid.split == a.V ? a.grid.ntiles : a.grid.split / kGtTile;
-  const int64_t rows = few ? 1 : (a.T + SmallTile::kRows - 1) / SmallTile::kRows;
-  const int64_t blocks = a.grid.large + rows * (a.grid.ntiles - before);
-  if (few) hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, true>), dim3((unsigned)blocks), dim3(kGtThreads), 0, s, a);
+  const int64_t blocks = blocks_of(a.T, a.V, a.grid);
+  if (few_tokens(a.T)) hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, true>), dim3((unsigned)blocks), dim3(kGtThreads), 0, s, a);
   else hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, false>), dim3((unsigned)blocks), dim3(kGtThreads), 0, s, a);
   return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP;
 }
@@ -606,7 +610,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int6
   at += part_bytes(T, V);
   a.zt = reinterpret_cast<float*>(at);
   at += up256((size_t)T * 4);
-  if (((T + 63) / 64) * ((V + 127) / 128) >= int64_t(1) << 23) return RGC_ERR_UNSUPPORTED;  // threads of a launch
+  if (blocks_of(T, V, grid_of(T, V)) >= int64_t(1) << 22) return RGC_ERR_UNSUPPORTED;  // 2^31 threads of a launch
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (r > 0) {  // the layer's X P, as rgc_project makes it
     st = rgc_project(X, ldx, P, XP, T, k, r, at, ws_bytes - (size_t)(at - static_cast<char*>(ws)), stream);

@@ -42,7 +42,11 @@ class LayerNormFunction(torch.autograd.Function):
 class LayerNorm(torch.nn.Module):
     """Norm of the last dimension (kind "layer", or "rms" for the root-mean-square
     norm, which has no bias). Gains in float32 unless told otherwise: beside
-    bf16 activations they cost nothing and their gradients stay float32."""
+    bf16 activations they cost nothing and their gradients stay float32.
+
+    As with every torch parameter, a backward pass is captured into a graph
+    only while no eager autograd graph over the same parameters is alive: torch
+    would tie the capture to that graph's stream and end the process."""
 
     def __init__(self, features: int, eps: float = 1e-5, kind: str = "layer", bias: bool = True, device=None,
                  dtype: torch.dtype = torch.float32):

@@ -48,7 +48,8 @@ class SketchedCrossEntropy(SketchedLinear):
     outside 0 .. vocabulary - 1 (-100, say) is ignored: loss 0, no gradient.
     Weigh and sum the losses as the objective asks (a mean over the tokens that
     count, advantages). begin_update, apply_update and the carried norm are
-    SketchedLinear's: the losses' backward adds the head's D^T (X P) to `sketch`.
+    SketchedLinear's: the losses' backward adds the head's D^T (X P) to `sketch`
+    (x has to require a gradient for the backward to come this far).
     The vocabulary is a multiple of 8, as every sketched layer's width.
     """
 

@@ -106,6 +106,13 @@ def test_against_64_bits(dev, T, V, k, r):
     _run(dev, T, V, k, r, seed=100 + T + V)
 
 
+# 256 x 256 tiles alone (129 and 144 of them), and rounds of them with small tiles behind (on 256 compute units)
+@pytest.mark.parametrize("T,V,k,r", [(520, 11016, 136, 16), (2100, 4001, 264, 0), (700, 24008, 72, 4), (1025, 16385, 72, 0)])
+def test_large_tiles_against_64_bits(dev, T, V, k, r):
+    print(T, V, k, r, flush=True)
+    _run(dev, T, V, k, r, seed=T + V)
+
+
 @pytest.mark.parametrize("left", [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64])
 def test_every_kind_of_last_step(dev, left):
     """dX's K ends `left` rows into a step of 64; the logits' K likewise where a layer's width allows it."""
