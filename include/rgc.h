@@ -398,8 +398,9 @@ rgc_status_t rgc_linear_backward(const uint16_t* D, int64_t ldd, const uint16_t*
  *   token, formed from z again for one piece of the vocabulary after another;
  *   dX = bf16(D W): T x k, row stride lddx, overwritten; each piece's D rounded
  *   to bf16, the pieces added in fp32;
- *   C += D^T XP with r > 0: V x r fp32, as rgc_accumulate adds, D as two bf16
- *   terms (hi + lo, 2^-17 relative), so that C's error is that of fp32 sums.
+ *   C += D^T XP with r > 0: V x r fp32, only added to as by rgc_accumulate, D in
+ *   fp32 or as two bf16 terms (hi + lo, 2^-18 relative) and the targets' entries
+ *   in fp32, so that C's error is that of fp32 sums.
  *   C is what rgc_apply turns into the head's update. r = 0 (XP and C may then
  *   be NULL) is a frozen head: dX alone. With r > 0 dX may be NULL (an input
  *   that needs no gradient): C alone.

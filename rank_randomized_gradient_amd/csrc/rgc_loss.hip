@@ -24,7 +24,8 @@
 // hi alone. The targets' entries are by far the largest of D (of the order of
 // g, the others of g / V), so what the terms leave of them is kept in fp32, one
 // value a token, and added where it costs little: rest_t W_y(t) to dX when it is
-// rounded, and rest_t XP_t to C's row y(t) in a last launch.
+// rounded, and rest_t XP_t to C's row y(t) in a last launch. Up to 128 tokens
+// one tile holds them all, and adds its rows of the sketch itself, from D in fp32.
 //
 // Bound by MFMA: 2 T V k operations for the loss, 6 T V k + 4 T V r for the
 // gradient. Where dX has few tiles (few tokens), each is split over K among
@@ -66,6 +67,9 @@ struct CeArgs {
   float* rest;         // D - hi at each token's target
   float* rest_sketch;  // with lo: D - hi - lo there
   int64_t ldd;
+  float* C;            // few tokens: the sketch's rows of the piece, added to here; else null
+  const uint16_t* XP;
+  int r;
 };
 
 typedef GtTile<8, 4, 2, false> LargeTile;   // 256 x 256
@@ -160,35 +164,83 @@ __device__ __forceinline__ void forward_tile(const CeArgs& a, int64_t m0, int64_
   }
 }
 
-// lse and loss of 64 tokens per workgroup: sixteen waves take every sixteenth
-// tile each, then their maxima and sums are joined in wave order.
+// Joins a token's tiles: a wave per token, lane l taking every 64th tile from
+// l, then the lanes' maxima and sums by a xor butterfly. The sixteen tokens of
+// a workgroup share the lines of their partial sums.
 __global__ __launch_bounds__(1024) void ce_finish_kernel(CeArgs a, float* loss, float* lse) {
-  __shared__ float tops[16][64], sums[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * 64 + lane;
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6);
+  if (t >= a.T) return;
   float top = -INFINITY, s = 0.f;
-  if (t < a.T) {
 #pragma unroll 4
-    for (int64_t j = wave; j < a.grid.ntiles; j += 16) {
-      const float2 p = a.part[j * a.T + t];
-      const float m = fmaxf(top, p.x), base = m == -INFINITY ? 0.f : m;
-      s = s * fast_exp(top - base) + p.y * fast_exp(p.x - base);
-      top = m;
-    }
+  for (int64_t j = lane; j < a.grid.ntiles; j += 64) {
+    const float2 p = a.part[j * a.T + t];
+    const float m = fmaxf(top, p.x), base = m == -INFINITY ? 0.f : m;
+    s = s * fast_exp(top - base) + p.y * fast_exp(p.x - base);
+    top = m;
   }
-  tops[wave][lane] = top;
-  sums[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && t < a.T) {
-    for (int w = 1; w < 16; ++w) top = fmaxf(top, tops[w][lane]);
-    const float base = top == -INFINITY ? 0.f : top;
-    s = 0.f;
-    for (int w = 0; w < 16; ++w) s += sums[w][lane] * fast_exp(tops[w][lane] - base);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const float x = __shfl_xor(top, off, 64), y = __shfl_xor(s, off, 64);
+    const float m = fmaxf(top, x), base = m == -INFINITY ? 0.f : m;
+    s = s * fast_exp(top - base) + y * fast_exp(x - base);
+    top = m;
+  }
+  if (lane == 0) {
     const float l = top + logf(s);
     const int64_t y = a.targets[t];
     lse[t] = l;
-    loss[t] = y >= 0 && y < a.V ? l - a.zt[t] : 0.f;
+    loss[t] = y >= 0 && y < a.vocab ? l - a.zt[t] : 0.f;
   }
+}
+
+// C's rows of a tile += D^T XP, for the tile that holds all T tokens: no partial
+// sums to join and no second term of D, which is taken in fp32 from the registers
+// by way of LDS. A thread takes four ranks of up to 16 neighbouring rows and
+// goes through the tokens in order.
+template <int MI, int NI, typename Tile>
+__device__ __forceinline__ void sketch_tile(const CeArgs& a, const Tile& t, int64_t n0, int width, char* smem,
+                                            const CeRows* rows) {
+  constexpr int kCols = Tile::kCols;
+  const int g = t.lane >> 4, li = t.lane & 15, wm = t.wave & 1, wn = t.wave >> 1;
+  const int T = (int)a.T, quads = a.r / 4;
+  float* d = reinterpret_cast<float*>(smem);  // [token][column]
+  uint2* xp = reinterpret_cast<uint2*>(smem + 4 * Tile::kRows * kCols);  // [token][quad]
+  static_assert(4 * Tile::kRows * kCols + 2 * Tile::kRows * 256 <= kCeLds, "D and XP of a tile in LDS");
+#pragma unroll
+  for (int mt = 0; mt < MI; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NI; ++nt)
+      *reinterpret_cast<f32x4_t*>(d + (16 * MI * wm + 16 * mt + li) * kCols + 16 * NI * wn + 16 * nt + 4 * g) = t.acc[mt][nt];
+  for (int i = threadIdx.x; i < T * quads; i += kGtThreads)  // zeros for the ignored, whatever their rows hold
+    xp[i] = rows->at[i / quads] == -2 ? make_uint2(0u, 0u) : reinterpret_cast<const uint2*>(a.XP)[i];
+  __syncthreads();
+  const int quad = threadIdx.x % quads, part = threadIdx.x / quads, parts = kGtThreads / quads;
+  for (int row0 = 4 * part; row0 < width; row0 += 4 * parts) {
+    f32x4_t sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (part < parts) {
+#pragma unroll 4
+      for (int k = 0; k < T; ++k) {
+        const uint2 x = xp[k * quads + quad];
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(d + k * kCols + row0);
+        const f32x4_t w = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u), __uint_as_float(x.y << 16),
+                           __uint_as_float(x.y & 0xFFFF0000u)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[i][e] = __builtin_fmaf(v[i], w[e], sum[i][e]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (row0 + i < width) {
+          f32x4_t* c = reinterpret_cast<f32x4_t*>(a.C + (n0 + row0 + i) * a.r + 4 * quad);
+          *c += sum[i];
+        }
+    }
+  }
+  __syncthreads();
 }
 
 // A piece's D, hi (and lo): T x ldd, zero in the columns behind the piece.
@@ -233,6 +285,9 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
         for (int e = 0; e < 4; ++e)
           if (first + 16 * nt + e >= width) t.acc[mt][nt][e] = 0.f;
     }
+  }
+  if constexpr (MI <= 4) {
+    if (a.C) sketch_tile<MI, NI>(a, t, n0, width, smem, rows);
   }
   RGC_LDS char* lds = (RGC_LDS char*)smem;
   uint32_t to[NI];  // this lane's places in the row of mt = 0
@@ -459,8 +514,9 @@ __global__ __launch_bounds__(256) void ce_xp_kernel(const uint2* XP, const int64
 int64_t tiles_of(int64_t n) { return (n + kGtTile - 1) / kGtTile; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Whether the logits take 64-row tiles.
+// Whether the logits take 64-row tiles, and whether one tile holds all tokens.
 bool few_tokens(int64_t T) { return T <= FlatTile::kRows; }
+bool one_tile(int64_t T) { return T <= SmallTile::kRows; }
 
 // Divides T x V logits into tiles. Large tiles run at the highest rate, but a
 // last round of them that fills few compute units costs as much as a full one:
@@ -480,7 +536,8 @@ CeGrid grid_of(int64_t T, int64_t V) {
   const int64_t rounds = m * n / cus;
   double best = (double)((m * n + cus - 1) / cus);
   int64_t columns = n;  // of large tiles
-  for (int64_t keep = rounds; keep >= 0 && keep >= rounds - 1; --keep) {
+  if (one_tile(T)) best = 1e30, columns = 0;  // half of a large tile's rows would be empty
+  for (int64_t keep = one_tile(T) ? 0 : rounds; keep >= 0 && keep >= rounds - 1; --keep) {
     const int64_t c = keep * cus / m < n ? keep * cus / m : n;
     const int64_t small = small_rows * small_columns(c * kGtTile);
     const double cost = (double)((m * c + cus - 1) / cus) + (double)((small + cus - 1) / cus) * 0.25 / kCeSmallRate;
@@ -513,6 +570,7 @@ struct Plan {
   int64_t piece;   // vocabulary rows of a piece
   int64_t pieces;
   int64_t splits;  // of dX's sums within a piece
+  bool fused;      // the sketch from the tiles of D themselves
   bool stacked;    // hi and lo in one accumulation of 2 T tokens
   size_t d, xp, rest, slab, acc;  // bytes of the workspace's parts
   size_t total() const { return d + xp + rest + slab + acc; }
@@ -520,7 +578,8 @@ struct Plan {
 
 Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
   Plan p{};
-  const int64_t terms = r > 0 ? 2 : 1;
+  p.fused = r > 0 && one_tile(T);
+  const int64_t terms = r > 0 && !p.fused ? 2 : 1;
   // a piece's D fills the 256 MB last-level cache at most
   int64_t piece = (int64_t(256) << 20) / (T * 2 * terms) / kGtTile * kGtTile;
   if (piece < 1024) piece = 1024;
@@ -543,10 +602,10 @@ Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
   }
   p.stacked = 2 * T <= kMaxTiledDim;
   p.d = up256((size_t)(terms * T * p.piece) * 2);
-  p.xp = r > 0 ? up256((size_t)((p.stacked ? 2 : 1) * T * r) * 2) : 0;
-  p.rest = up256((size_t)T * 4) * (r > 0 ? 2 : 1);
+  p.xp = r > 0 && !p.fused ? up256((size_t)((p.stacked ? 2 : 1) * T * r) * 2) : 0;
+  p.rest = up256((size_t)T * 4) * terms;
   p.slab = p.pieces > 1 || p.splits > 1 ? up256((size_t)(p.splits * T * k) * 4) : 0;
-  if (r > 0) {
+  if (terms == 2) {
     // every width the pieces have: the whole ones and the last
     const int64_t tokens = p.stacked ? 2 * T : T, last = V - (p.pieces - 1) * p.piece;
     const size_t a = rgc_accumulate_workspace_size(tokens, p.piece, r), b = rgc_accumulate_workspace_size(tokens, last, r);
@@ -617,7 +676,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int6
     if (st != RGC_OK) return st;
   }
   if ((st = logits_launch<false>(a, s)) != RGC_OK) return st;
-  hipLaunchKernelGGL(ce_finish_kernel, dim3((unsigned)((T + 63) / 64)), dim3(1024), 0, s, a, loss, lse);
+  hipLaunchKernelGGL(ce_finish_kernel, dim3((unsigned)((T + 15) / 16)), dim3(1024), 0, s, a, loss, lse);
   return launched();
 }
 
@@ -650,7 +709,8 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
   float* slab = p.slab ? reinterpret_cast<float*>(at + p.d + p.xp + p.rest) : nullptr;
   char* acc = at + p.d + p.xp + p.rest + p.slab;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (r > 0) {
+  const bool accumulate = r > 0 && !p.fused;
+  if (accumulate) {
     const int64_t n = T * r / 4;
     hipLaunchKernelGGL(ce_xp_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, reinterpret_cast<const uint2*>(XP),
                        targets, V, T, (int)(r / 4), p.stacked ? 2 : 1, reinterpret_cast<uint2*>(xp));
@@ -668,7 +728,8 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
     const int64_t v0 = q * p.piece, rows = V - v0 < p.piece ? V - v0 : p.piece;
     a.W = W + v0 * ldw, a.V = rows, a.v0 = v0;
     a.ldd = tiles_of(rows) * kGtTile;
-    a.hi = D, a.lo = r > 0 ? D + T * a.ldd : nullptr;
+    a.hi = D, a.lo = accumulate ? D + T * a.ldd : nullptr;
+    if (p.fused) a.C = C + v0 * r, a.XP = XP, a.r = (int)r;
     if ((st = logits_launch<true>(a, s)) != RGC_OK) return st;
     if (dX) {
       x.D = a.hi, x.W = a.W, x.ldd = a.ldd, x.K = rows, x.first = q == 0;
@@ -677,7 +738,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
       hipLaunchKernelGGL(ce_dx_kernel, dim3((unsigned)(x.mtiles * x.ntiles * p.splits)), dim3(kGtThreads), 0, s, x);
       if ((st = launched()) != RGC_OK) return st;
     }
-    if (r > 0) {
+    if (accumulate) {
       float* c = C + v0 * r;
       if (p.stacked) {
         st = rgc_accumulate(D, a.ldd, xp, c, 2 * T, rows, r, acc, p.acc, stream);
@@ -688,7 +749,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
       if (st != RGC_OK) return st;
     }
   }
-  if (r > 0) {
+  if (accumulate) {
     hipLaunchKernelGGL(ce_rest_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, targets, a.rest_sketch, XP, C, T, V,
                        (int)r);
     if ((st = launched()) != RGC_OK) return st;

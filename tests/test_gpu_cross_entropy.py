@@ -94,10 +94,12 @@ def _run(dev, T, V, k, r, seed, **kw):
 
 
 # one token, one entry; widths of one 16-byte chunk; K of the logits (k) and of dX (V) ending anywhere in a step of
-# 64; tiles ending anywhere; every kind of rank; more entries than one piece of the vocabulary
+# 64; tiles ending anywhere; every kind of rank; more entries than one piece of the vocabulary; one tile of tokens
+# (up to 64, up to 128), which makes its own part of the sketch, and one more
 SHAPES = [(1, 1, 8, 0), (1, 8, 8, 8), (2, 7, 16, 0), (24, 1000, 64, 16), (300, 777, 520, 0), (257, 2056, 72, 4),
           (513, 264, 1000, 8), (129, 1025, 136, 0), (255, 17, 264, 0), (256, 256, 256, 256), (64, 4104, 2048, 128),
-          (1000, 1048, 200, 48), (33, 70008, 64, 16), (5, 70001, 24, 0)]
+          (1000, 1048, 200, 48), (33, 70008, 64, 16), (5, 70001, 24, 0), (65, 1000, 72, 4), (100, 2056, 136, 48),
+          (128, 520, 264, 256), (129, 1000, 64, 16), (7, 1288, 264, 240)]
 
 
 @pytest.mark.parametrize("T,V,k,r", SHAPES)
