@@ -472,16 +472,35 @@ __global__ __launch_bounds__(kGtThreads, 1) void ce_dx_kernel(DxArgs a) {
   }
 }
 
-// dX = bf16(sum of the slabs + rest W_y), eight columns to a thread.
+// dX = bf16(sum of the slabs + rest W_y), eight columns to a thread. GROUPS > 1:
+// that many threads share the slabs of eight columns (thread group q takes slabs
+// q, q + GROUPS, ...) and join through LDS in order of q.
+template <int GROUPS>
 __global__ __launch_bounds__(256) void ce_join_kernel(DxArgs a, int splits) {
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, all = a.T * a.k;
-  if (at >= all) return;
-  f32x4_t u = *reinterpret_cast<const f32x4_t*>(a.slab + at), v = *reinterpret_cast<const f32x4_t*>(a.slab + at + 4);
+  constexpr int kVectors = 256 / GROUPS;
+  __shared__ f32x4_t parts[GROUPS > 1 ? GROUPS : 1][kVectors][2];
+  const int v = threadIdx.x % kVectors, q = threadIdx.x / kVectors;
+  const int64_t at = ((int64_t)blockIdx.x * kVectors + v) * 8, all = a.T * a.k;
+  f32x4_t lo = {0.f, 0.f, 0.f, 0.f}, hi = {0.f, 0.f, 0.f, 0.f};
+  if (at < all) {
 #pragma unroll 4
-  for (int s = 1; s < splits; ++s) {
-    u += *reinterpret_cast<const f32x4_t*>(a.slab + s * all + at);
-    v += *reinterpret_cast<const f32x4_t*>(a.slab + s * all + at + 4);
+    for (int s = q; s < splits; s += GROUPS) {
+      lo += *reinterpret_cast<const f32x4_t*>(a.slab + s * all + at);
+      hi += *reinterpret_cast<const f32x4_t*>(a.slab + s * all + at + 4);
+    }
   }
+  if constexpr (GROUPS > 1) {
+    parts[q][v][0] = lo;
+    parts[q][v][1] = hi;
+    __syncthreads();
+    if (q > 0) return;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) {
+      lo += parts[i][v][0];
+      hi += parts[i][v][1];
+    }
+  }
+  if (at >= all) return;
   const int64_t row = at / a.k, col = at - row * a.k;
   const uint16_t* wy;
   const float rest = rest_of(a, row, &wy);
@@ -490,13 +509,13 @@ __global__ __launch_bounds__(256) void ce_join_kernel(DxArgs a, int splits) {
     load_bf16_row<8>(wy + col, w);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      u[e] = __builtin_fmaf(rest, w[e], u[e]);
-      v[e] = __builtin_fmaf(rest, w[e + 4], v[e]);
+      lo[e] = __builtin_fmaf(rest, w[e], lo[e]);
+      hi[e] = __builtin_fmaf(rest, w[e + 4], hi[e]);
     }
   }
   *reinterpret_cast<uint4*>(a.dX + row * a.lddx + col) =
-      make_uint4(f32x2_to_bf16x2_rne(u[0], u[1]), f32x2_to_bf16x2_rne(u[2], u[3]), f32x2_to_bf16x2_rne(v[0], v[1]),
-                 f32x2_to_bf16x2_rne(v[2], v[3]));
+      make_uint4(f32x2_to_bf16x2_rne(lo[0], lo[1]), f32x2_to_bf16x2_rne(lo[2], lo[3]), f32x2_to_bf16x2_rne(hi[0], hi[1]),
+                 f32x2_to_bf16x2_rne(hi[2], hi[3]));
 }
 
 // XP for the accumulation, `copies` times over (for the two terms of D), with
@@ -755,9 +774,12 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
     if ((st = launched()) != RGC_OK) return st;
   }
   if (dX && p.splits > 1) {
-    const int64_t n = (T * k / 8 + 255) / 256;
     x.dX = dX;
-    hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)n), dim3(256), 0, s, x, (int)p.splits);
+    const int64_t vectors = T * k / 8;  // (128 slabs of 3 x 512 in 14 us by one thread each)
+    if (p.splits >= 32)
+      hipLaunchKernelGGL(ce_join_kernel<8>, dim3((unsigned)((vectors + 31) / 32)), dim3(256), 0, s, x, (int)p.splits);
+    else
+      hipLaunchKernelGGL(ce_join_kernel<1>, dim3((unsigned)((vectors + 255) / 256)), dim3(256), 0, s, x, (int)p.splits);
     st = launched();
   }
   return st;
