@@ -15,7 +15,9 @@ class AdamW:
     state_bits 8 holds both moments as e4m3 with a scale per 128 elements (2.06
     bytes an element), 32 as float32 (8 bytes). `seed` and the count of steps
     give the rounding bits, so a run repeats bit for bit. Parameters and
-    gradients are contiguous bf16 or float32 tensors.
+    gradients are contiguous bf16 or float32 tensors. The step count and the
+    rounding key are host values: a step captured into a graph would repeat
+    both in every replay.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
