@@ -196,8 +196,8 @@ __global__ __launch_bounds__(1024) void ce_finish_kernel(CeArgs a, float* loss, 
 
 // C's rows of a tile += D^T XP, for the tile that holds all T tokens: no partial
 // sums to join and no second term of D, which is taken in fp32 from the registers
-// by way of LDS. A thread takes four ranks of up to 16 neighbouring rows and
-// goes through the tokens in order.
+// by way of LDS. A thread takes four ranks of four neighbouring rows at a time
+// and goes through the tokens in order.
 template <int MI, int NI, typename Tile>
 __device__ __forceinline__ void sketch_tile(const CeArgs& a, const Tile& t, int64_t n0, int width, char* smem,
                                             const CeRows* rows) {

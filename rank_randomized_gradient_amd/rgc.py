@@ -799,8 +799,9 @@ def rgc_layer_norm_forward(X: torch.Tensor, weight: torch.Tensor | None = None, 
     kid = _norm_kind(kind)
     wt = _norm_params(n, weight, bias)
     if Y is None:
-        Y = torch.empty((rows, n), dtype=X.dtype, device=dev)
-    ldy = _norm_rows(Y, X, "Y")
+        Y, ldy = torch.empty((rows, n), dtype=X.dtype, device=dev), n
+    else:
+        ldy = _norm_rows(Y, X, "Y")
     mean = torch.empty(rows, dtype=torch.float32, device=dev) if kid == RGC_NORM_LAYER else None
     rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     with _on(dev):
@@ -833,8 +834,9 @@ def rgc_layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Ten
         if tuple(t.shape) != (rows,):
             raise RgcError(f"{name} must have one value per row")
     if dX is None:
-        dX = torch.empty((rows, n), dtype=X.dtype, device=dev)
-    lddx = _norm_rows(dX, X, "dX")
+        dX, lddx = torch.empty((rows, n), dtype=X.dtype, device=dev), n
+    else:
+        lddx = _norm_rows(dX, X, "dX")
     pt = torch.float32 if weight is None else weight.dtype
     dweight = torch.empty(n, dtype=pt, device=dev)
     dbias = torch.empty(n, dtype=pt, device=dev) if bias else None
