@@ -370,13 +370,14 @@ __global__ __launch_bounds__(256) void ce_rest_kernel(const int64_t* targets, co
   if (t >= T) return;
   const int64_t y = targets[t];
   if (y < 0 || y >= V) return;
-  // 512 targets at a time, so that their loads are in flight together
+  // 512 targets at a time, so that their loads are in flight together (from
+  // clamped places: a load under a condition is waited for before the next)
   for (int64_t j0 = 0; j0 < t; j0 += 512) {
     bool same = false;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const int64_t j = j0 + 64 * c + lane;
-      same |= j < t && targets[j] == y;
+      const int64_t j = j0 + 64 * c + lane, other = targets[j < T ? j : T - 1];
+      same |= j < t && other == y;
     }
     if (__any(same)) return;
   }
@@ -385,9 +386,10 @@ __global__ __launch_bounds__(256) void ce_rest_kernel(const int64_t* targets, co
     uint64_t same[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const int64_t j = j0 + 64 * c + lane;
-      same[c] = __ballot(j < T && targets[j] == y);
+      const int64_t j = j0 + 64 * c + lane, other = targets[j < T ? j : T - 1];
+      same[c] = __ballot(j < T && other == y);
     }
+#pragma unroll
     for (int c = 0; c < 8; ++c)
       while (same[c]) {
         const int64_t j = j0 + 64 * c + __builtin_ctzll(same[c]);
