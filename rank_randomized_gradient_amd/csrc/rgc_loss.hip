@@ -194,10 +194,38 @@ __global__ __launch_bounds__(1024) void ce_finish_kernel(CeArgs a, float* loss, 
   }
 }
 
+// R rows and four ranks of C for a thread, the tokens in order.
+template <int R>
+__device__ __forceinline__ void sketch_rows(float* C, int r, const float* d, int cols, const uint2* xp, int T, int width) {
+  const int quads = r / 4, quad = threadIdx.x % quads, part = threadIdx.x / quads, parts = kGtThreads / quads;
+  if (part >= parts) return;
+  for (int row0 = R * part; row0 < width; row0 += R * parts) {
+    f32x4_t sum[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) sum[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < T; ++k) {
+      const uint2 x = xp[k * quads + quad];
+      const f32x4_t w = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u), __uint_as_float(x.y << 16),
+                         __uint_as_float(x.y & 0xFFFF0000u)};
+      float v[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) v[i] = d[k * cols + row0 + i];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[i][e] = __builtin_fmaf(v[i], w[e], sum[i][e]);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (row0 + i < width) *reinterpret_cast<f32x4_t*>(C + (int64_t)(row0 + i) * r + 4 * quad) += sum[i];
+  }
+}
+
 // C's rows of a tile += D^T XP, for the tile that holds all T tokens: no partial
 // sums to join and no second term of D, which is taken in fp32 from the registers
-// by way of LDS. A thread takes four ranks of four neighbouring rows at a time
-// and goes through the tokens in order.
+// by way of LDS. As many neighbouring rows to a thread as give the 512 threads
+// the tile's 128 rows in one pass (above rank 64 eight, for fewer LDS reads).
 template <int MI, int NI, typename Tile>
 __device__ __forceinline__ void sketch_tile(const CeArgs& a, const Tile& t, int64_t n0, int width, char* smem,
                                             const CeRows* rows) {
@@ -212,34 +240,17 @@ __device__ __forceinline__ void sketch_tile(const CeArgs& a, const Tile& t, int6
 #pragma unroll
     for (int nt = 0; nt < NI; ++nt)
       *reinterpret_cast<f32x4_t*>(d + (16 * MI * wm + 16 * mt + li) * kCols + 16 * NI * wn + 16 * nt + 4 * g) = t.acc[mt][nt];
-  for (int i = threadIdx.x; i < T * quads; i += kGtThreads)  // zeros for the ignored, whatever their rows hold
-    xp[i] = rows->at[i / quads] == -2 ? make_uint2(0u, 0u) : reinterpret_cast<const uint2*>(a.XP)[i];
-  __syncthreads();
-  const int quad = threadIdx.x % quads, part = threadIdx.x / quads, parts = kGtThreads / quads;
-  for (int row0 = 4 * part; row0 < width; row0 += 4 * parts) {
-    f32x4_t sum[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (part < parts) {
 #pragma unroll 4
-      for (int k = 0; k < T; ++k) {
-        const uint2 x = xp[k * quads + quad];
-        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(d + k * kCols + row0);
-        const f32x4_t w = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u), __uint_as_float(x.y << 16),
-                           __uint_as_float(x.y & 0xFFFF0000u)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[i][e] = __builtin_fmaf(v[i], w[e], sum[i][e]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (row0 + i < width) {
-          f32x4_t* c = reinterpret_cast<f32x4_t*>(a.C + (n0 + row0 + i) * a.r + 4 * quad);
-          *c += sum[i];
-        }
-    }
+  for (int i = threadIdx.x; i < T * quads; i += kGtThreads) {
+    const uint2 x = reinterpret_cast<const uint2*>(a.XP)[i];
+    const bool live = rows->at[i / quads] != -2;  // zeros for the ignored, whatever their rows hold
+    xp[i] = make_uint2(live ? x.x : 0u, live ? x.y : 0u);
   }
+  __syncthreads();
+  float* C = a.C + n0 * a.r;
+  if (a.r > 64) sketch_rows<8>(C, a.r, d, kCols, xp, T, width);
+  else if (a.r > 16) sketch_rows<4>(C, a.r, d, kCols, xp, T, width);
+  else sketch_rows<1>(C, a.r, d, kCols, xp, T, width);
   __syncthreads();
 }
 
