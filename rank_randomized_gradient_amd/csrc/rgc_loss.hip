@@ -74,9 +74,11 @@ struct CeArgs {
 
 typedef GtTile<8, 4, 2, false> LargeTile;   // 256 x 256
 typedef GtTile<4, 2, 4, false> SmallTile;   // 128 x 128
-typedef GtTile<2, 2, 5, false> FlatTile;    // 64 x 128, for few tokens
-constexpr int kCeLds = LargeTile::kLds;
-static_assert(SmallTile::kLds <= kCeLds && FlatTile::kLds <= kCeLds, "one LDS array serves the tiles");
+// 64 x 128, for few tokens: three stages, so that two workgroups share a compute
+// unit, one's epilogue under the other's product. 64 x 50000 x 1024: D of rank 128
+// 49 us with one workgroup on five stages, 40 us so; the forward 23 and 19 us.
+typedef GtTile<2, 2, 3, false> FlatTile;
+static_assert(SmallTile::kLds <= LargeTile::kLds, "one LDS array serves the tiles of a launch");
 
 // What an epilogue needs of a tile's rows, fetched before the product.
 struct CeRows {
@@ -234,7 +236,7 @@ __device__ __forceinline__ void sketch_tile(const CeArgs& a, const Tile& t, int6
   const int T = (int)a.T, quads = a.r / 4;
   float* d = reinterpret_cast<float*>(smem);  // [token][column]
   uint2* xp = reinterpret_cast<uint2*>(smem + 4 * Tile::kRows * kCols);  // [token][quad]
-  static_assert(4 * Tile::kRows * kCols + 2 * Tile::kRows * 256 <= kCeLds, "D and XP of a tile in LDS");
+  static_assert(4 * Tile::kRows * kCols + 2 * Tile::kRows * 256 <= Tile::kLds, "D and XP of a tile in LDS");
 #pragma unroll
   for (int mt = 0; mt < MI; ++mt)
 #pragma unroll
@@ -347,8 +349,8 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
 
 // The logits' kernel of both directions: the tile of this workgroup.
 template <bool BACKWARD, bool FEW>
-__global__ __launch_bounds__(kGtThreads, 1) void ce_logits_kernel(CeArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[kCeLds];
+__global__ __launch_bounds__(kGtThreads, FEW ? 4 : 1) void ce_logits_kernel(CeArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[FEW ? FlatTile::kLds : LargeTile::kLds];
   __shared__ CeRows rows;
   int64_t i, j;
   if (!FEW && (int64_t)blockIdx.x < a.grid.large) {
@@ -364,10 +366,10 @@ __global__ __launch_bounds__(kGtThreads, 1) void ce_logits_kernel(CeArgs a) {
            a.grid.ntiles - before, 2 * kCeDown, &i, &j);
   const int64_t m0 = i * Tile::kRows, n0 = a.grid.split + j * Tile::kCols;
   if constexpr (BACKWARD) {
-    if constexpr (FEW) d_tile<2, 2, 5>(a, m0, n0, smem, &rows);
+    if constexpr (FEW) d_tile<2, 2, 3>(a, m0, n0, smem, &rows);
     else d_tile<4, 2, 4>(a, m0, n0, smem, &rows);
   } else {
-    if constexpr (FEW) forward_tile<2, 2, 5>(a, m0, n0, before + j, smem, &rows);
+    if constexpr (FEW) forward_tile<2, 2, 3>(a, m0, n0, before + j, smem, &rows);
     else forward_tile<4, 2, 4>(a, m0, n0, before + j, smem, &rows);
   }
 }
