@@ -78,6 +78,9 @@ typedef GtTile<4, 2, 4, false> SmallTile;   // 128 x 128
 // unit, one's epilogue under the other's product. 64 x 50000 x 1024: D of rank 128
 // 49 us with one workgroup on five stages, 40 us so; the forward 23 and 19 us.
 typedef GtTile<2, 2, 3, false> FlatTile;
+// 128 x 128 on two stages, two workgroups to a compute unit: for a launch of small
+// tiles alone that gives every compute unit more than one (pair_tiles).
+typedef GtTile<4, 2, 2, false> PairTile;
 static_assert(SmallTile::kLds <= LargeTile::kLds, "one LDS array serves the tiles of a launch");
 
 // What an epilogue needs of a tile's rows, fetched before the product.
@@ -299,7 +302,7 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
           if (first + 16 * nt + e >= width) t.acc[mt][nt][e] = 0.f;
     }
   }
-  if constexpr (MI <= 4) {
+  if constexpr (MI <= 4 && STAGES > 2) {  // (two stages leave no LDS for it)
     if (a.C) sketch_tile<MI, NI>(a, t, n0, width, smem, rows);
   }
   RGC_LDS char* lds = (RGC_LDS char*)smem;
@@ -372,6 +375,17 @@ __global__ __launch_bounds__(kGtThreads, FEW ? 4 : 1) void ce_logits_kernel(CeAr
     if constexpr (FEW) forward_tile<2, 2, 3>(a, m0, n0, before + j, smem, &rows);
     else forward_tile<4, 2, 4>(a, m0, n0, before + j, smem, &rows);
   }
+}
+
+template <bool BACKWARD>
+__global__ __launch_bounds__(kGtThreads, 4) void ce_pair_kernel(CeArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[PairTile::kLds];
+  __shared__ CeRows rows;
+  int64_t i, j;
+  gt_place(gt_logical(blockIdx.x, gridDim.x), (a.T + PairTile::kRows - 1) / PairTile::kRows, a.grid.ntiles, 2 * kCeDown, &i, &j);
+  const int64_t m0 = i * PairTile::kRows, n0 = j * PairTile::kCols;
+  if constexpr (BACKWARD) d_tile<4, 2, 2>(a, m0, n0, smem, &rows);
+  else forward_tile<4, 2, 2>(a, m0, n0, j, smem, &rows);
 }
 
 // C_y += sum of rest_t XP_t over the tokens with target y, in token order. A
@@ -590,12 +604,28 @@ int64_t blocks_of(int64_t T, int64_t V, const CeGrid& g) {
   return g.large + (T + SmallTile::kRows - 1) / SmallTile::kRows * (g.ntiles - before);
 }
 
+// Whether a launch takes two workgroups to a compute unit, one's epilogue under
+// the other's product: where there are no large tiles and more small ones than
+// compute units. 300 x 20000 x 1024 (471 tiles): forward 34 us with one workgroup
+// on four stages, 26 us so; 300 x 20000 x 4096: 100 and 73 us. Where no unit gets a
+// second the deeper stages win, 100 x 12000 x 2048 (94): 29 and 33 us. So they do
+// in a forward of several rounds with little epilogue to hide: 128 x 70000 x 4096
+// (547) 163 and 189 us, 128 x 95000 x 2048 (743) 111 and 119, but 128 x 70000 x 1024
+// 51 and 45; the backwards of the three gain 8, 2 and 12 %. The tile's own sketch
+// needs the larger LDS.
+bool pair_tiles(const CeArgs& a, int64_t blocks, bool backward) {
+  const int64_t cus = device_compute_units();
+  return a.grid.large == 0 && !a.C && blocks > cus && (backward || blocks <= 2 * cus || a.k <= 1024);
+}
+
 template <bool BACKWARD>
 rgc_status_t logits_launch(CeArgs& a, hipStream_t s) {
   a.grid = grid_of(a.T, a.V);
   const int64_t blocks = blocks_of(a.T, a.V, a.grid);
-  if (few_tokens(a.T)) hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, true>), dim3((unsigned)blocks), dim3(kGtThreads), 0, s, a);
-  else hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, false>), dim3((unsigned)blocks), dim3(kGtThreads), 0, s, a);
+  const dim3 grid((unsigned)blocks), threads(kGtThreads);
+  if (few_tokens(a.T)) hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, true>), grid, threads, 0, s, a);
+  else if (pair_tiles(a, blocks, BACKWARD)) hipLaunchKernelGGL((ce_pair_kernel<BACKWARD>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, false>), grid, threads, 0, s, a);
   return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP;
 }
 

@@ -108,6 +108,14 @@ def test_against_64_bits(dev, T, V, k, r):
     _run(dev, T, V, k, r, seed=100 + T + V)
 
 
+# two workgroups to a compute unit (more 128 x 128 tiles than compute units, no larger ones): one row of tiles, three,
+# six; more than two rounds of them at a width where the forward takes the other form
+@pytest.mark.parametrize("T,V,k,r", [(100, 33000, 72, 0), (300, 20001, 136, 0), (700, 9000, 72, 8), (66, 65800, 1032, 0)])
+def test_tiles_in_pairs(dev, T, V, k, r):
+    print(T, V, k, r, flush=True)
+    _run(dev, T, V, k, r, seed=500 + T + V)
+
+
 # 256 x 256 tiles alone (129 and 144 of them), and rounds of them with small tiles behind (on 256 compute units)
 @pytest.mark.parametrize("T,V,k,r", [(520, 11016, 136, 16), (2100, 4001, 264, 0), (700, 24008, 72, 4), (1025, 16385, 72, 0)])
 def test_large_tiles_against_64_bits(dev, T, V, k, r):
