@@ -55,8 +55,7 @@ class AdamW:
                 continue
             if self.state[i] is None:
                 self.state[i] = self._fresh(p)
-            self.state[i]["step"] += 1
-            calls.setdefault((p.dtype, p.grad.dtype, p.device, self.state[i]["step"]), []).append(i)
+            calls.setdefault((p.dtype, p.grad.dtype, p.device, self.state[i]["step"] + 1), []).append(i)
         for n, ((_, _, _, t), at) in enumerate(calls.items()):
             s = [self.state[i] for i in at]
             eight = self.state_bits == 8
@@ -67,6 +66,8 @@ class AdamW:
                                 eps=self.eps, weight_decay=self.weight_decay,
                                 M_scales=[x["M_scale"] for x in s] if eight else None,
                                 V_scales=[x["V_scale"] for x in s] if eight else None, grad_scale=grad_scale)
+            for x in s:  # (a refused call raises before this)
+                x["step"] = t
 
     def zero_grad(self, set_to_none: bool = True) -> None:
         for p in self.params:

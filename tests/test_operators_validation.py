@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from rank_randomized_gradient_amd import rgc
+from rank_randomized_gradient_amd.adamw import AdamW
 
 OK, NULL, SHAPE, UNSUP, ALIGN, WS, VALUE = 0, 1, 2, 3, 4, 5, 7
 FAKE = 0x10000  # an aligned address that is never dereferenced
@@ -148,3 +149,14 @@ def test_the_binding_refuses_cpu_tensors_and_mismatched_lists():
         with pytest.raises(rgc.RgcError):
             call()
     assert rgc.rgc_adamw_batch([], [], [], [], 1e-3, 1) == []
+
+
+def test_a_refused_step_is_not_counted():
+    """A parameter's step count sets its bias corrections: it counts the updates made, not the calls refused."""
+    p = torch.nn.Parameter(torch.ones(8))
+    p.grad = torch.ones(8)
+    opt = AdamW([p])
+    for _ in range(2):
+        with pytest.raises(rgc.RgcError):
+            opt.step()  # a CPU tensor
+    assert opt.state[0] is None or opt.state[0]["step"] == 0
