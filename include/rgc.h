@@ -396,11 +396,10 @@ rgc_status_t rgc_linear_backward(const uint16_t* D, int64_t ldd, const uint16_t*
  * Backward, from grad[t] = dL/dloss[t] and the forward's lse:
  *   D_tv = grad[t] (exp(z_tv - lse[t]) - [v = targets[t]]), 0 for an ignored
  *   token, formed from z again for one piece of the vocabulary after another;
- *   dX = bf16(D W): T x k, row stride lddx, overwritten; each piece's D rounded
- *   to bf16, the pieces added in fp32;
- *   C += D^T XP with r > 0: V x r fp32, only added to as by rgc_accumulate, D in
- *   fp32 or as two bf16 terms (hi + lo, 2^-18 relative) and the targets' entries
- *   in fp32, so that C's error is that of fp32 sums.
+ *   dX = bf16(D W): T x k, row stride lddx, overwritten; the pieces added in fp32;
+ *   C += D^T XP with r > 0: V x r fp32, only added to as by rgc_accumulate.
+ *   In both D is held in fp32 or as two bf16 terms (hi + lo, off by 2^-17 of D at
+ *   most), the targets' entries in fp32.
  *   C is what rgc_apply turns into the head's update. r = 0 (XP and C may then
  *   be NULL) is a frozen head: dX alone. With r > 0 dX may be NULL (an input
  *   that needs no gradient): C alone.

@@ -69,8 +69,12 @@ struct GtTile {
 
   // m_rem, n_rem: rows of A and columns of the product that exist (>= 1); what
   // lies behind them is read from the last one and must not be used.
+  // PAIRED: the tile takes kRows / 2 rows of A and the same rows of a second matrix
+  // `second` elements behind it. A wave's first half of its rows comes from A, the
+  // other from the second, so that acc[mt] and acc[mt + MH] belong together.
+  template <bool PAIRED = false>
   __device__ __forceinline__ void init(const uint16_t* A_, int64_t lda, const uint16_t* B_, int64_t ldb_, int64_t m_rem,
-                                       int64_t n_rem, int64_t K_, char* smem) {
+                                       int64_t n_rem, int64_t K_, char* smem, int64_t second = 0) {
     A = A_, B = B_, ldb = ldb_, K = K_;
     nsteps = (K + kGtStep - 1) / kGtStep;
     lane = threadIdx.x & 63;
@@ -85,9 +89,14 @@ struct GtTile {
       if (of_a || !BKM) {
         // eight rows of 128 bytes; lane l fills slot l % 8 of row l / 8
         const int64_t last = (of_a ? m_rem : n_rem) - 1;
-        int64_t row = 8 * c + (lane >> 3);
+        int64_t row = 8 * c + (lane >> 3), from = 0;
+        if (PAIRED && of_a) {
+          const int in_wave = (int)row % (16 * MI);
+          from = in_wave >= 16 * MH ? second : 0;
+          row = 16 * MH * (row / (16 * MI)) + in_wave % (16 * MH);
+        }
         row = row < last ? row : last;
-        voff[v] = (uint32_t)((row * (of_a ? lda : ldb) + 8 * chunk()) * 2);
+        voff[v] = (uint32_t)((from + row * (of_a ? lda : ldb) + 8 * chunk()) * 2);
       } else if (v == kCopiesA) {
         int64_t col = column(c);
         col = col + 8 <= n_rem ? col : n_rem - 8;

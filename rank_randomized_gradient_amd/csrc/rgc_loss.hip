@@ -13,21 +13,26 @@
 // maxima and sums of exponentials; a second launch joins the tiles of a row.
 // Backward: the vocabulary goes by in pieces. A piece's D is formed from z
 // again (z costs 2 T V k operations a second time; keeping it would cost 2 T V
-// bytes and more), written in bf16 to the workspace, and used twice from
-// there while it is in the last-level cache: D W, added to dX in fp32, and
-// D^T XP, added to the sketch by the sketch's own accumulation.
+// bytes and more), written to the workspace, and used twice from there while it
+// is in the last-level cache: D W, added to dX in fp32, and D^T XP, added to the
+// sketch by the sketch's own accumulation.
 //
-// The sketch is fp32, and a D rounded once to bf16 would put an error of 2^-9
-// into each of its terms. So with a sketch D is kept as two bf16 terms,
-// D = hi + lo (error 2^-18), stacked along the tokens: C += [hi; lo]^T [XP; XP]
-// is one accumulation over 2 T tokens. dX is rounded to bf16 itself and takes
-// hi alone. The targets' entries are by far the largest of D (of the order of
-// g, the others of g / V), so what the terms leave of them is kept in fp32, one
-// value a token, and added where it costs little: rest_t W_y(t) to dX when it is
+// D is kept as two bf16 terms, D = hi + lo (each rounding leaves at most 2^-8 of
+// what it rounds, so the pair is off by 2^-17 of D at most), and both products
+// take both. One term would do where the softmax is flat, but not for a token
+// whose mass lies on a few entries with rows of W near each other: their large
+// entries of D cancel in dX, and 2^-8 of each does not (D of +-1/2 on two rows 5%
+// apart: dX off by up to 8% in one term, by its own rounding in two). A tile of
+// dX takes 128 tokens, their hi and lo as its 256 rows, and adds the two halves
+// of its sums in its registers. For the sketch the terms are stacked along the
+// tokens: C += [hi; lo]^T [XP; XP] is one accumulation over 2 T tokens.
+// What the terms leave of the targets' entries, by far the largest of a flat
+// softmax's D (of the order of g, the others of g / V), is kept in fp32, one value
+// a token, and added where it costs little: rest_t W_y(t) to dX when it is
 // rounded, and rest_t XP_t to C's row y(t) in a last launch. Up to 128 tokens
 // one tile holds them all, and adds its rows of the sketch itself, from D in fp32.
 //
-// Bound by MFMA: 2 T V k operations for the loss, 6 T V k + 4 T V r for the
+// Bound by MFMA: 2 T V k operations for the loss, 6 T V k + 4 T V r more for the
 // gradient. Where dX has few tiles (few tokens), each is split over K among
 // several workgroups, which add into slabs of their own; a last launch adds
 // the slabs and rounds. All sums have a fixed order.
@@ -63,9 +68,8 @@ struct CeArgs {
   const float* lse;    // backward
   const float* grad;
   uint16_t* hi;        // backward: T x ldd, bf16
-  uint16_t* lo;        // or null: no sketch
-  float* rest;         // D - hi at each token's target
-  float* rest_sketch;  // with lo: D - hi - lo there
+  uint16_t* lo;        // or null: nothing takes D from here
+  float* rest;         // with lo: D - hi - lo at each token's target
   int64_t ldd;
   float* C;            // few tokens: the sketch's rows of the piece, added to here; else null
   const uint16_t* XP;
@@ -259,10 +263,11 @@ __device__ __forceinline__ void sketch_tile(const CeArgs& a, const Tile& t, int6
   __syncthreads();
 }
 
-// A piece's D, hi (and lo): T x ldd, zero in the columns behind the piece.
+// A piece's D, hi and lo: T x ldd each, zero in the columns behind the piece.
 // The tile's bf16 values are laid out in LDS first, so that they are stored in
 // whole rows (16-byte chunk q of row t at place q ^ (t % 16)). The
-// lo pass forms D - hi from the fp32 values, which stay in the registers.
+// lo pass forms D - hi from the fp32 values, which stay in the registers. Without
+// lo (a fused sketch and no dX) nothing is stored.
 template <int MI, int NI, int STAGES>
 __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, char* smem, CeRows* rows) {
   typedef GtTile<MI, NI, STAGES, false> Tile;
@@ -305,6 +310,7 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
   if constexpr (MI <= 4 && STAGES > 2) {  // (two stages leave no LDS for it)
     if (a.C) sketch_tile<MI, NI>(a, t, n0, width, smem, rows);
   }
+  if (!a.lo) return;
   RGC_LDS char* lds = (RGC_LDS char*)smem;
   uint32_t to[NI];  // this lane's places in the row of mt = 0
 #pragma unroll
@@ -313,9 +319,8 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
   const int row0 = threadIdx.x / kRowChunks, q = (threadIdx.x % kRowChunks) ^ (row0 & 15);
   constexpr int kRowsAtOnce = kGtThreads / kRowChunks;  // a multiple of 16: q holds for every pass
   static_assert(kRowsAtOnce % 16 == 0, "rows of a pass");
-  const int terms = a.lo ? 2 : 1;
 #pragma unroll 1
-  for (int term = 0; term < terms; ++term) {
+  for (int term = 0; term < 2; ++term) {
     if (term) __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < MI; ++mt)
@@ -328,17 +333,17 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
                                     __uint_as_float(h.y << 16), __uint_as_float(h.y & 0xFFFF0000u)};
         *(RGC_LDS u32x2v_t*)(lds + to[nt] + 256 * kRowChunks * mt) = h;
       }
-    // what is left of the targets' entries: after hi for dX, after lo for the sketch
-    float* rest = term ? a.rest_sketch : a.rest;
+    if (term) {  // what the terms leave of the targets' entries
 #pragma unroll
-    for (int mt = 0; mt < MI; ++mt) {
-      const int row = 16 * MI * wm + 16 * mt + li, at = rows->at[row] - first;
-      if (__any(at >= 0 && at < 16 * NI)) {
+      for (int mt = 0; mt < MI; ++mt) {
+        const int row = 16 * MI * wm + 16 * mt + li, at = rows->at[row] - first;
+        if (__any(at >= 0 && at < 16 * NI)) {
 #pragma unroll
-        for (int nt = 0; nt < NI; ++nt)
+          for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (16 * nt + e == at) rest[m0 + row] = t.acc[mt][nt][e];
+            for (int e = 0; e < 4; ++e)
+              if (16 * nt + e == at) a.rest[m0 + row] = t.acc[mt][nt][e];
+        }
       }
     }
     __syncthreads();
@@ -433,7 +438,7 @@ __global__ __launch_bounds__(256) void ce_rest_kernel(const int64_t* targets, co
 }
 
 struct DxArgs {
-  const uint16_t* D;  // T x ldd, the piece's hi terms
+  const uint16_t* D;  // T x ldd, the piece's hi terms; the lo terms follow
   const uint16_t* W;  // the piece's first row
   int64_t ldd, ldw;
   int64_t T, K, k;    // K: rows of the piece
@@ -457,6 +462,11 @@ __device__ __forceinline__ float rest_of(const DxArgs& a, int64_t t, const uint1
   return live ? a.rest[t] : 0.f;
 }
 
+// Tokens of a tile of dX, two rows each (hi and lo). What the second term costs:
+// loss and gradient of 4096 x 131072 x 4096 at r = 128 11.5 ms with hi alone, 15.1
+// with both; 1001 x 50001 x 2048 frozen 594 and 776 us.
+constexpr int kDxTokens = kGtTile / 2;
+
 __global__ __launch_bounds__(kGtThreads, 1) void ce_dx_kernel(DxArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[GtTile<8, 4, 2, true>::kLds];
   const int64_t tiles = a.mtiles * a.ntiles;
@@ -464,18 +474,19 @@ __global__ __launch_bounds__(kGtThreads, 1) void ce_dx_kernel(DxArgs a) {
   const int64_t split = place / tiles;
   int64_t i, j;
   gt_place(place - split * tiles, a.mtiles, a.ntiles, kCeDown, &i, &j);
-  const int64_t m0 = i * kGtTile, n0 = j * kGtTile;
+  const int64_t m0 = i * kDxTokens, n0 = j * kGtTile;
   const int64_t k0 = split * a.steps * kGtStep;
   const int64_t K = a.K - k0 < a.steps * kGtStep ? a.K - k0 : a.steps * kGtStep;
   GtTile<8, 4, 2, true> t;
-  t.init(a.D + m0 * a.ldd + k0, a.ldd, a.W + k0 * a.ldw + n0, a.ldw, a.T - m0, a.k - n0, K, smem);
+  // (hi and lo are 2^28 bytes at most together, so their distance fits a copy's 32-bit offset)
+  t.init<true>(a.D + m0 * a.ldd + k0, a.ldd, a.W + k0 * a.ldw + n0, a.ldw, a.T - m0, a.k - n0, K, smem, a.T * a.ldd);
   if (K > 0) t.run();
 
   const int g = t.lane >> 4, li = t.lane & 15, wm = t.wave & 1, wn = t.wave >> 1;
   float* slab = a.slab ? a.slab + split * a.T * a.k : nullptr;
 #pragma unroll
-  for (int mt = 0; mt < 8; ++mt) {
-    const int64_t row = m0 + 128 * wm + 16 * mt + li;
+  for (int mt = 0; mt < 4; ++mt) {
+    const int64_t row = m0 + 64 * wm + 16 * mt + li;
     if (row >= a.T) continue;
     const uint16_t* wy = nullptr;
     const float rest = a.dX ? rest_of(a, row, &wy) : 0.f;
@@ -483,7 +494,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void ce_dx_kernel(DxArgs a) {
     for (int nt = 0; nt < 4; ++nt) {
       const int64_t col = n0 + 64 * wn + 16 * nt + 4 * g;
       if (col >= a.k) continue;  // k is a multiple of 8: four columns are all in or all out
-      f32x4_t v = t.acc[mt][nt];
+      f32x4_t v = t.acc[mt][nt] + t.acc[mt + 4][nt];
       if (!a.first) v += *reinterpret_cast<const f32x4_t*>(slab + row * a.k + col);
       if (a.dX) {
         if (rest != 0.f) {
@@ -560,6 +571,7 @@ __global__ __launch_bounds__(256) void ce_xp_kernel(const uint2* XP, const int64
 }
 
 int64_t tiles_of(int64_t n) { return (n + kGtTile - 1) / kGtTile; }
+int64_t dx_rows(int64_t T) { return (T + kDxTokens - 1) / kDxTokens; }  // rows of tiles of dX
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Whether the logits take 64-row tiles, and whether one tile holds all tokens.
@@ -643,9 +655,8 @@ struct Plan {
 Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
   Plan p{};
   p.fused = r > 0 && one_tile(T);
-  const int64_t terms = r > 0 && !p.fused ? 2 : 1;
-  // a piece's D fills the 256 MB last-level cache at most
-  int64_t piece = (int64_t(256) << 20) / (T * 2 * terms) / kGtTile * kGtTile;
+  // a piece's D, two terms, fills the 256 MB last-level cache at most
+  int64_t piece = (int64_t(256) << 20) / (T * 4) / kGtTile * kGtTile;
   if (piece < 1024) piece = 1024;
   if (piece > kMaxTiledDim) piece = kMaxTiledDim;
   p.pieces = (V + piece - 1) / piece;
@@ -654,7 +665,7 @@ Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
   // as many splits as take the least time: rounds of tiles on the compute units
   // (4.7 TFLOP/s each with all at work), and the slabs' way to memory and back
   // at 4 TB/s. At least four steps to a split.
-  const int64_t tiles = tiles_of(T) * tiles_of(k), cus = device_compute_units();
+  const int64_t tiles = dx_rows(T) * tiles_of(k), cus = device_compute_units();
   const int64_t steps = (p.piece + kGtStep - 1) / kGtStep;
   double best = 1e30;
   p.splits = 1;
@@ -665,11 +676,11 @@ Plan plan_of(int64_t T, int64_t V, int64_t k, int64_t r) {
     if (cost < best) best = cost, p.splits = s;
   }
   p.stacked = 2 * T <= kMaxTiledDim;
-  p.d = up256((size_t)(terms * T * p.piece) * 2);
+  p.d = up256((size_t)(T * p.piece) * 4);
   p.xp = r > 0 && !p.fused ? up256((size_t)((p.stacked ? 2 : 1) * T * r) * 2) : 0;
-  p.rest = up256((size_t)T * 4) * terms;
+  p.rest = up256((size_t)T * 4);
   p.slab = p.pieces > 1 || p.splits > 1 ? up256((size_t)(p.splits * T * k) * 4) : 0;
-  if (terms == 2) {
+  if (r > 0 && !p.fused) {
     // every width the pieces have: the whole ones and the last
     const int64_t tokens = p.stacked ? 2 * T : T, last = V - (p.pieces - 1) * p.piece;
     const size_t a = rgc_accumulate_workspace_size(tokens, p.piece, r), b = rgc_accumulate_workspace_size(tokens, last, r);
@@ -784,15 +795,14 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
   a.X = X, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = T, a.vocab = V, a.k = k;
   a.lse = lse, a.grad = grad;
   a.rest = reinterpret_cast<float*>(at + p.d + p.xp);
-  a.rest_sketch = a.rest + up256((size_t)T * 4) / 4;
   DxArgs x{};
-  x.ldw = ldw, x.T = T, x.k = k, x.mtiles = tiles_of(T), x.ntiles = tiles_of(k), x.slab = slab, x.lddx = lddx;
+  x.ldw = ldw, x.T = T, x.k = k, x.mtiles = dx_rows(T), x.ntiles = tiles_of(k), x.slab = slab, x.lddx = lddx;
   x.V0 = W, x.targets = targets, x.rest = a.rest, x.vocab = V;
   for (int64_t q = 0; q < p.pieces; ++q) {
     const int64_t v0 = q * p.piece, rows = V - v0 < p.piece ? V - v0 : p.piece;
     a.W = W + v0 * ldw, a.V = rows, a.v0 = v0;
     a.ldd = tiles_of(rows) * kGtTile;
-    a.hi = D, a.lo = accumulate ? D + T * a.ldd : nullptr;
+    a.hi = D, a.lo = dX || accumulate ? D + T * a.ldd : nullptr;
     if (p.fused) a.C = C + v0 * r, a.XP = XP, a.r = (int)r;
     if ((st = logits_launch<true>(a, s)) != RGC_OK) return st;
     if (dX) {
@@ -814,7 +824,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
     }
   }
   if (accumulate) {
-    hipLaunchKernelGGL(ce_rest_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, targets, a.rest_sketch, XP, C, T, V,
+    hipLaunchKernelGGL(ce_rest_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, targets, a.rest, XP, C, T, V,
                        (int)r);
     if ((st = launched()) != RGC_OK) return st;
   }
