@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define RGC_ABI_VERSION 7
+#define RGC_ABI_VERSION 8
 
 typedef enum {
   RGC_OK = 0,
@@ -468,14 +468,27 @@ rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_d
  * sqrt(v) as e4m3 bytes in units of a scale per block of 128 elements,
  * Mscales[i] and Vscales[i], float[(numels[i] + 127) / 128]: the power of two
  * (at least 2^-126) that brings the block's largest finite magnitude into 128
- * .. 256. m is rounded to nearest, sqrt(v) stochastically (with the other half
- * of the word), never to zero unless it is zero; an infinite or NaN moment
- * becomes a NaN byte and does not count for the scale. All states start as
- * zero bytes. Mscales and Vscales may be NULL with 32 bits.
+ * .. 256. sqrt(v) is rounded stochastically (with the other half of the word),
+ * never to zero unless it is zero; an infinite or NaN moment becomes a NaN byte
+ * and does not count for the scale. All states start as zero bytes. Mscales and
+ * Vscales may be NULL with 32 bits.
+ * m in 8 bits: with RGC_ADAMW_STOCHASTIC_M rounded stochastically too (with half
+ * e%2 of word ((e%8)/2 + 1) % 4), so that its mean follows the formula at any beta1.
+ * Without the flag (rgc_adamw_batch) rounded to nearest, for beta1 up to 0.9 only
+ * (RGC_ERR_VALUE above, where it would no longer decay): m then stops short of a
+ * constant gradient, at 0.6 to 0.8 of it for beta1 = 0.9, and an element whose
+ * gradients end while its block's go on keeps up to 2^-14 of the block's largest m.
  * Arrays are HOST arrays of n entries, n without limit (48 tensors a launch);
  * parameters, gradients and moments 16-byte aligned, at most 2^34 elements. A
  * tensor may be listed once only. RGC_ERR_VALUE: step < 1, a beta outside
  * [0, 1), eps below 2^-126 (as fp32), or a scalar that is not finite. */
+typedef enum { RGC_ADAMW_STOCHASTIC_M = 1 } rgc_adamw_flags_t;
+
+rgc_status_t rgc_adamw_batch_with(unsigned flags, int64_t n, rgc_dtype_t pt, rgc_dtype_t gt, int state_bits,
+                                  void* const* Ps, const void* const* Gs, void* const* Ms, void* const* Vs,
+                                  float* const* Mscales, float* const* Vscales, const int64_t* numels, double lr,
+                                  double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                                  const float* grad_scale, uint64_t seed, void* stream);
 rgc_status_t rgc_adamw_batch(int64_t n, rgc_dtype_t pt, rgc_dtype_t gt, int state_bits, void* const* Ps,
                              const void* const* Gs, void* const* Ms, void* const* Vs, float* const* Mscales,
                              float* const* Vscales, const int64_t* numels, double lr, double beta1, double beta2,

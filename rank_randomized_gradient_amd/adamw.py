@@ -13,7 +13,7 @@ class AdamW:
     """step() updates every parameter that has a gradient, in place.
 
     state_bits 8 holds both moments as e4m3 with a scale per 128 elements (2.06
-    bytes an element), 32 as float32 (8 bytes). `seed` and the count of steps
+    bytes an element), rounded stochastically, 32 as float32 (8 bytes). `seed` and the count of steps
     give the rounding bits, so a run repeats bit for bit. Parameters and
     gradients are contiguous bf16 or float32 tensors. The step count and the
     rounding key are host values: a step captured into a graph would repeat
@@ -65,7 +65,8 @@ class AdamW:
                                 [x["V"] for x in s], self.lr, t, seed=key, beta1=self.betas[0], beta2=self.betas[1],
                                 eps=self.eps, weight_decay=self.weight_decay,
                                 M_scales=[x["M_scale"] for x in s] if eight else None,
-                                V_scales=[x["V_scale"] for x in s] if eight else None, grad_scale=grad_scale)
+                                V_scales=[x["V_scale"] for x in s] if eight else None, grad_scale=grad_scale,
+                                m_rounding="stochastic")
             for x in s:  # (a refused call raises before this)
                 x["step"] = t
 

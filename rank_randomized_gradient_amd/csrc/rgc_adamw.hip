@@ -12,13 +12,20 @@
 // power-of-two scale each, chosen so that the block's largest finite magnitude
 // lies in 128 .. 256 units (below e4m3's largest, 448). Powers of two make the
 // scaling exact, so the only error is the rounding to four significant bits.
-// m changes by up to 1 - b1 of itself a step, of the order of e4m3's step, and
-// is rounded to nearest. sqrt(v) changes by at most (1 - b2) / 2 of itself
-// while the gradient is small, far below half a step: rounded to nearest it
-// would never decay, so it is rounded stochastically. What is not zero never
-// rounds to zero, since a zero sqrt(v) under a momentum that is not zero
-// would leave eps alone to divide by. Infinities and NaN become NaN codes and
-// are left out of the scale: they spoil their own elements only.
+// A moment that moves by less than half a step of its code stands still if it is
+// rounded to nearest, whatever moves it. sqrt(v) changes by at most (1 - b2) / 2
+// of itself while the gradient is small, and so would never decay: it is rounded
+// stochastically. m changes by up to 1 - b1 of itself, and half a step is 1/30 to
+// 1/16 of it: at b1 = 0.9 a block of zero gradients still decays to nothing, at
+// 0.95 it does not, and m / sqrt(v) of a parameter that should stand still grows
+// without end; under a constant gradient m stops short of it, at 0.72 of it for b1 =
+// 0.9, 0.54 for 0.95, 0.19 for 0.99 (means over random gradients). So m is rounded
+// stochastically too (STOCHASTIC), which keeps its mean. Rounding it to nearest is
+// the other form, up to b1 = 0.9; there an element whose gradients end beside live
+// ones keeps four subnormal steps of its block, 2^-14 of the block's largest.
+// A sqrt(v) that is not zero never rounds to zero, since a zero one under a
+// momentum that is not zero would leave eps alone to divide by. Infinities and NaN
+// become NaN codes and are left out of the scale: they spoil their own elements only.
 //
 // Bound by memory: 2 p + g + 16 bytes an element in fp32 states, 2 p + g + 4
 // in 8 bits (10 bytes for bf16). 134M bf16 parameters with 8-bit states take 241
@@ -27,9 +34,9 @@
 // element checked for NaN the 8-bit step took 283 us, bound by instructions.
 // Eight consecutive elements to a thread, so
 // one Philox call (128 bits) serves the thread: element j of the eight takes
-// half j % 2 of word j / 2 for its parameter and the other half, its
-// neighbour's, for its second moment, which makes an element's two rounding
-// errors independent of each other. A block of 128 is sixteen lanes, so its
+// half j % 2 of word j / 2 for its parameter, the other half, its neighbour's, for
+// its second moment and half j % 2 of the next word (the first after the last) for
+// its first, which makes an element's rounding errors independent of each other. A block of 128 is sixteen lanes, so its
 // maxima are lane rotations within a row of sixteen.
 #include <math.h>
 
@@ -173,7 +180,31 @@ __device__ __forceinline__ uint32_t unit_exponent(uint32_t top) {
   return (uint32_t)(e < 1 ? 1 : e);
 }
 
-template <typename PT, typename GT, bool EIGHT>
+// Eight numbers of magnitude below 256 rounded to e4m3 values with the 16 random
+// bits r[j] each: three bits of mantissa, the 20 below them rounded by the random
+// ones (a carry goes up through the magnitude; the sign bit is out of reach).
+// e4m3's subnormals have the step of its smallest normal numbers, 2^-9, so what
+// lies below 2^-6 is rounded lifted by that much, where fp32 truncates at that
+// step. Whether a lane of the wave held such a number.
+__device__ __forceinline__ bool round_codes(float (&q)[8], const uint32_t (&r)[8]) {
+  bool small = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) small |= !(fabsf(q[j]) >= 0.015625f);
+  if (__any(small)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = fabsf(q[j]), lift = x < 0.015625f ? 0.015625f : 0.f;
+      const float y = __uint_as_float((__float_as_uint(x + lift) + (r[j] << 4)) & 0xFFF00000u) - lift;
+      q[j] = copysignf(y, q[j]);
+    }
+    return true;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j] = __uint_as_float((__float_as_uint(q[j]) + (r[j] << 4)) & 0xFFF00000u);
+  return false;
+}
+
+template <typename PT, typename GT, bool EIGHT, bool STOCHASTIC>
 __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs a) {
   const float scale = a.scale ? *a.scale : 1.f;
   if (!finite(scale)) return;  // gradients that overflowed: the step is skipped
@@ -267,31 +298,19 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs a) {
     const uint32_t me = unit_exponent(row_max(mt)), ve = unit_exponent(row_max(vt));
     const float im = __uint_as_float((254u - me) << 23), iv = __uint_as_float((254u - ve) << 23);  // 1 / unit
     float qm[8], qv[8];
-    bool small = false;
+    uint32_t rm[8], rv[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       qm[j] = m[j] * im;
       qv[j] = root[j] * iv;
-      small |= !(qv[j] >= 0.015625f);
+      const uint32_t next = word[(j / 2 + 1) & 3];
+      rm[j] = j & 1 ? next >> 16 : next & 0xFFFFu;
+      rv[j] = j & 1 ? word[j / 2] & 0xFFFFu : word[j / 2] >> 16;
     }
-    // sqrt(v): three bits of mantissa, the 20 below them rounded by 16 random
-    // bits. e4m3's subnormals have the step of its smallest normal numbers,
-    // 2^-9, so what lies below 2^-6 is rounded lifted by that much, where fp32
-    // truncates at that step.
-    if (__any(small)) {
+    if constexpr (STOCHASTIC) round_codes(qm, rm);
+    if (round_codes(qv, rv)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t r = j & 1 ? word[j / 2] & 0xFFFFu : word[j / 2] >> 16;
-        const float x = qv[j], lift = x < 0.015625f ? 0.015625f : 0.f;
-        const float y = __uint_as_float((__float_as_uint(x + lift) + (r << 4)) & 0xFFF00000u) - lift;
-        qv[j] = x > 0.f ? fmaxf(y, 0.001953125f) : 0.f;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t r = j & 1 ? word[j / 2] & 0xFFFFu : word[j / 2] >> 16;
-        qv[j] = __uint_as_float((__float_as_uint(qv[j]) + (r << 4)) & 0xFFF00000u);
-      }
+      for (int j = 0; j < 8; ++j) qv[j] = root[j] > 0.f ? fmaxf(qv[j], 0.001953125f) : 0.f;
     }
     if (wild) {
 #pragma unroll
@@ -314,10 +333,11 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs a) {
 }
 
 template <typename PT, typename GT>
-void launch(const AdamArgs& a, bool eight, hipStream_t s) {
+void launch(const AdamArgs& a, bool eight, bool stochastic, hipStream_t s) {
   const dim3 grid(a.base[a.count]);
-  if (eight) hipLaunchKernelGGL((adamw_kernel<PT, GT, true>), grid, dim3(kAdamThreads), 0, s, a);
-  else hipLaunchKernelGGL((adamw_kernel<PT, GT, false>), grid, dim3(kAdamThreads), 0, s, a);
+  if (!eight) hipLaunchKernelGGL((adamw_kernel<PT, GT, false, false>), grid, dim3(kAdamThreads), 0, s, a);
+  else if (stochastic) hipLaunchKernelGGL((adamw_kernel<PT, GT, true, true>), grid, dim3(kAdamThreads), 0, s, a);
+  else hipLaunchKernelGGL((adamw_kernel<PT, GT, true, false>), grid, dim3(kAdamThreads), 0, s, a);
 }
 
 bool dtype_ok(rgc_dtype_t t) { return t == RGC_BF16 || t == RGC_F32; }
@@ -327,17 +347,22 @@ bool dtype_ok(rgc_dtype_t t) { return t == RGC_BF16 || t == RGC_F32; }
 
 using namespace rgc;
 
-extern "C" rgc_status_t rgc_adamw_batch(int64_t n, rgc_dtype_t pt, rgc_dtype_t gt, int state_bits, void* const* Ps,
-                                        const void* const* Gs, void* const* Ms, void* const* Vs, float* const* Mscales,
-                                        float* const* Vscales, const int64_t* numels, double lr, double beta1,
-                                        double beta2, double eps, double weight_decay, int64_t step,
-                                        const float* grad_scale, uint64_t seed, void* stream) {
+extern "C" rgc_status_t rgc_adamw_batch_with(unsigned flags, int64_t n, rgc_dtype_t pt, rgc_dtype_t gt, int state_bits,
+                                             void* const* Ps, const void* const* Gs, void* const* Ms, void* const* Vs,
+                                             float* const* Mscales, float* const* Vscales, const int64_t* numels,
+                                             double lr, double beta1, double beta2, double eps, double weight_decay,
+                                             int64_t step, const float* grad_scale, uint64_t seed, void* stream) {
   if (n < 0) return RGC_ERR_SHAPE;
-  if (!dtype_ok(pt) || !dtype_ok(gt) || (state_bits != 8 && state_bits != 32) || n > INT32_MAX) return RGC_ERR_UNSUPPORTED;
+  if (!dtype_ok(pt) || !dtype_ok(gt) || (state_bits != 8 && state_bits != 32) || n > INT32_MAX ||
+      (flags & ~(unsigned)RGC_ADAMW_STOCHASTIC_M))
+    return RGC_ERR_UNSUPPORTED;
+  const bool stochastic = (flags & RGC_ADAMW_STOCHASTIC_M) != 0;
   // scalars that would divide by zero or give values that are not finite for finite inputs
   if (!(fabs(lr) <= 1e30) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps <= 1e30) ||
       !((float)eps >= 0x1p-126f) || !(fabs(weight_decay) <= 1e30) || step < 1)
     return RGC_ERR_VALUE;
+  // a first moment that rounding to nearest would hold in place
+  if (state_bits == 8 && !stochastic && beta1 > 0.9) return RGC_ERR_VALUE;
   if (n == 0) return RGC_OK;
   const bool eight = state_bits == 8;
   if (!Ps || !Gs || !Ms || !Vs || !numels || (eight && (!Mscales || !Vscales))) return RGC_ERR_NULL;
@@ -378,13 +403,22 @@ extern "C" rgc_status_t rgc_adamw_batch(int64_t n, rgc_dtype_t pt, rgc_dtype_t g
     a.base[a.count] = (uint32_t)groups;
     if (groups == 0) continue;
     if (pt == RGC_F32) {
-      if (gt == RGC_F32) launch<float, float>(a, eight, s);
-      else launch<float, uint16_t>(a, eight, s);
+      if (gt == RGC_F32) launch<float, float>(a, eight, stochastic, s);
+      else launch<float, uint16_t>(a, eight, stochastic, s);
     } else {
-      if (gt == RGC_F32) launch<uint16_t, float>(a, eight, s);
-      else launch<uint16_t, uint16_t>(a, eight, s);
+      if (gt == RGC_F32) launch<uint16_t, float>(a, eight, stochastic, s);
+      else launch<uint16_t, uint16_t>(a, eight, stochastic, s);
     }
     if (hipGetLastError() != hipSuccess) return RGC_ERR_HIP;
   }
   return RGC_OK;
+}
+
+extern "C" rgc_status_t rgc_adamw_batch(int64_t n, rgc_dtype_t pt, rgc_dtype_t gt, int state_bits, void* const* Ps,
+                                        const void* const* Gs, void* const* Ms, void* const* Vs, float* const* Mscales,
+                                        float* const* Vscales, const int64_t* numels, double lr, double beta1,
+                                        double beta2, double eps, double weight_decay, int64_t step,
+                                        const float* grad_scale, uint64_t seed, void* stream) {
+  return rgc_adamw_batch_with(0, n, pt, gt, state_bits, Ps, Gs, Ms, Vs, Mscales, Vscales, numels, lr, beta1, beta2, eps,
+                              weight_decay, step, grad_scale, seed, stream);
 }

@@ -49,6 +49,8 @@ _DTYPES = {torch.bfloat16: RGC_BF16, torch.float32: RGC_F32}
 _TYPE_NAMES = {"BFloat16": RGC_BF16, "Float": RGC_F32}
 RGC_NORM_LAYER = 0
 RGC_NORM_RMS = 1
+RGC_ADAMW_STOCHASTIC_M = 1
+_M_ROUNDINGS = {"nearest": 0, "stochastic": RGC_ADAMW_STOCHASTIC_M}
 _NORMS = {"layer": RGC_NORM_LAYER, "rms": RGC_NORM_RMS}
 ADAMW_BLOCK = 128  # elements of an 8-bit state that share a scale
 
@@ -124,6 +126,10 @@ SIGNATURES = {
     "rgc_layer_norm_backward_workspace_size": (_sz, [_i64, _i64]),
     "rgc_layer_norm_backward": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _vp,
                                                _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "rgc_adamw_batch_with": (ctypes.c_int, [ctypes.c_uint, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                            ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_vp),
+                                            ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_vp),
+                                            ctypes.POINTER(_i64), _f64, _f64, _f64, _f64, _f64, _i64, _vp, _u64, _vp]),
     "rgc_adamw_batch": (ctypes.c_int, [_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(_vp),
                                        ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_vp),
                                        ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_i64), _f64, _f64, _f64,
@@ -871,14 +877,19 @@ def _adamw_list(ts, name: str, types, sizes, block: int = 1):
 
 def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: float = 0.9, beta2: float = 0.999,
                     eps: float = 1e-8, weight_decay: float = 0.0, M_scales=None, V_scales=None,
-                    grad_scale: torch.Tensor | None = None):
+                    grad_scale: torch.Tensor | None = None, m_rounding: str = "nearest"):
     """One AdamW step, in place, over lists of parameters Ps and gradients Gs
     (each list bf16 or float32) with moments Ms and Vs: float32, or
     float8_e4m3fn with M_scales and V_scales (float32, one per 128 elements; Vs
     then holds square roots). `step` counts from 1; bf16 parameters and 8-bit
     second moments are rounded stochastically from `seed`. grad_scale: a device
-    float32 that multiplies every gradient; one that is not finite skips the step."""
+    float32 that multiplies every gradient; one that is not finite skips the step.
+    m_rounding: of 8-bit first moments, "stochastic" (their mean follows the
+    formula at any beta1) or "nearest" (beta1 up to 0.9 only: they stop short of a
+    steady gradient, by a quarter or so)."""
     lib = load_library()
+    if m_rounding not in _M_ROUNDINGS:
+        raise RgcError('m_rounding must be "nearest" or "stochastic"')
     n = len(Ps)
     eight = M_scales is not None or V_scales is not None
     lists = [Gs, Ms, Vs] + ([M_scales, V_scales] if eight else [])
@@ -906,10 +917,11 @@ def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: 
         if grad_scale.numel() != 1:
             raise RgcError("grad_scale must be one float32")
     with _on(dev):
-        _check(lib.rgc_adamw_batch(n, _TYPE_NAMES[given[0][2]], _TYPE_NAMES[given[1][2]], 8 if eight else 32, pp, gp, mp,
-                                   vp, msp, vsp, (_i64 * n).from_buffer_copy(sizes), lr, beta1, beta2, eps, weight_decay, step,
-                                   grad_scale.data_ptr() if grad_scale is not None else None,
-                                   seed & 0xFFFFFFFFFFFFFFFF, _stream(dev)))
+        _check(lib.rgc_adamw_batch_with(_M_ROUNDINGS[m_rounding], n, _TYPE_NAMES[given[0][2]], _TYPE_NAMES[given[1][2]],
+                                        8 if eight else 32, pp, gp, mp, vp, msp, vsp, (_i64 * n).from_buffer_copy(sizes),
+                                        lr, beta1, beta2, eps, weight_decay, step,
+                                        grad_scale.data_ptr() if grad_scale is not None else None,
+                                        seed & 0xFFFFFFFFFFFFFFFF, _stream(dev)))
     return Ps
 
 
