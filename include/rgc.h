@@ -457,8 +457,8 @@ rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_d
  * (type gt) and moments Ms[i], Vs[i] (in place). In fp32, for every element:
  *   g' = g * *grad_scale (1 if NULL: e.g. a clipping coefficient, on the device)
  *   m <- beta1 m + (1 - beta1) g',  v <- beta2 v + (1 - beta2) g'^2
- *   p <- p (1 - lr weight_decay)
- *        - lr/(1 - beta1^step) * m / (sqrt(v)/sqrt(1 - beta2^step) + eps)
+ *   p <- p - (lr weight_decay p
+ *             + lr/(1 - beta1^step) * m / (sqrt(v)/sqrt(1 - beta2^step) + eps))
  * A *grad_scale that is not finite skips the step: nothing changes.
  * bf16 parameters are rounded stochastically as rgc_apply's weights are, with
  * the bits of Philox4x32-10 (counter (e/8 low, e/8 high, 4, i), key = seed)

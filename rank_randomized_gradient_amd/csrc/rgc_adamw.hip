@@ -1,9 +1,11 @@
 // One AdamW step over many tensors, with moments in fp32 or in 8 bits:
 //
 //   g' = scale g,  m <- b1 m + (1 - b1) g',  v <- b2 v + (1 - b2) g'^2
-//   p <- p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//   p <- p - (lr wd p + lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps))
 //
-// in fp32 whatever the stored types. bf16 parameters are rounded
+// in fp32 whatever the stored types. Both terms are joined before the one
+// subtraction: a factor 1 - lr wd rounded to fp32 would be 1 at lr wd = 1e-8 and
+// decay twice as fast as asked at 3e-8. bf16 parameters are rounded
 // stochastically, as the sketched update's weights are: no fp32 copy is kept,
 // and a step far below half a unit in the last place still moves the weight
 // in expectation.
@@ -65,7 +67,7 @@ struct AdamArgs {
   uint32_t first;  // index of the launch's first tensor within the call
   uint32_t key0, key1;
   float b1, c1, b2, c2;  // b1, 1 - b1, b2, 1 - b2
-  float keep;            // 1 - lr wd
+  float decay;           // lr wd
   float size;            // lr / (1 - b1^t)
   float root;            // 1 / sqrt(1 - b2^t)
   float eps;
@@ -253,8 +255,11 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs a) {
     for (int j = 0; j < 8; ++j) root[j] = plain_root(v[j]);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j)  // (the reciprocal is good to one unit in the last place)
-    p[j] = p[j] * a.keep - a.size * (m[j] * __builtin_amdgcn_rcpf(root[j] * a.root + a.eps));
+  for (int j = 0; j < 8; ++j) {  // (the reciprocal is good to one unit in the last place)
+    // an infinite parameter's decay is finite, or infinity would be subtracted from itself
+    const float d = __builtin_amdgcn_fmed3f(p[j], -0x1.fffffep127f, 0x1.fffffep127f) * a.decay;
+    p[j] = p[j] - (d + a.size * (m[j] * __builtin_amdgcn_rcpf(root[j] * a.root + a.eps)));
+  }
   u32x4 bits{0u, 0u, 0u, 0u};
   if constexpr (EIGHT || sizeof(PT) == 2) {
     const uint64_t group = (uint64_t)at / 8;
@@ -379,7 +384,7 @@ extern "C" rgc_status_t rgc_adamw_batch_with(unsigned flags, int64_t n, rgc_dtyp
   AdamArgs a{};
   a.key0 = (uint32_t)seed, a.key1 = (uint32_t)(seed >> 32);
   a.b1 = (float)beta1, a.c1 = (float)(1 - beta1), a.b2 = (float)beta2, a.c2 = (float)(1 - beta2);
-  a.keep = (float)(1 - lr * weight_decay);
+  a.decay = (float)(lr * weight_decay);
   a.size = (float)(lr / (1 - pow(beta1, (double)step)));
   a.root = (float)(1 / sqrt(1 - pow(beta2, (double)step)));
   a.eps = (float)eps;
