@@ -481,7 +481,9 @@ rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_d
  * Arrays are HOST arrays of n entries, n without limit (48 tensors a launch);
  * parameters, gradients and moments 16-byte aligned, at most 2^34 elements. A
  * tensor may be listed once only. RGC_ERR_VALUE: step < 1, a beta outside
- * [0, 1), eps below 2^-126 (as fp32), or a scalar that is not finite. */
+ * [0, 1) (as fp32: one just below 1 rounds to it), eps below 2^-126 (as fp32), lr,
+ * lr weight_decay or lr/(1 - beta1^step) above 1e30, or a scalar that is not
+ * finite. */
 typedef enum { RGC_ADAMW_STOCHASTIC_M = 1 } rgc_adamw_flags_t;
 
 rgc_status_t rgc_adamw_batch_with(unsigned flags, int64_t n, rgc_dtype_t pt, rgc_dtype_t gt, int state_bits,

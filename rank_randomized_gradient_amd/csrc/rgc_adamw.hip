@@ -363,8 +363,9 @@ extern "C" rgc_status_t rgc_adamw_batch_with(unsigned flags, int64_t n, rgc_dtyp
     return RGC_ERR_UNSUPPORTED;
   const bool stochastic = (flags & RGC_ADAMW_STOCHASTIC_M) != 0;
   // scalars that would divide by zero or give values that are not finite for finite inputs
-  if (!(fabs(lr) <= 1e30) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps <= 1e30) ||
-      !((float)eps >= 0x1p-126f) || !(fabs(weight_decay) <= 1e30) || step < 1)
+  if (!(fabs(lr) <= 1e30) || !(beta1 >= 0 && (float)beta1 < 1) || !(beta2 >= 0 && (float)beta2 < 1) || !(eps <= 1e30) ||
+      !((float)eps >= 0x1p-126f) || !(fabs(weight_decay) <= 1e30) || !(fabs(lr * weight_decay) <= 1e30) || step < 1 ||
+      !(fabs(lr) <= 1e30 * (1 - pow(beta1, (double)step))))
     return RGC_ERR_VALUE;
   // a first moment that rounding to nearest would hold in place
   if (state_bits == 8 && !stochastic && beta1 > 0.9) return RGC_ERR_VALUE;

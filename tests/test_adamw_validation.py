@@ -35,3 +35,12 @@ def test_flags(lib):
     assert _with(lib, flags=1 << 20) == UNSUP
     with pytest.raises(rgc.RgcError):
         rgc.rgc_adamw_batch([], [], [], [], 1e-3, 1, m_rounding="down")
+
+
+def test_scalars_that_would_make_infinities_of_finite_inputs(lib):
+    assert _with(lib, bits=32, lr=1e20, wd=1e20) == VALUE  # lr wd
+    assert _with(lib, bits=32, lr=1e29, beta1=0.999999) == VALUE  # lr / (1 - beta1)
+    assert _with(lib, bits=32, lr=1e29, beta1=0.999999, step=10 ** 9) == OK
+    # a beta that fp32 holds as 1 would never forget
+    assert _with(lib, bits=32, beta1=1 - 1e-9) == _with(lib, bits=32, beta2=1 - 1e-9) == VALUE
+    assert _with(lib, bits=32, beta1=1 - 2.0 ** -24, beta2=1 - 2.0 ** -24) == OK
