@@ -484,7 +484,10 @@ rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_d
  * [0, 1) (as fp32: one just below 1 rounds to it), eps below 2^-126 (as fp32), lr,
  * lr weight_decay or lr/(1 - beta1^step) above 1e30, or a scalar that is not
  * finite. */
-typedef enum { RGC_ADAMW_STOCHASTIC_M = 1 } rgc_adamw_flags_t;
+typedef enum {
+  RGC_ADAMW_STOCHASTIC_M = 1,
+  RGC_ADAMW_CHECK_ONLY = 2 /* nothing is launched: what the call would be refused for, or RGC_OK */
+} rgc_adamw_flags_t;
 
 rgc_status_t rgc_adamw_batch_with(unsigned flags, int64_t n, rgc_dtype_t pt, rgc_dtype_t gt, int state_bits,
                                   void* const* Ps, const void* const* Gs, void* const* Ms, void* const* Vs,

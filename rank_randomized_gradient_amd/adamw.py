@@ -15,7 +15,7 @@ class AdamW:
     state_bits 8 holds both moments as e4m3 with a scale per 128 elements (2.06
     bytes an element), rounded stochastically, 32 as float32 (8 bytes). `seed` and the count of steps
     give the rounding bits, so a run repeats bit for bit. Parameters and
-    gradients are contiguous bf16 or float32 tensors. The step count and the
+    gradients are contiguous bf16 or float32 tensors at multiples of 16 bytes. The step count and the
     rounding key are host values: a step captured into a graph would repeat
     both in every replay.
     """
@@ -47,28 +47,33 @@ class AdamW:
     def step(self, grad_scale: torch.Tensor | None = None) -> None:
         """One step from the parameters' .grad, times grad_scale (a float32 on the
         device, e.g. a clipping coefficient; one that is not finite leaves the
-        parameters and moments as they are, though the step is counted)."""
-        self.steps += 1
-        calls: dict = {}  # one call for each pair of types, device and step count
+        parameters and moments as they are, though the step is counted). A step that is
+        refused changes nothing."""
+        groups: dict = {}  # one call for each pair of types, device and step count
         for i, p in enumerate(self.params):
             if p.grad is None:
                 continue
             if self.state[i] is None:
                 self.state[i] = self._fresh(p)
-            calls.setdefault((p.dtype, p.grad.dtype, p.device, self.state[i]["step"] + 1), []).append(i)
-        for n, ((_, _, _, t), at) in enumerate(calls.items()):
+            groups.setdefault((p.dtype, p.grad.dtype, p.device, self.state[i]["step"] + 1), []).append(i)
+        eight, calls = self.state_bits == 8, []
+        for n, ((_, _, _, t), at) in enumerate(groups.items()):
             s = [self.state[i] for i in at]
-            eight = self.state_bits == 8
             # every call of a run has a key of its own: the seed, the step above bit 32 and the call above bit 56
-            key = self.seed + (self.steps << 32) + (n << 56)
-            rgc.rgc_adamw_batch([self.params[i].data for i in at], [self.params[i].grad for i in at], [x["M"] for x in s],
-                                [x["V"] for x in s], self.lr, t, seed=key, beta1=self.betas[0], beta2=self.betas[1],
-                                eps=self.eps, weight_decay=self.weight_decay,
-                                M_scales=[x["M_scale"] for x in s] if eight else None,
-                                V_scales=[x["V_scale"] for x in s] if eight else None, grad_scale=grad_scale,
-                                m_rounding="stochastic")
-            for x in s:  # (a refused call raises before this)
-                x["step"] = t
+            key = self.seed + ((self.steps + 1) << 32) + (n << 56)
+            calls.append(rgc._adamw_call([self.params[i].data for i in at], [self.params[i].grad for i in at],
+                                         [x["M"] for x in s], [x["V"] for x in s], self.lr, t, key, self.betas[0],
+                                         self.betas[1], self.eps, self.weight_decay,
+                                         [x["M_scale"] for x in s] if eight else None,
+                                         [x["V_scale"] for x in s] if eight else None, grad_scale, "stochastic"))
+        if len(calls) > 1:  # a call that would be refused is found before any is made
+            for call in calls:
+                call(rgc.RGC_ADAMW_CHECK_ONLY)
+        for call, ((_, _, _, t), at) in zip(calls, groups.items()):
+            call()
+            for i in at:
+                self.state[i]["step"] = t
+        self.steps += 1
 
     def zero_grad(self, set_to_none: bool = True) -> None:
         for p in self.params:

@@ -359,7 +359,7 @@ extern "C" rgc_status_t rgc_adamw_batch_with(unsigned flags, int64_t n, rgc_dtyp
                                              int64_t step, const float* grad_scale, uint64_t seed, void* stream) {
   if (n < 0) return RGC_ERR_SHAPE;
   if (!dtype_ok(pt) || !dtype_ok(gt) || (state_bits != 8 && state_bits != 32) || n > INT32_MAX ||
-      (flags & ~(unsigned)RGC_ADAMW_STOCHASTIC_M))
+      (flags & ~(unsigned)(RGC_ADAMW_STOCHASTIC_M | RGC_ADAMW_CHECK_ONLY)))
     return RGC_ERR_UNSUPPORTED;
   const bool stochastic = (flags & RGC_ADAMW_STOCHASTIC_M) != 0;
   // scalars that would divide by zero or give values that are not finite for finite inputs
@@ -382,6 +382,7 @@ extern "C" rgc_status_t rgc_adamw_batch_with(unsigned flags, int64_t n, rgc_dtyp
         (eight && (!aligned_to(Mscales[i], 4) || !aligned_to(Vscales[i], 4))))
       return RGC_ERR_ALIGN;
   }
+  if (flags & RGC_ADAMW_CHECK_ONLY) return RGC_OK;
   AdamArgs a{};
   a.key0 = (uint32_t)seed, a.key1 = (uint32_t)(seed >> 32);
   a.b1 = (float)beta1, a.c1 = (float)(1 - beta1), a.b2 = (float)beta2, a.c2 = (float)(1 - beta2);

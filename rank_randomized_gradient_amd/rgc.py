@@ -50,6 +50,7 @@ _TYPE_NAMES = {"BFloat16": RGC_BF16, "Float": RGC_F32}
 RGC_NORM_LAYER = 0
 RGC_NORM_RMS = 1
 RGC_ADAMW_STOCHASTIC_M = 1
+RGC_ADAMW_CHECK_ONLY = 2
 _M_ROUNDINGS = {"nearest": 0, "stochastic": RGC_ADAMW_STOCHASTIC_M}
 _NORMS = {"layer": RGC_NORM_LAYER, "rms": RGC_NORM_RMS}
 ADAMW_BLOCK = 128  # elements of an 8-bit state that share a scale
@@ -887,6 +888,15 @@ def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: 
     m_rounding: of 8-bit first moments, "stochastic" (their mean follows the
     formula at any beta1) or "nearest" (beta1 up to 0.9 only: they stop short of a
     steady gradient, by a quarter or so)."""
+    call = _adamw_call(Ps, Gs, Ms, Vs, lr, step, seed, beta1, beta2, eps, weight_decay, M_scales, V_scales, grad_scale,
+                       m_rounding)
+    call()
+    return Ps
+
+
+def _adamw_call(Ps, Gs, Ms, Vs, lr, step, seed, beta1, beta2, eps, weight_decay, M_scales, V_scales, grad_scale,
+                m_rounding):
+    """rgc_adamw_batch's checks, and a function that makes the call (with further flags, if given)."""
     lib = load_library()
     if m_rounding not in _M_ROUNDINGS:
         raise RgcError('m_rounding must be "nearest" or "stochastic"')
@@ -896,7 +906,7 @@ def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: 
     if any(x is None or len(x) != n for x in lists):
         raise RgcError("Ps, Gs, Ms, Vs (and the scales) must be lists of one length")
     if n == 0:
-        return Ps
+        return lambda flags=0: None
     dev = _need_gpu(Ps[0], *([grad_scale] if grad_scale is not None else []))
     state = ("Float8_e4m3fn",) if eight else ("Float",)
     given = [_adamw_list(Ps, "Ps", tuple(_TYPE_NAMES), None)]
@@ -916,13 +926,17 @@ def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: 
         _dense(grad_scale, torch.float32, "grad_scale")
         if grad_scale.numel() != 1:
             raise RgcError("grad_scale must be one float32")
-    with _on(dev):
-        _check(lib.rgc_adamw_batch_with(_M_ROUNDINGS[m_rounding], n, _TYPE_NAMES[given[0][2]], _TYPE_NAMES[given[1][2]],
-                                        8 if eight else 32, pp, gp, mp, vp, msp, vsp, (_i64 * n).from_buffer_copy(sizes),
-                                        lr, beta1, beta2, eps, weight_decay, step,
-                                        grad_scale.data_ptr() if grad_scale is not None else None,
-                                        seed & 0xFFFFFFFFFFFFFFFF, _stream(dev)))
-    return Ps
+    counts = (_i64 * n).from_buffer_copy(sizes)
+
+    def call(flags: int = 0) -> None:
+        with _on(dev):
+            _check(lib.rgc_adamw_batch_with(flags | _M_ROUNDINGS[m_rounding], n, _TYPE_NAMES[given[0][2]],
+                                            _TYPE_NAMES[given[1][2]], 8 if eight else 32, pp, gp, mp, vp, msp, vsp, counts,
+                                            lr, beta1, beta2, eps, weight_decay, step,
+                                            grad_scale.data_ptr() if grad_scale is not None else None,
+                                            seed & 0xFFFFFFFFFFFFFFFF, _stream(dev)))
+
+    return call
 
 
 # ---- test hooks -------------------------------------------------------------

@@ -44,3 +44,16 @@ def test_scalars_that_would_make_infinities_of_finite_inputs(lib):
     # a beta that fp32 holds as 1 would never forget
     assert _with(lib, bits=32, beta1=1 - 1e-9) == _with(lib, bits=32, beta2=1 - 1e-9) == VALUE
     assert _with(lib, bits=32, beta1=1 - 2.0 ** -24, beta2=1 - 2.0 ** -24) == OK
+
+
+def test_check_only(lib):
+    """The refusals of the call, and nothing launched: addresses that are never read."""
+    fake = (ctypes.c_void_p * 1)(0x10000)
+    n = (ctypes.c_int64 * 1)(100)
+
+    def call(p=fake, lr=1e-3):
+        return lib.rgc_adamw_batch_with(rgc.RGC_ADAMW_CHECK_ONLY, 1, 0, 0, 32, p, fake, fake, fake, None, None, n, lr, 0.9,
+                                        0.999, 1e-8, 0.0, 1, None, 1, None)
+
+    assert call() == OK and call((ctypes.c_void_p * 1)(0x10008)) == 4 and call((ctypes.c_void_p * 1)(None)) == 1
+    assert call(lr=float("nan")) == VALUE
