@@ -480,10 +480,11 @@ rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_d
  * gradients end while its block's go on keeps up to 2^-14 of the block's largest m.
  * Arrays are HOST arrays of n entries, n without limit (48 tensors a launch);
  * parameters, gradients and moments 16-byte aligned, at most 2^34 elements. A
- * tensor may be listed once only. RGC_ERR_VALUE: step < 1, a beta outside
- * [0, 1) (as fp32: one just below 1 rounds to it), eps below 2^-126 (as fp32), lr,
- * lr weight_decay or lr/(1 - beta1^step) above 1e30, or a scalar that is not
- * finite. */
+ * tensor may be listed once only, and what is written (parameters, moments,
+ * scales) shares no memory with any other tensor of the call (the binding refuses
+ * it). RGC_ERR_VALUE: step < 1, a beta outside [0, 1) (as fp32: one just below 1
+ * rounds to it), eps below 2^-126 (as fp32), lr, lr weight_decay or
+ * lr/(1 - beta1^step) above 1e30, or a scalar that is not finite. */
 typedef enum {
   RGC_ADAMW_STOCHASTIC_M = 1,
   RGC_ADAMW_CHECK_ONLY = 2 /* nothing is launched: what the call would be refused for, or RGC_OK */

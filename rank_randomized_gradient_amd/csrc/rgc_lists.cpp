@@ -66,19 +66,52 @@ PyObject* pack(PyObject*, PyObject* args) {
   return Py_BuildValue("(NNsi)", pointers, counts, c10::toString(type), device.is_cuda() ? (int)device.index() : -1);
 }
 
-// distinct(pointers) -> whether no address that is not zero occurs twice
-PyObject* distinct(PyObject*, PyObject* bytes) {
-  if (!PyBytes_Check(bytes)) {
-    PyErr_SetString(PyExc_TypeError, "bytes of addresses are wanted");
-    return nullptr;
+struct Range {
+  uint64_t from, to;
+  bool operator<(const Range& other) const { return from < other.from; }
+};
+
+// The ranges of a (pointers, counts, bytes of an element) triple that hold anything, in ascending order.
+bool ranges_of(PyObject* triple, std::vector<Range>& out) {
+  PyObject *pointers, *counts;
+  long long size;
+  if (!PyArg_ParseTuple(triple, "SSL", &pointers, &counts, &size)) return false;
+  if (PyBytes_GET_SIZE(pointers) != PyBytes_GET_SIZE(counts)) {
+    PyErr_SetString(PyExc_ValueError, "as many counts as pointers are wanted");
+    return false;
   }
-  const uint64_t* p = reinterpret_cast<const uint64_t*>(PyBytes_AS_STRING(bytes));
-  const Py_ssize_t n = PyBytes_GET_SIZE(bytes) / 8;
+  const uint64_t* p = reinterpret_cast<const uint64_t*>(PyBytes_AS_STRING(pointers));
+  const int64_t* c = reinterpret_cast<const int64_t*>(PyBytes_AS_STRING(counts));
+  const Py_ssize_t n = PyBytes_GET_SIZE(pointers) / 8;
+  const size_t first = out.size();
+  for (Py_ssize_t i = 0; i < n; ++i)
+    if (c[i] > 0) out.push_back({p[i], p[i] + (uint64_t)(c[i] * size)});
+  if (!std::is_sorted(out.begin() + first, out.end())) std::sort(out.begin() + first, out.end());
+  std::inplace_merge(out.begin(), out.begin() + first, out.end());
+  return true;
+}
+
+// disjoint(read, written, written, ...) -> whether no written range meets another or a read one; each a tuple
+// (pointers, counts, bytes of an element) as pack gives the first two
+PyObject* disjoint(PyObject*, PyObject* args) {
+  const Py_ssize_t lists = PyTuple_GET_SIZE(args);
   bool yes = true;
   try {
-    std::vector<uint64_t> v(p, p + n);
-    std::sort(v.begin(), v.end());
-    for (size_t i = 1; i < v.size(); ++i) yes = yes && (v[i] != v[i - 1] || v[i] == 0);
+    std::vector<Range> read, written;
+    for (Py_ssize_t i = 0; i < lists; ++i) {
+      PyObject* t = PyTuple_GET_ITEM(args, i);
+      if (!PyTuple_Check(t)) {
+        PyErr_SetString(PyExc_TypeError, "tuples of pointers, counts and an element's bytes are wanted");
+        return nullptr;
+      }
+      if (!ranges_of(t, i == 0 ? read : written)) return nullptr;
+    }
+    for (size_t i = 1; i < written.size(); ++i) yes = yes && written[i - 1].to <= written[i].from;
+    size_t w = 0;
+    for (const Range& r : read) {  // (written ranges are ascending and apart here, or the answer is no already)
+      while (w < written.size() && written[w].to <= r.from) ++w;
+      yes = yes && (w == written.size() || r.to <= written[w].from);
+    }
   } catch (const std::exception&) {
     return PyErr_NoMemory();
   }
@@ -87,7 +120,7 @@ PyObject* distinct(PyObject*, PyObject* bytes) {
 
 PyMethodDef kMethods[] = {
     {"pack", pack, METH_VARARGS, "Addresses and sizes of a list of dense tensors of one type and device, or None."},
-    {"distinct", distinct, METH_O, "Whether no address occurs twice."},
+    {"disjoint", disjoint, METH_VARARGS, "Whether no written range meets another or a read one."},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_rgc_lists", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -47,6 +47,7 @@ RGC_BF16 = 0
 RGC_F32 = 1
 _DTYPES = {torch.bfloat16: RGC_BF16, torch.float32: RGC_F32}
 _TYPE_NAMES = {"BFloat16": RGC_BF16, "Float": RGC_F32}
+_ITEM_BYTES = {"BFloat16": 2, "Float": 4, "Float8_e4m3fn": 1}
 RGC_NORM_LAYER = 0
 RGC_NORM_RMS = 1
 RGC_ADAMW_STOCHASTIC_M = 1
@@ -918,8 +919,9 @@ def _adamw_call(Ps, Gs, Ms, Vs, lr, step, seed, beta1, beta2, eps, weight_decay,
                   for ts, name in ((M_scales, "M_scales"), (V_scales, "V_scales"))]
     if any(x[3] != dev.index for x in given):
         raise RgcError("all tensors must be on the same device")
-    if n > 1 and not all(_lists().distinct(given[i][0]) for i in (0, 2, 3)):
-        raise RgcError("a tensor is listed twice")
+    spans = [(x[0], x[1], _ITEM_BYTES[x[2]]) for x in given]
+    if not _lists().disjoint(spans[1], spans[0], *spans[2:]):
+        raise RgcError("a tensor is listed twice, or shares memory with another that the step writes")
     pp, gp, mp, vp, *scales = [(_vp * n).from_buffer_copy(x[0]) for x in given]
     msp, vsp = scales if eight else (None, None)
     if grad_scale is not None:
