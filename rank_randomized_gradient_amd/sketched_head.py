@@ -17,10 +17,14 @@ from .sketched_linear import SketchedLinear
 
 
 class SketchedCrossEntropyFunction(torch.autograd.Function):
-    """Per-token losses; saves X, X P and each token's log sum of exponentials."""
+    """Per-token losses; saves X, X P and each token's log sum of exponentials.
+
+    `anchor` is a scalar that requires a gradient and gets none: it brings the
+    backward here, where the sketch is added to, whether or not x requires one
+    (the weight does not)."""
 
     @staticmethod
-    def forward(ctx, x, weight, targets, proj, sketch):
+    def forward(ctx, x, weight, targets, proj, sketch, anchor=None):
         x2 = x.reshape(-1, x.shape[-1])
         if not x2.is_contiguous():
             x2 = x2.contiguous()
@@ -38,7 +42,7 @@ class SketchedCrossEntropyFunction(torch.autograd.Function):
         g = dloss.reshape(-1).to(torch.float32).contiguous()
         dx = rgc.rgc_linear_cross_entropy_backward(x2, weight, t, lse, g, xp, ctx.sketch,
                                                    input_grad=ctx.needs_input_grad[0])
-        return None if dx is None else dx.reshape(ctx.in_shape), None, None, None, None
+        return None if dx is None else dx.reshape(ctx.in_shape), None, None, None, None, None
 
 
 class SketchedCrossEntropy(SketchedLinear):
@@ -48,8 +52,8 @@ class SketchedCrossEntropy(SketchedLinear):
     outside 0 .. vocabulary - 1 (-100, say) is ignored: loss 0, no gradient.
     Weigh and sum the losses as the objective asks (a mean over the tokens that
     count, advantages). begin_update, apply_update and the carried norm are
-    SketchedLinear's: the losses' backward adds the head's D^T (X P) to `sketch`
-    (x has to require a gradient for the backward to come this far).
+    SketchedLinear's: the losses' backward adds the head's D^T (X P) to `sketch`,
+    also for an x that requires no gradient.
     The vocabulary is a multiple of 8, as every sketched layer's width.
     """
 
@@ -58,4 +62,5 @@ class SketchedCrossEntropy(SketchedLinear):
             raise rgc.RgcError("begin_update(seed) must draw the projection before the first forward")
         if targets.dtype != torch.int64 or targets.shape != x.shape[:-1]:
             raise rgc.RgcError("targets must be int64, one for each row of x")
-        return SketchedCrossEntropyFunction.apply(x, self.weight, targets, self.proj, self.sketch)
+        anchor = torch.zeros((), requires_grad=True)
+        return SketchedCrossEntropyFunction.apply(x, self.weight, targets, self.proj, self.sketch, anchor)
