@@ -24,10 +24,14 @@ from . import rgc
 
 class SketchedLinearFunction(torch.autograd.Function):
     """Y = X W^T and XP = X P from one call; saves XP (T x r), not X; backward:
-    dX = D W and C += D^T XP from one call (C alone when X needs no gradient)."""
+    dX = D W and C += D^T XP from one call (C alone when X needs no gradient).
+
+    `anchor` is a scalar that requires a gradient and gets none: it brings the
+    backward here, where the sketch is added to, whether or not x requires one
+    (the weight does not)."""
 
     @staticmethod
-    def forward(ctx, x, weight, proj, sketch, workspace):
+    def forward(ctx, x, weight, proj, sketch, workspace, anchor=None):
         x2 = x.reshape(-1, x.shape[-1])
         if not x2.is_contiguous():
             x2 = x2.contiguous()
@@ -51,7 +55,7 @@ class SketchedLinearFunction(torch.autograd.Function):
         else:
             rgc.rgc_accumulate(d2, xp, ctx.sketch, workspace=ctx.workspace)
             dx = None
-        return dx, None, None, None, None
+        return dx, None, None, None, None, None
 
 
 class SketchedLinear(torch.nn.Module):
@@ -114,7 +118,8 @@ class SketchedLinear(torch.nn.Module):
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if self.proj_seed is None:
             raise rgc.RgcError("begin_update(seed) must draw the projection before the first forward")
-        return SketchedLinearFunction.apply(x, self.weight, self.proj, self.sketch, self.workspace)
+        anchor = torch.zeros((), requires_grad=True)
+        return SketchedLinearFunction.apply(x, self.weight, self.proj, self.sketch, self.workspace, anchor)
 
     def apply_update(self, seed: int, tau: float | None = None, alpha: float | None = None,
                      stats: torch.Tensor | None = None) -> None:
