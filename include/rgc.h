@@ -404,7 +404,10 @@ rgc_status_t rgc_linear_backward(const uint16_t* D, int64_t ldd, const uint16_t*
  *   be NULL) is a frozen head: dX alone. With r > 0 dX may be NULL (an input
  *   that needs no gradient): C alone.
  * Limits: T and k at most 65536, V at most 2^24 and, with r > 0, a multiple of
- * 8 in the backward (as every layer's d); k, ldx, ldw and lddx multiples of 8,
+ * 8 in the backward (as every layer's d); T and V together below 2^22 tiles of the
+ * forward (RGC_ERR_UNSUPPORTED and a workspace size of 0 otherwise): 256 x 256
+ * ones for many tokens, so 65536 tokens go with V up to 4 million (64 x 128 up to
+ * 64 tokens, 128 x 128 up to 128: every V); k, ldx, ldw and lddx multiples of 8,
  * leading dimensions at most 2^23; X, W, P, XP, C and dX 16-byte aligned; r 0 or a
  * supported rank. T = 0 is a no-op. The workspaces hold the tiles' partial
  * results (forward) and one piece's D with dX's fp32 sums (backward). */

@@ -710,6 +710,9 @@ rgc_status_t check_shape(int64_t T, int64_t V, int64_t k, int64_t r) {
 
 rgc_status_t launched() { return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP; }
 
+// Whether the forward's one launch over all tiles stays below 2^31 threads.
+bool forward_fits(int64_t T, int64_t V) { return blocks_of(T, V, grid_of(T, V)) < int64_t(1) << 22; }
+
 // A token's partial sums, one for each column of tiles.
 size_t part_bytes(int64_t T, int64_t V) { return up256((size_t)grid_of(T, V).ntiles * (size_t)T * 8); }
 
@@ -719,7 +722,7 @@ size_t part_bytes(int64_t T, int64_t V) { return up256((size_t)grid_of(T, V).nti
 using namespace rgc;
 
 extern "C" size_t rgc_linear_cross_entropy_forward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r) {
-  if (!shape_ok(T, V, k, r)) return 0;
+  if (!shape_ok(T, V, k, r) || !forward_fits(T, V)) return 0;
   return part_bytes(T, V) + up256((size_t)T * 4) + (r > 0 ? rgc_project_workspace_size(T, k, r) : 0);
 }
 
@@ -729,6 +732,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int6
                                                          int64_t r, void* ws, size_t ws_bytes, void* stream) {
   rgc_status_t st = check_shape(T, V, k, r);
   if (st != RGC_OK || T == 0) return st;
+  if (!forward_fits(T, V)) return RGC_ERR_UNSUPPORTED;
   if ((st = check_rows(X, ldx, k)) != RGC_OK) return st;
   if ((st = check_rows(W, ldw, k)) != RGC_OK) return st;
   if (!targets || !loss || !lse || (r > 0 && (!P || !XP))) return RGC_ERR_NULL;
@@ -744,7 +748,6 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int6
   at += part_bytes(T, V);
   a.zt = reinterpret_cast<float*>(at);
   at += up256((size_t)T * 4);
-  if (blocks_of(T, V, grid_of(T, V)) >= int64_t(1) << 22) return RGC_ERR_UNSUPPORTED;  // 2^31 threads of a launch
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (r > 0) {  // the layer's X P, as rgc_project makes it
     st = rgc_project(X, ldx, P, XP, T, k, r, at, ws_bytes - (size_t)(at - static_cast<char*>(ws)), stream);
