@@ -33,12 +33,14 @@ def hipcc() -> str:
 
 
 def lists_command(out: str) -> list:
-    """g++'s command for the CPython module that unpacks lists of tensors (host code only)."""
+    """The host compiler's command for the CPython module that unpacks lists of tensors: CXX, g++, or ROCm's clang."""
     from torch.utils import cpp_extension
 
-    inc = [f"-I{p}" for p in [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]]
+    cxx = os.environ.get("CXX") or shutil.which("g++") or os.path.join(os.path.dirname(hipcc()), "amdclang++")
+    # (torch's headers as a system's: their warnings are not this module's)
+    inc = [x for p in [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]] for x in ("-isystem", p)]
     lib = [f"-L{p}" for p in cpp_extension.library_paths()]
-    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", *inc,
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *inc,
             os.path.join(CSRC, "rgc_lists.cpp"), "-o", out, *lib, "-lc10", "-ltorch_cpu", "-ltorch_python"]
 
 
