@@ -398,6 +398,7 @@ rgc_status_t rgc_linear_backward(const uint16_t* D, int64_t ldd, const uint16_t*
  *   token, formed from z again for one piece of the vocabulary after another;
  *   dX = bf16(D W): T x k, row stride lddx, overwritten; the pieces added in fp32;
  *   C += D^T XP with r > 0: V x r fp32, only added to as by rgc_accumulate.
+ *   dX may be X, with the same row stride.
  *   In both D is held in fp32 or as two bf16 terms (hi + lo, off by 2^-17 of D at
  *   most), the targets' entries in fp32.
  *   C is what rgc_apply turns into the head's update. r = 0 (XP and C may then
@@ -438,9 +439,11 @@ rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int64_t ldx, c
  * float[rows]. weight NULL stands for ones, bias NULL for none; mean and rstd
  * may be NULL in the forward (not kept), mean in an RMS backward; dbias NULL
  * is not formed. Everything in fp32, fixed order, one rounding per output.
- * Any n from 1 to 65536 and rows up to 2^31; pointers aligned to their
- * elements (16-byte aligned rows of a multiple of 8 elements move in 16-byte
- * vectors, others element by element). eps must be finite and not negative. */
+ * Any n from 1 to 65536 and rows up to 2^31; pointers aligned to their elements
+ * (rows move in 16-byte vectors wherever they start, the last elements of an n
+ * that is no multiple of 8, and a backward above n = 16384, one by one). Y may be
+ * X, and dX may be X or dY, with the same row stride. eps must be finite and not
+ * negative. */
 typedef enum { RGC_BF16 = 0, RGC_F32 = 1 } rgc_dtype_t;
 typedef enum { RGC_NORM_LAYER = 0, RGC_NORM_RMS = 1 } rgc_norm_kind_t;
 
