@@ -688,6 +688,8 @@ def _scratch(workspace: Workspace | None, nbytes: int, dev: torch.device):
     buffer of the call's own from torch's allocator, which orders its reuse on
     the stream and keeps it for a graph that captured the call."""
     if workspace is not None:
+        if workspace.buf.device != dev:
+            raise RgcError("the workspace must be on the tensors' device")
         return (*workspace.get(nbytes), workspace.buf)
     buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     return ctypes.c_void_p(buf.data_ptr()), nbytes, buf
