@@ -62,5 +62,5 @@ class SketchedCrossEntropy(SketchedLinear):
             raise rgc.RgcError("begin_update(seed) must draw the projection before the first forward")
         if targets.dtype != torch.int64 or targets.shape != x.shape[:-1]:
             raise rgc.RgcError("targets must be int64, one for each row of x")
-        anchor = torch.zeros((), requires_grad=True)
+        anchor = torch.zeros((), device="cpu", requires_grad=True)
         return SketchedCrossEntropyFunction.apply(x, self.weight, targets, self.proj, self.sketch, anchor)

@@ -118,7 +118,7 @@ class SketchedLinear(torch.nn.Module):
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if self.proj_seed is None:
             raise rgc.RgcError("begin_update(seed) must draw the projection before the first forward")
-        anchor = torch.zeros((), requires_grad=True)
+        anchor = torch.zeros((), device="cpu", requires_grad=True)
         return SketchedLinearFunction.apply(x, self.weight, self.proj, self.sketch, self.workspace, anchor)
 
     def apply_update(self, seed: int, tau: float | None = None, alpha: float | None = None,
