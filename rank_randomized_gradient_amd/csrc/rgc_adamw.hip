@@ -30,9 +30,10 @@
 // become NaN codes and are left out of the scale: they spoil their own elements only.
 //
 // Bound by memory: 2 p + g + 16 bytes an element in fp32 states, 2 p + g + 4
-// in 8 bits (10 bytes for bf16). 134M bf16 parameters with 8-bit states take 241
-// us on MI355X (5.6 TB/s; a copy reaches 5.2), 33.5M fp32 ones with fp32 states
-// 173 us (5.4 TB/s). With a correctly rounded division and square root and every
+// in 8 bits (10 bytes for bf16). 134M bf16 parameters with 8-bit states take 248
+// us on MI355X (5.4 TB/s; a copy reaches 5.2; 238 on the same tensors step after
+// step, with m rounded either way), 60 ragged fp32 ones of 29M elements with fp32
+// states 161 us (5.1 TB/s). With a correctly rounded division and square root and every
 // element checked for NaN the 8-bit step took 283 us, bound by instructions.
 // Eight consecutive elements to a thread, so
 // one Philox call (128 bits) serves the thread: element j of the eight takes
