@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define RGC_ABI_VERSION 8
+#define RGC_ABI_VERSION 9
 
 typedef enum {
   RGC_OK = 0,
@@ -424,6 +424,29 @@ rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int64_t ldx, c
                                                int64_t V, int64_t k, int64_t r, void* ws, size_t ws_bytes,
                                                void* stream);
 
+/* The head's log probabilities, with entropies: the same products without kept
+ * logits, for a policy's loss. For token t, its lse as above and p_tv =
+ * exp(z_tv - lse[t]):
+ *   logp[t] = z_t,tokens[t] - lse[t],  entropy[t] = -sum_v p_tv log p_tv;
+ * both 0 for a token outside 0 .. V-1, which takes no part.
+ * Backward, from grad_logp[t] and grad_entropy[t] (either may be NULL: zeros) and
+ * the forward's lse and entropy (entropy may be NULL without grad_entropy):
+ *   D_tv = grad_logp[t] ([v = tokens[t]] - p_tv)
+ *          - grad_entropy[t] p_tv (z_tv - lse[t] + entropy[t]),
+ * taken further as the cross entropy's D is. All else, the limits and the meaning of
+ * P, XP, C, dX and r among it, is as for the cross entropy. */
+size_t rgc_linear_log_prob_forward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r);
+rgc_status_t rgc_linear_log_prob_forward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                         const uint16_t* P, const int64_t* tokens, float* logp, float* entropy,
+                                         float* lse, uint16_t* XP, int64_t T, int64_t V, int64_t k, int64_t r, void* ws,
+                                         size_t ws_bytes, void* stream);
+size_t rgc_linear_log_prob_backward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r);
+rgc_status_t rgc_linear_log_prob_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                          const int64_t* tokens, const float* lse, const float* entropy,
+                                          const float* grad_logp, const float* grad_entropy, const uint16_t* XP, float* C,
+                                          uint16_t* dX, int64_t lddx, int64_t T, int64_t V, int64_t k, int64_t r,
+                                          void* ws, size_t ws_bytes, void* stream);
+
 /* ---- Layer norms ------------------------------------------------------------
  *
  * Row norms between the sketched layers, with their weights' gradients (which
@@ -455,6 +478,74 @@ rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_d
                                      int64_t lddy, const void* X, int64_t ldx, const void* weight, const float* mean,
                                      const float* rstd, void* dX, int64_t lddx, void* dweight, void* dbias,
                                      int64_t rows, int64_t n, void* ws, size_t ws_bytes, void* stream);
+
+/* The norm of a residual stream together with the addition that makes it:
+ *   S = X + R, rounded to the tensors' type, and Y = the norm of S, with the very
+ *   bits of rgc_layer_norm_forward of S (mean and rstd too).
+ * Backward: dX = dS + the norm's own dx (the gradient of X and of R alike; one
+ * rounding), dweight and dbias as above. dS NULL stands for zeros.
+ * X, R, S, Y, dY, dS, dX: rows x n of type xt, row strides as above. S may be X or
+ * R, and Y whichever of the two S is not; dX may be S, dY or dS; each with the same
+ * row stride. The rest is as for the layer norms. */
+rgc_status_t rgc_add_norm_forward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* X, int64_t ldx,
+                                  const void* R, int64_t ldr, const void* weight, const void* bias, double eps, void* S,
+                                  int64_t lds, void* Y, int64_t ldy, float* mean, float* rstd, int64_t rows, int64_t n,
+                                  void* stream);
+size_t rgc_add_norm_backward_workspace_size(int64_t rows, int64_t n);
+rgc_status_t rgc_add_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* dY, int64_t lddy,
+                                   const void* dS, int64_t ldds, const void* S, int64_t lds, const void* weight,
+                                   const float* mean, const float* rstd, void* dX, int64_t lddx, void* dweight,
+                                   void* dbias, int64_t rows, int64_t n, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Log probabilities of logits at hand ---------------------------------------
+ *
+ * For rows of V logits z (a rollout's, a reference model's), with lse = log sum_v
+ * exp z_v and p = exp(z - lse):
+ *   logp[i] = z_tokens[i] - lse[i], entropy[i] = -sum_v p_v log p_v, and the `top`
+ *   most likely entries in descending order, of equal ones the lowest index first:
+ *   top_ids[i][j], top_logp[i][j] = z - lse (rows x top, contiguous).
+ * A token outside 0 .. V-1 takes no part: its logp and entropy are 0 (lse and the
+ * alternatives are its row's). tokens NULL: no logp (which may be NULL), and every
+ * row's entropy.
+ * Entries of -inf are forbidden ones: no part in lse and entropy. A row of nothing
+ * else has lse and logp -inf, entropy 0. NaN or +inf make their row's numbers NaN; in
+ * the order of the alternatives NaN lies above +inf.
+ * Backward, from grad_logp and grad_entropy (either may be NULL: zeros) and the
+ * forward's lse and entropy (entropy may be NULL without grad_entropy):
+ *   dz_v = grad_logp ([v = token] - p_v) - grad_entropy p_v (z_v - lse + entropy),
+ * a row of zeros for a token that takes no part and for a row of -inf.
+ * Z, dZ: rows x V of type zt, row strides at least V (at most 2^31), aligned to
+ * their elements; dZ may be Z, with the same row stride. logp, entropy, lse,
+ * top_logp, grads: float; tokens, top_ids: int64. Sums in fp32, in a fixed order.
+ * rows at most 2^31, V at most 2^24, top at most 64 and at most V. rows = 0 is a no-op. */
+size_t rgc_log_prob_forward_workspace_size(int64_t rows, int64_t V, int64_t top);
+rgc_status_t rgc_log_prob_forward(rgc_dtype_t zt, const void* Z, int64_t ldz, const int64_t* tokens, float* logp,
+                                  float* entropy, float* lse, int64_t top, float* top_logp, int64_t* top_ids,
+                                  int64_t rows, int64_t V, void* ws, size_t ws_bytes, void* stream);
+rgc_status_t rgc_log_prob_backward(rgc_dtype_t zt, const void* Z, int64_t ldz, const int64_t* tokens, const float* lse,
+                                   const float* entropy, const float* grad_logp, const float* grad_entropy, void* dZ,
+                                   int64_t lddz, int64_t rows, int64_t V, void* stream);
+
+/* ---- The gradients' global norm, and clipping ------------------------------------
+ *
+ * out[0] = norm = |s| sqrt(sum over n tensors of their squares), out[1] = scale =
+ * s min(1, max_norm / norm), s = *grad_scale (1 if NULL): the factor that brings
+ * gradients that are to be multiplied by s anyway to a norm of max_norm at most.
+ * scale is what rgc_adamw_batch takes as grad_scale, on the device. A norm that is
+ * not finite (in fp64) gives a scale of NaN, which skips that step. The squares are added in
+ * fp64 in a fixed order, and each result is rounded once. A tensor listed twice counts twice.
+ * rgc_scale_batch multiplies the tensors by *scale in place (bf16 rounded to
+ * nearest); a scale that is 1 or not finite changes nothing.
+ * Gs, gts, numels: HOST arrays of n entries (at most 2^24): tensor i has numels[i] (at most 2^34)
+ * contiguous elements of type gts[i], aligned to its elements. out: float[2].
+ * max_norm may be infinite (the norm alone); RGC_ERR_VALUE if it is negative or NaN.
+ * In rgc_scale_batch no two tensors share memory. */
+size_t rgc_grad_norm_batch_workspace_size(int64_t n, const int64_t* numels);
+rgc_status_t rgc_grad_norm_batch(int64_t n, const rgc_dtype_t* gts, const void* const* Gs, const int64_t* numels,
+                                 double max_norm, const float* grad_scale, float* out, void* ws, size_t ws_bytes,
+                                 void* stream);
+rgc_status_t rgc_scale_batch(int64_t n, const rgc_dtype_t* gts, void* const* Gs, const int64_t* numels,
+                             const float* scale, void* stream);
 
 /* ---- AdamW for the tensors that keep a dense gradient -------------------------
  *

@@ -31,6 +31,14 @@ from .rgc import (  # noqa: F401
     rgc_linear_cross_entropy_backward,
     rgc_layer_norm_forward,
     rgc_layer_norm_backward,
+    rgc_add_norm_forward,
+    rgc_add_norm_backward,
+    rgc_linear_log_prob_forward,
+    rgc_linear_log_prob_backward,
+    rgc_log_prob_forward,
+    rgc_log_prob_backward,
+    rgc_grad_norm_batch,
+    rgc_scale_batch,
     rgc_adamw_batch,
     rgc_sample_projection,
     rgc_sample_projections,
@@ -39,6 +47,8 @@ from .rgc import (  # noqa: F401
     rgc_test_stochastic_round,
 )
 from .sketched_linear import SketchedLinear, SketchedLinearFunction  # noqa: F401,E402
-from .sketched_head import SketchedCrossEntropy, SketchedCrossEntropyFunction  # noqa: F401,E402
-from .layer_norm import LayerNorm, LayerNormFunction  # noqa: F401,E402
+from .sketched_head import SketchedCrossEntropy, SketchedCrossEntropyFunction, SketchedLogProbFunction  # noqa: F401,E402
+from .layer_norm import AddNormFunction, LayerNorm, LayerNormFunction  # noqa: F401,E402
+from .logits import LogProbFunction, log_prob  # noqa: F401,E402
+from .clip import clip_grad_norm  # noqa: F401,E402
 from .adamw import AdamW  # noqa: F401,E402

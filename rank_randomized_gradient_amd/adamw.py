@@ -44,11 +44,17 @@ class AdamW:
                 "V_scale": torch.zeros(blocks, dtype=torch.float32, device=p.device)}
 
     @torch.no_grad()
-    def step(self, grad_scale: torch.Tensor | None = None) -> None:
+    def step(self, grad_scale: torch.Tensor | None = None, max_norm: float | None = None) -> torch.Tensor | None:
         """One step from the parameters' .grad, times grad_scale (a float32 on the
         device, e.g. a clipping coefficient; one that is not finite leaves the
         parameters and moments as they are, though the step is counted). A step that is
-        refused changes nothing."""
+        refused changes nothing. With max_norm the gradients, times grad_scale, are clipped to that
+        global norm as the step reads them (they stay as they are in memory), and their norm before clipping is
+        returned, a float32 on the device; a norm that is not finite is a grad_scale that is not."""
+        norm = None
+        grads = [p.grad for p in self.params if p.grad is not None] if max_norm is not None else []
+        if grads:
+            norm, grad_scale = rgc.rgc_grad_norm_batch(grads, max_norm, grad_scale)
         groups: dict = {}  # one call for each pair of types, device and step count
         for i, p in enumerate(self.params):
             if p.grad is None:
@@ -74,6 +80,7 @@ class AdamW:
             for i in at:
                 self.state[i]["step"] = t
         self.steps += 1
+        return None if norm is None else norm[0]
 
     def zero_grad(self, set_to_none: bool = True) -> None:
         for p in self.params:

@@ -14,6 +14,7 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "librgc.so")
 LISTS_PATH = os.path.join(PKG_DIR, "_rgc_lists.so")
 SOURCES = ["rgc_sketch.hip", "rgc_apply.hip", "rgc_projection.hip", "rgc_linear.hip", "rgc_loss.hip", "rgc_norm.hip", "rgc_adamw.hip",
+           "rgc_clip.hip", "rgc_logits.hip",
            "rgc_abi.cpp"]
 
 # -ffp-contract=off: the update's pre-rounding value w - s*h and the Box-Muller

@@ -1,0 +1,24 @@
+"""Clipping of all dense gradients by their global norm."""
+from __future__ import annotations
+
+import torch
+
+from . import rgc
+
+
+@torch.no_grad()
+def clip_grad_norm(params, max_norm: float) -> torch.Tensor:
+    """Multiplies the parameters' gradients, in place, by min(1, max_norm / norm) and
+    returns their norm (a scalar on the device; nothing waits for it). A norm that is not
+    finite leaves the gradients as they are. Where AdamW takes the gradients
+    next, its step(max_norm=...) clips them as it reads them instead."""
+    grads, seen = [], set()
+    for p in [params] if torch.is_tensor(params) else params:
+        if p.grad is not None and id(p) not in seen:
+            seen.add(id(p))
+            grads.append(p.grad)
+    if not grads:
+        return torch.zeros(())
+    norm, scale = rgc.rgc_grad_norm_batch(grads, max_norm)
+    rgc.rgc_scale_batch(grads, scale)
+    return norm[0]

@@ -66,6 +66,55 @@ PyObject* pack(PyObject*, PyObject* args) {
   return Py_BuildValue("(NNsi)", pointers, counts, c10::toString(type), device.is_cuda() ? (int)device.index() : -1);
 }
 
+// pack_gradients(tensors) -> (pointers, sizes, types, bytes, device index)
+//   tensors: a list or tuple of dense tensors on one device, each bf16 (type 0) or float32 (1)
+// pointers and sizes as above, types: bytes of int32, bytes: of int64, each tensor's. None instead of the tuple if the tensors are not as described.
+PyObject* pack_gradients(PyObject*, PyObject* list) {
+  PyObject* fast = PySequence_Fast(list, "a list of tensors is wanted");
+  if (!fast) return nullptr;
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
+  PyObject* pointers = PyBytes_FromStringAndSize(nullptr, n * 8);
+  PyObject* counts = PyBytes_FromStringAndSize(nullptr, n * 8);
+  PyObject* types = PyBytes_FromStringAndSize(nullptr, n * 4);
+  PyObject* lengths = PyBytes_FromStringAndSize(nullptr, n * 8);
+  if (!pointers || !counts || !types || !lengths) {
+    Py_XDECREF(pointers), Py_XDECREF(counts), Py_XDECREF(types), Py_XDECREF(lengths), Py_DECREF(fast);
+    return nullptr;
+  }
+  uint64_t* p = reinterpret_cast<uint64_t*>(PyBytes_AS_STRING(pointers));
+  int64_t* c = reinterpret_cast<int64_t*>(PyBytes_AS_STRING(counts));
+  int32_t* k = reinterpret_cast<int32_t*>(PyBytes_AS_STRING(types));
+  int64_t* b = reinterpret_cast<int64_t*>(PyBytes_AS_STRING(lengths));
+  at::Device device(at::kCPU);
+  bool good = n > 0;
+  try {
+    for (Py_ssize_t i = 0; good && i < n; ++i) {
+      PyObject* o = PySequence_Fast_GET_ITEM(fast, i);
+      good = THPVariable_Check(o);
+      if (!good) break;
+      const at::Tensor& t = THPVariable_Unpack(o);
+      good = t.defined() && t.layout() == at::kStrided;
+      if (!good) break;
+      if (i == 0) device = t.device();
+      const at::ScalarType type = t.scalar_type();
+      good = (type == at::kBFloat16 || type == at::kFloat) && t.device() == device && t.is_contiguous();
+      if (!good) break;
+      c[i] = t.numel();
+      k[i] = type == at::kFloat;
+      b[i] = c[i] * (type == at::kFloat ? 4 : 2);
+      p[i] = reinterpret_cast<uint64_t>(t.data_ptr());
+    }
+  } catch (const std::exception&) {  // e.g. a tensor without storage
+    good = false;
+  }
+  Py_DECREF(fast);
+  if (!good) {
+    Py_DECREF(pointers), Py_DECREF(counts), Py_DECREF(types), Py_DECREF(lengths);
+    Py_RETURN_NONE;
+  }
+  return Py_BuildValue("(NNNNi)", pointers, counts, types, lengths, device.is_cuda() ? (int)device.index() : -1);
+}
+
 struct Range {
   uint64_t from, to;
   bool operator<(const Range& other) const { return from < other.from; }
@@ -120,6 +169,7 @@ PyObject* disjoint(PyObject*, PyObject* args) {
 
 PyMethodDef kMethods[] = {
     {"pack", pack, METH_VARARGS, "Addresses and sizes of a list of dense tensors of one type and device, or None."},
+    {"pack_gradients", pack_gradients, METH_O, "Addresses, sizes, types and bytes of a list of dense bf16 and float32 tensors, or None."},
     {"disjoint", disjoint, METH_VARARGS, "Whether no written range meets another or a read one."},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -1,0 +1,524 @@
+// Log probabilities of given tokens, entropies and the most likely alternatives
+// of rows of logits, and the gradient of the first two.
+//
+//   lse = m + log s,  s = sum exp(z - m),  m = max z
+//   logp = z_y - m - log s,  H = log s - q / s,  q = sum exp(z - m) (z - m)
+//   dz_v = p_v (-gl - ge (z_v - lse + H)) + gl [v = y],  p = exp(z - lse)
+//
+// Entries of -inf have no probability: they add nothing to s and q and get no
+// gradient. A row of nothing else has lse = -inf, a log probability of -inf, an
+// entropy of 0 and no gradient. NaN and +inf make their row NaN.
+//
+// Both directions are bound by memory: the forward reads a row once, the
+// backward reads and writes it once.
+//
+// The backward's z - lse loses log s where lse is large (a row of the type's
+// lowest value throughout: its probabilities would be 1 each). From |lse| = 1024 on, where
+// half a step of lse is 2^-15, it makes m and log s anew and takes z - m - log s.
+//
+// Forward: a workgroup takes a row, or one of several parts of it where there are
+// few rows; a second launch then joins the parts. Every thread keeps its own
+// maximum and its two sums against it, brought to the new maximum once for every
+// batch of vectors it reads.
+//
+// Alternatives: each wave holds the largest entries it has met, in descending
+// order, one to a lane, as 64-bit keys: the value's bits in an order of unsigned
+// numbers, then the complement of the index, so that no two keys are equal and of equal
+// values the lowest index comes first. An entry is looked at only if it
+// reaches the threshold, the largest of the waves' `top`th keys, so that a row of n
+// entries makes about top (1 + log(n / top)) insertions in all: each a ballot for the
+// place and a shift by a lane. The first batch would insert nearly everything; its
+// threshold comes from the lanes' maxima, of which `top` lie at or above a number
+// found bit by bit. At the end the waves' lists are merged, two sorted lists of 64 at a time.
+#include <math.h>
+
+#include "rgc_internal.hpp"
+
+namespace rgc {
+namespace {
+
+constexpr int64_t kLpMaxVocab = int64_t(1) << 24;
+constexpr int64_t kLpMaxRows = int64_t(1) << 31;
+constexpr int64_t kLpMaxLeadingDim = int64_t(1) << 31;
+constexpr int kLpMaxTop = 64;
+constexpr int kLpThreads = 256;
+constexpr int kLpWaves = kLpThreads / 64;
+constexpr int kLpBatch = 4;                              // vectors of eight that a thread reads together
+constexpr int kLpRound = kLpThreads * 8 * kLpBatch;      // entries of a workgroup's batch
+constexpr int64_t kLpMaxParts = 64;
+constexpr float kLpFloor = -200.f;  // least z - m in a product with its exponential, which is 0 from -104 on
+constexpr float kLpFar = 1024.f;       // of lse: see above
+constexpr float kLpLog2e = 1.4426950408889634f;
+
+typedef unsigned long long u64;
+
+struct LpArgs {
+  const void* z;
+  int64_t ldz, rows;
+  int V, top;
+  int parts;           // of a row
+  int part;            // entries of a part, a multiple of 8
+  const int64_t* tokens;
+  float* logp;
+  float* entropy;
+  float* lse;
+  float* top_logp;
+  int64_t* top_ids;
+  f32x4_t* sums;       // parts > 1: (m, s, q) of each
+  u64* keys;           // parts > 1: top of each
+  // backward
+  void* dz;
+  int64_t lddz;
+  const float* grad_logp;
+  const float* grad_entropy;
+};
+
+__device__ __forceinline__ float lp_exp(float x) { return __builtin_amdgcn_exp2f(x * kLpLog2e); }
+
+// Eight logits as loaded.
+template <typename ZT>
+struct LpVec;
+template <>
+struct LpVec<uint16_t> {
+  typedef u32x4v_t any_t __attribute__((aligned(2)));
+  u32x4v_t v;
+  __device__ __forceinline__ void none() { v = u32x4v_t{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u}; }
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const any_t*>(p); }
+  __device__ __forceinline__ void load_some(const uint16_t* p, int count) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < count) v[i / 2] = i & 1 ? (v[i / 2] & 0xFFFFu) | (uint32_t)p[i] << 16 : (v[i / 2] & 0xFFFF0000u) | p[i];
+  }
+  __device__ __forceinline__ float get(int i) const { return __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16); }
+  static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_bits_to_f32(*p); }
+  static __device__ __forceinline__ void store(uint16_t* p, const float (&f)[8]) {
+    *reinterpret_cast<any_t*>(p) = u32x4v_t{f32x2_to_bf16x2_rne(f[0], f[1]), f32x2_to_bf16x2_rne(f[2], f[3]),
+                                            f32x2_to_bf16x2_rne(f[4], f[5]), f32x2_to_bf16x2_rne(f[6], f[7])};
+  }
+  static __device__ __forceinline__ void put(uint16_t* p, float f) { *p = (uint16_t)f32_to_bf16_rne(f); }
+};
+template <>
+struct LpVec<float> {
+  typedef f32x4_t any_t __attribute__((aligned(4)));
+  f32x4_t a, b;
+  __device__ __forceinline__ void none() { a = b = f32x4_t{-INFINITY, -INFINITY, -INFINITY, -INFINITY}; }
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const any_t*>(p)[0];
+    b = reinterpret_cast<const any_t*>(p)[1];
+  }
+  __device__ __forceinline__ void load_some(const float* p, int count) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < count) (i < 4 ? a : b)[i & 3] = p[i];
+  }
+  __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
+  static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
+    reinterpret_cast<any_t*>(p)[0] = f32x4_t{f[0], f[1], f[2], f[3]};
+    reinterpret_cast<any_t*>(p)[1] = f32x4_t{f[4], f[5], f[6], f[7]};
+  }
+  static __device__ __forceinline__ void put(float* p, float f) { *p = f; }
+};
+
+// The value's bits in an order of unsigned numbers: -0 is 0, and every NaN lies above infinity.
+__device__ __forceinline__ uint32_t order_of(float z) {
+  const uint32_t b = __float_as_uint(z + 0.f);
+  const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
+  return __builtin_isnan(z) ? 0xFFFFFFFFu : o;
+}
+__device__ __forceinline__ float value_of(uint32_t order) {
+  return __uint_as_float(order & 0x80000000u ? order ^ 0x80000000u : ~order);
+}
+__device__ __forceinline__ u64 key_of(float z, int index) { return (u64)order_of(z) << 32 | (uint32_t)~index; }
+
+__device__ __forceinline__ u64 read_lane(u64 v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane), hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+  return (u64)hi << 32 | lo;
+}
+
+// The 64 largest of two descending lists, in descending order: the pairwise
+// larger of one list and the other backwards, which rise and fall once, sorted by halving distances.
+__device__ __forceinline__ u64 merge_lists(u64 mine, u64 backwards) {
+  u64 v = mine > backwards ? mine : backwards;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const u64 other = __shfl_xor(v, off, 64);
+    const bool upper = lane & off, greater = v > other;
+    v = upper != greater ? v : other;
+  }
+  return v;
+}
+
+// Joins (m, s, q) with another's: all sums against the larger maximum.
+__device__ __forceinline__ void join_sums(float& m, float& s, float& q, float m1, float s1, float q1) {
+  const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.f : top;
+  const float d0 = m - base, d1 = m1 - base, f0 = lp_exp(d0), f1 = lp_exp(d1);
+  q = __builtin_fmaf(s, fmaxf(d0, kLpFloor), q) * f0 + __builtin_fmaf(s1, fmaxf(d1, kLpFloor), q1) * f1;
+  s = s * f0 + s1 * f1;
+  m = top;
+}
+
+// What a row gives, from its sums in every lane and its list, one key to a lane.
+template <typename ZT>
+__device__ __forceinline__ void finish_row(const LpArgs& a, int64_t row, float m, float s, float q, u64 list) {
+  const int lane = threadIdx.x & 63;
+  const bool empty = m == -INFINITY && s == 0.f;
+  const float ls = logf(s), lse = empty ? -INFINITY : m + ls;
+  if (lane == 0) {
+    a.lse[row] = lse;
+    float h = ls - q / s;
+    h = empty || h < 0.f ? 0.f : h;  // (rounding can take it below 0; NaN stays)
+    if (a.tokens) {
+      const int64_t y = a.tokens[row];
+      const bool live = y >= 0 && y < a.V;
+      const float zy = live ? LpVec<ZT>::one(static_cast<const ZT*>(a.z) + row * a.ldz + y) : 0.f;
+      a.logp[row] = live ? (empty ? -INFINITY : zy - m - ls) : 0.f;
+      if (!live) h = 0.f;
+    }
+    a.entropy[row] = h;
+  }
+  if (lane < a.top) {
+    const float z = value_of((uint32_t)(list >> 32));
+    a.top_logp[row * a.top + lane] = empty ? -INFINITY : z - m - ls;
+    a.top_ids[row * a.top + lane] = (uint32_t)~(uint32_t)list;
+  }
+}
+
+template <typename ZT, bool TOP>
+__global__ __launch_bounds__(kLpThreads) void lp_forward_kernel(LpArgs a) {
+  __shared__ u64 lists[kLpWaves][64];
+  __shared__ f32x4_t sums[kLpWaves];
+  __shared__ u64 bar;  // the largest of the waves' thresholds: a key at or below it is not among the row's `top`
+  const int lane = threadIdx.x & 63, wave = wave_index();
+  const int64_t jobs = a.rows * a.parts;
+  for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+    const int64_t row = job / a.parts;
+    const int first = (int)(job - row * a.parts) * a.part;
+    const int end = a.V - first < a.part ? a.V : first + a.part;
+    const ZT* z = static_cast<const ZT*>(a.z) + row * a.ldz;
+    float m = -INFINITY, s = 0.f, q = 0.f;
+    u64 list = 0, limit = 0;  // limit: this wave's view of the bar
+    if (TOP) {
+      if (threadIdx.x == 0) bar = 0;
+      __syncthreads();
+    }
+    for (int c0 = first; c0 < end; c0 += kLpRound) {
+      LpVec<ZT> v[kLpBatch];
+      const int c = c0 + 8 * (int)threadIdx.x;
+      if (c0 + kLpRound <= end) {
+#pragma unroll
+        for (int u = 0; u < kLpBatch; ++u) v[u].load(z + c + u * (8 * kLpThreads));
+      } else {
+#pragma unroll
+        for (int u = 0; u < kLpBatch; ++u) {
+          const int at = c + u * (8 * kLpThreads);
+          v[u].none();
+          if (at + 8 <= end) v[u].load(z + at);
+          else if (at < end) v[u].load_some(z + at, end - at);
+        }
+      }
+      float high[kLpBatch], batch = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kLpBatch; ++u) {
+        high[u] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) high[u] = fmaxf(high[u], v[u].get(e));
+        batch = fmaxf(batch, high[u]);
+      }
+      {
+        const float top = fmaxf(m, batch), base = top == -INFINITY ? 0.f : top;
+        const float d0 = m - base, f0 = lp_exp(d0);
+        q = __builtin_fmaf(s, fmaxf(d0, kLpFloor), q) * f0;
+        s *= f0;
+        m = top;
+#pragma unroll
+        for (int u = 0; u < kLpBatch; ++u) {
+          float s8 = 0.f, q8 = 0.f;  // (short sums first: a thread adds thousands)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float d = v[u].get(e) - base, p = lp_exp(d);
+            s8 += p;
+            q8 = __builtin_fmaf(p, fmaxf(d, kLpFloor), q8);
+          }
+          s += s8;
+          q += q8;
+        }
+      }
+      if constexpr (TOP) {
+        if (c0 == first) {
+          // the largest number of sixteen bits that `top` of the lanes' maxima reach
+          const uint32_t mine = order_of(batch) >> 16;
+          uint32_t reach = 0;
+#pragma unroll
+          for (int bit = 15; bit >= 0; --bit) {
+            const uint32_t t = reach | 1u << bit;
+            if (__builtin_popcountll(__ballot(mine >= t)) >= a.top) reach = t;
+          }
+          limit = reach ? ((u64)reach << 48) - 1 : 0;
+          if (lane == 0 && limit) atomicMax(&bar, limit);
+        }
+        {
+          const u64 seen = *(volatile u64*)&bar;
+          limit = seen > limit ? seen : limit;
+          limit = uniform_u64(limit);
+        }
+        const u64 before = limit;
+        float reach = limit ? value_of((uint32_t)(limit >> 32)) : -INFINITY;  // (a NaN where the limit is one)
+        const bool odd = !(s - s == 0.f);  // NaN or infinities among this thread's entries
+#pragma unroll
+        for (int u = 0; u < kLpBatch; ++u) {
+          if (!__any(odd || !(high[u] < reach))) continue;
+          const int at = c + u * (8 * kLpThreads);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = v[u].get(e);
+            if (!__any(!(x < reach))) continue;
+            const u64 key = at + e < end ? key_of(x, at + e) : 0;
+            u64 todo = __ballot(key > limit);
+            while (todo) {
+              const int from = __builtin_ctzll(todo);
+              const u64 k = read_lane(key, from);
+              const int place = __builtin_popcountll(__ballot(list > k));
+              const u64 above = __shfl_up(list, 1, 64);
+              list = lane < place ? list : lane == place ? k : above;
+              const u64 last = read_lane(list, a.top - 1);
+              limit = last > limit ? last : limit;
+              todo &= todo - 1;
+              todo &= __ballot(key > limit);
+            }
+            reach = limit ? value_of((uint32_t)(limit >> 32)) : -INFINITY;
+          }
+        }
+        if (lane == 0 && limit > before) atomicMax(&bar, limit);
+      }
+    }
+    // the lanes' sums, then the waves'
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+      join_sums(m, s, q, __shfl_xor(m, off, 64), __shfl_xor(s, off, 64), __shfl_xor(q, off, 64));
+    if (lane == 0) sums[wave] = f32x4_t{m, s, q, 0.f};
+    if (TOP) lists[wave][lane] = list;
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int w = 1; w < kLpWaves; ++w) {
+        join_sums(m, s, q, sums[w].x, sums[w].y, sums[w].z);
+        if (TOP) list = merge_lists(list, lists[w][63 - lane]);
+      }
+      if (a.parts == 1) {
+        finish_row<ZT>(a, row, m, s, q, list);
+      } else {
+        if (lane == 0) a.sums[job] = f32x4_t{m, s, q, 0.f};
+        if (TOP && lane < a.top) a.keys[job * a.top + lane] = list;
+      }
+    }
+    __syncthreads();  // before the next row's bar, sums and lists
+  }
+}
+
+// Joins a row's parts: a wave per row.
+template <typename ZT, bool TOP>
+__global__ __launch_bounds__(64) void lp_join_kernel(LpArgs a) {
+  const int lane = threadIdx.x;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    float m = -INFINITY, s = 0.f, q = 0.f;
+    if (lane < a.parts) {
+      const f32x4_t x = a.sums[row * a.parts + lane];
+      m = x.x, s = x.y, q = x.z;
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+      join_sums(m, s, q, __shfl_xor(m, off, 64), __shfl_xor(s, off, 64), __shfl_xor(q, off, 64));
+    u64 list = 0;
+    if constexpr (TOP) {
+      const u64* keys = a.keys + row * a.parts * a.top;
+      for (int p = 0; p < a.parts; ++p) {
+        const int back = 63 - lane;
+        list = merge_lists(list, back < a.top ? keys[(int64_t)p * a.top + back] : 0);
+      }
+    }
+    finish_row<ZT>(a, row, m, s, q, list);
+  }
+}
+
+// What the entries of a row need for their gradients.
+struct LpRow {
+  float base, ls;  // z - base - ls is the log probability
+  float gl, flat, slope;
+  int64_t y;
+  bool live;
+};
+
+// A batch of a row's gradients, from entry c0 on.
+template <typename ZT>
+__device__ __forceinline__ void backward_batch(const ZT* z, ZT* dz, int V, int c0, const LpRow& r) {
+  const int c = c0 + 8 * (int)threadIdx.x;
+  LpVec<ZT> v[kLpBatch];
+#pragma unroll
+  for (int u = 0; u < kLpBatch; ++u) {
+    const int at = c + u * (8 * kLpThreads);
+    v[u].none();
+    if (r.live && at + 8 <= V) v[u].load(z + at);
+    else if (r.live && at < V) v[u].load_some(z + at, V - at);
+  }
+#pragma unroll
+  for (int u = 0; u < kLpBatch; ++u) {
+    const int at = c + u * (8 * kLpThreads);
+    if (at >= V) continue;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = v[u].get(e) - r.base - r.ls;
+      f[e] = lp_exp(d) * __builtin_fmaf(r.slope, fmaxf(d, kLpFloor), r.flat);
+      if (at + e == r.y) f[e] += r.gl;
+      if (!r.live) f[e] = 0.f;
+    }
+    if (at + 8 <= V) {
+      LpVec<ZT>::store(dz + at, f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (at + e < V) LpVec<ZT>::put(dz + at + e, f[e]);
+    }
+  }
+}
+
+template <typename ZT>
+__global__ __launch_bounds__(kLpThreads) void lp_backward_kernel(LpArgs a) {
+  __shared__ float2 sums[kLpWaves];
+  const int64_t parts = (a.V + kLpRound - 1) / kLpRound, jobs = a.rows * parts;
+  for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+    const int64_t row = job / parts;
+    const int c0 = (int)(job - row * parts) * kLpRound;
+    const ZT* z = static_cast<const ZT*>(a.z) + row * a.ldz;
+    ZT* dz = static_cast<ZT*>(a.dz) + row * a.lddz;
+    LpRow r;
+    r.y = a.tokens[row];
+    r.base = a.lse[row], r.ls = 0.f;
+    r.live = r.y >= 0 && r.y < a.V && r.base != -INFINITY;
+    const float ge = a.grad_entropy ? a.grad_entropy[row] : 0.f;
+    r.gl = a.grad_logp ? a.grad_logp[row] : 0.f;
+    r.flat = ge != 0.f ? -__builtin_fmaf(ge, a.entropy[row], r.gl) : -r.gl, r.slope = -ge;
+    if (!(r.live && fabsf(r.base) >= kLpFar && r.base != INFINITY)) {
+      backward_batch(z, dz, a.V, c0, r);
+      continue;
+    }
+    // a far row is one workgroup's (dz may be z: nobody else may write it before it is read)
+    if (c0 > 0) continue;
+    float m = -INFINITY, s = 0.f, q = 0.f;
+    for (int at = threadIdx.x; at < a.V; at += kLpThreads) m = fmaxf(m, LpVec<ZT>::one(z + at));
+    for (int at = threadIdx.x; at < a.V; at += kLpThreads) s += lp_exp(LpVec<ZT>::one(z + at) - (m == -INFINITY ? 0.f : m));
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) join_sums(m, s, q, __shfl_xor(m, off, 64), __shfl_xor(s, off, 64), 0.f);
+    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = make_float2(m, s);
+    __syncthreads();
+    m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kLpWaves; ++w) join_sums(m, s, q, sums[w].x, sums[w].y, 0.f);
+    r.base = m, r.ls = logf(s);
+    for (int at = 0; at < a.V; at += kLpRound) backward_batch(z, dz, a.V, at, r);
+    __syncthreads();  // before the next far row's sums
+  }
+}
+
+size_t elem(rgc_dtype_t t) { return t == RGC_F32 ? 4 : 2; }
+
+// Parts of a row of the forward: one where there are rows enough for eight workgroups to
+// each compute unit, else as many as make that, of at least half a batch.
+int64_t parts_of(int64_t rows, int64_t V) {
+  const int64_t want = ((int64_t)device_compute_units() * 8 + rows - 1) / rows;
+  const int64_t most = (V + kLpRound / 2 - 1) / (kLpRound / 2);
+  int64_t parts = want < most ? want : most;
+  if (parts > kLpMaxParts) parts = kLpMaxParts;
+  return parts < 1 ? 1 : parts;
+}
+int64_t part_of(int64_t V, int64_t parts) { return ((V + parts - 1) / parts + 7) / 8 * 8; }
+
+size_t sums_bytes(int64_t rows, int64_t parts) { return ((size_t)rows * parts * sizeof(f32x4_t) + 255) / 256 * 256; }
+
+rgc_status_t check_shape(rgc_dtype_t zt, int64_t rows, int64_t V, int64_t top) {
+  if (zt != RGC_BF16 && zt != RGC_F32) return RGC_ERR_UNSUPPORTED;
+  if (rows < 0 || V <= 0 || top < 0 || top > V) return RGC_ERR_SHAPE;
+  if (rows > kLpMaxRows || V > kLpMaxVocab || top > kLpMaxTop) return RGC_ERR_UNSUPPORTED;
+  return RGC_OK;
+}
+rgc_status_t check_rows(const void* p, int64_t ld, int64_t V, rgc_dtype_t t) {
+  if (!p) return RGC_ERR_NULL;
+  if (ld < V) return RGC_ERR_SHAPE;
+  if (ld > kLpMaxLeadingDim) return RGC_ERR_UNSUPPORTED;
+  if (!aligned_to(p, elem(t))) return RGC_ERR_ALIGN;
+  return RGC_OK;
+}
+
+unsigned grid_of(int64_t jobs) {
+  const int64_t most = int64_t(1) << 20;  // (launches stay below 2^31 threads)
+  return (unsigned)(jobs < most ? jobs : most);
+}
+
+template <typename ZT, bool TOP>
+rgc_status_t forward_launch(const LpArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((lp_forward_kernel<ZT, TOP>), dim3(grid_of(a.rows * a.parts)), dim3(kLpThreads), 0, s, a);
+  if (a.parts > 1) hipLaunchKernelGGL((lp_join_kernel<ZT, TOP>), dim3(grid_of(a.rows)), dim3(64), 0, s, a);
+  return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP;
+}
+
+}  // namespace
+}  // namespace rgc
+
+using namespace rgc;
+
+extern "C" size_t rgc_log_prob_forward_workspace_size(int64_t rows, int64_t V, int64_t top) {
+  if (check_shape(RGC_BF16, rows, V, top) != RGC_OK || rows == 0) return 0;
+  const int64_t parts = parts_of(rows, V);
+  return parts == 1 ? 0 : sums_bytes(rows, parts) + (size_t)(rows * parts * top) * sizeof(u64);
+}
+
+extern "C" rgc_status_t rgc_log_prob_forward(rgc_dtype_t zt, const void* Z, int64_t ldz, const int64_t* tokens, float* logp,
+                                             float* entropy, float* lse, int64_t top, float* top_logp, int64_t* top_ids,
+                                             int64_t rows, int64_t V, void* ws, size_t ws_bytes, void* stream) {
+  rgc_status_t st = check_shape(zt, rows, V, top);
+  if (st != RGC_OK || rows == 0) return st;
+  if ((st = check_rows(Z, ldz, V, zt)) != RGC_OK) return st;
+  if (!entropy || !lse || (tokens && !logp) || (top > 0 && (!top_logp || !top_ids))) return RGC_ERR_NULL;
+  if (!aligned_to(tokens, 8) || !aligned_to(logp, 4) || !aligned_to(entropy, 4) || !aligned_to(lse, 4) ||
+      !aligned_to(top_logp, 4) || !aligned_to(top_ids, 8))
+    return RGC_ERR_ALIGN;
+  const size_t need = rgc_log_prob_forward_workspace_size(rows, V, top);
+  if (need > 0 && (!ws || ws_bytes < need)) return RGC_ERR_WORKSPACE;
+  if (!aligned_to(ws, 256)) return RGC_ERR_ALIGN;
+  LpArgs a{};
+  a.z = Z, a.ldz = ldz, a.rows = rows, a.V = (int)V, a.top = (int)top;
+  a.parts = (int)parts_of(rows, V), a.part = (int)part_of(V, a.parts);
+  a.tokens = tokens, a.logp = logp, a.entropy = entropy, a.lse = lse, a.top_logp = top_logp, a.top_ids = top_ids;
+  if (a.parts > 1) {
+    a.sums = static_cast<f32x4_t*>(ws);
+    a.keys = reinterpret_cast<u64*>(static_cast<char*>(ws) + sums_bytes(rows, a.parts));
+  }
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (zt == RGC_F32) return top > 0 ? forward_launch<float, true>(a, s) : forward_launch<float, false>(a, s);
+  return top > 0 ? forward_launch<uint16_t, true>(a, s) : forward_launch<uint16_t, false>(a, s);
+}
+
+extern "C" rgc_status_t rgc_log_prob_backward(rgc_dtype_t zt, const void* Z, int64_t ldz, const int64_t* tokens,
+                                              const float* lse, const float* entropy, const float* grad_logp,
+                                              const float* grad_entropy, void* dZ, int64_t lddz, int64_t rows, int64_t V,
+                                              void* stream) {
+  rgc_status_t st = check_shape(zt, rows, V, 0);
+  if (st != RGC_OK || rows == 0) return st;
+  if ((st = check_rows(Z, ldz, V, zt)) != RGC_OK) return st;
+  if ((st = check_rows(dZ, lddz, V, zt)) != RGC_OK) return st;
+  if (!tokens || !lse || (!grad_logp && !grad_entropy) || (grad_entropy && !entropy)) return RGC_ERR_NULL;
+  if (!aligned_to(tokens, 8) || !aligned_to(lse, 4) || !aligned_to(entropy, 4) || !aligned_to(grad_logp, 4) ||
+      !aligned_to(grad_entropy, 4))
+    return RGC_ERR_ALIGN;
+  LpArgs a{};
+  a.z = Z, a.ldz = ldz, a.rows = rows, a.V = (int)V, a.tokens = tokens, a.dz = dZ, a.lddz = lddz;
+  a.lse = const_cast<float*>(lse), a.entropy = const_cast<float*>(entropy);
+  a.grad_logp = grad_logp, a.grad_entropy = grad_entropy;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const unsigned grid = grid_of(rows * ((V + kLpRound - 1) / kLpRound));
+  if (zt == RGC_F32) hipLaunchKernelGGL(lp_backward_kernel<float>, dim3(grid), dim3(kLpThreads), 0, s, a);
+  else hipLaunchKernelGGL(lp_backward_kernel<uint16_t>, dim3(grid), dim3(kLpThreads), 0, s, a);
+  return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP;
+}

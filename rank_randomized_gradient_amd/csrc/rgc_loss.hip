@@ -65,8 +65,11 @@ struct CeArgs {
   CeGrid grid;
   float2* part;        // forward: (maximum, sum) of each tile row, [tile column][token]
   float* zt;           // forward: the target's logit
+  float* part_q;       // log probabilities: each tile row's third sum
   const float* lse;    // backward
-  const float* grad;
+  const float* grad;   // of the losses, or of the log probabilities (then null stands for zeros)
+  const float* entropy;
+  const float* grad_entropy;  // log probabilities: or null, zeros
   uint16_t* hi;        // backward: T x ldd, bf16
   uint16_t* lo;        // or null: nothing takes D from here
   float* rest;         // with lo: D - hi - lo at each token's target
@@ -92,9 +95,19 @@ struct CeRows {
   float lse[kGtTile], grad[kGtTile];
   int at[kGtTile];  // the target's column in the tile; -1: elsewhere; -2: an ignored token
 };
+// D = p (flat + slope (z - lse)) + grad [v = y] of the log probabilities
+struct LpRows : CeRows {
+  float flat[kGtTile], slope[kGtTile];
+};
+template <bool LOGP>
+using RowsOf = std::conditional_t<LOGP, LpRows, CeRows>;
 
-template <typename Tile>
-__device__ __forceinline__ void load_rows(const CeArgs& a, int64_t m0, int64_t n0, bool backward, CeRows* r) {
+// Smallest z - lse (and difference of two maxima) that enters a product with its
+// exponential: that of what lies below, -inf among it, is 0, and 0 times it must be 0.
+constexpr float kLogFloor = -200.f;
+
+template <typename Tile, bool LOGP>
+__device__ __forceinline__ void load_rows(const CeArgs& a, int64_t m0, int64_t n0, bool backward, RowsOf<LOGP>* r) {
   const int row = threadIdx.x;
   if (row >= Tile::kRows) return;
   const bool live = m0 + row < a.T;
@@ -102,7 +115,12 @@ __device__ __forceinline__ void load_rows(const CeArgs& a, int64_t m0, int64_t n
   r->at[row] = y < 0 || y >= a.vocab ? -2 : c >= 0 && c < Tile::kCols ? (int)c : -1;
   if (backward) {
     r->lse[row] = live ? a.lse[m0 + row] : 0.f;
-    r->grad[row] = live ? a.grad[m0 + row] : 0.f;
+    r->grad[row] = live && (!LOGP || a.grad) ? a.grad[m0 + row] : 0.f;
+    if constexpr (LOGP) {
+      const float ge = live && a.grad_entropy ? a.grad_entropy[m0 + row] : 0.f;
+      r->slope[row] = -ge;
+      r->flat[row] = ge != 0.f ? -__builtin_fmaf(ge, a.entropy[m0 + row], r->grad[row]) : -r->grad[row];
+    }
   }
 }
 
@@ -110,16 +128,19 @@ __device__ __forceinline__ void load_rows(const CeArgs& a, int64_t m0, int64_t n
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // The tile of rows m0 .. and columns n0 .. of z, reduced to slot `column` of its rows.
-template <int MI, int NI, int STAGES>
-__device__ __forceinline__ void forward_tile(const CeArgs& a, int64_t m0, int64_t n0, int64_t column, char* smem, CeRows* rows) {
+// LOGP: with sum of exp(z - m) (z - m) beside the sum of exp(z - m), for the entropy.
+template <bool LOGP, int MI, int NI, int STAGES>
+__device__ __forceinline__ void forward_tile(const CeArgs& a, int64_t m0, int64_t n0, int64_t column, char* smem,
+                                             RowsOf<LOGP>* rows) {
   typedef GtTile<MI, NI, STAGES, false> Tile;
-  load_rows<Tile>(a, m0, n0, false, rows);
+  constexpr int kSums = LOGP ? 3 : 2;
+  load_rows<Tile, LOGP>(a, m0, n0, false, rows);
   Tile t;
   t.init(a.X + m0 * a.ldx, a.ldx, a.W + n0 * a.ldw, a.ldw, a.T - m0, a.V - n0, a.k, smem);
   t.run();
 
   const int g = t.lane >> 4, li = t.lane & 15, wm = t.wave & 1, wn = t.wave >> 1;
-  float* sums = reinterpret_cast<float*>(smem);  // [row][wn]: maximum, sum
+  float* sums = reinterpret_cast<float*>(smem);  // [row][wn]: maximum, sum, third sum
   const int first = 16 * NI * wn + 4 * g;
   const int width = (int)(a.V - n0 < Tile::kCols ? a.V - n0 : Tile::kCols);
 #pragma unroll
@@ -148,28 +169,44 @@ __device__ __forceinline__ void forward_tile(const CeArgs& a, int64_t m0, int64_
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const float base = top == -INFINITY ? 0.f : top;
-    float s = 0.f;
+    float s = 0.f, q = 0.f;
 #pragma unroll
     for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s += fast_exp(t.acc[mt][nt][e] - base);
+      for (int e = 0; e < 4; ++e) {
+        const float d = t.acc[mt][nt][e] - base, p = fast_exp(d);
+        s += p;
+        if constexpr (LOGP) q = __builtin_fmaf(p, fmaxf(d, kLogFloor), q);
+      }
     s += __shfl_xor(s, 16, 64);
     s += __shfl_xor(s, 32, 64);
+    if constexpr (LOGP) {
+      q += __shfl_xor(q, 16, 64);
+      q += __shfl_xor(q, 32, 64);
+    }
     if (g == 0) {
-      sums[8 * row + 2 * wn] = top;
-      sums[8 * row + 2 * wn + 1] = s;
+      float* slot = sums + kSums * (4 * row + wn);
+      slot[0] = top;
+      slot[1] = s;
+      if constexpr (LOGP) slot[2] = q;
     }
   }
   __syncthreads();
   const int row = threadIdx.x;
   if (row < Tile::kRows && m0 + row < a.T) {
-    float top = sums[8 * row], s = 0.f;
+    const float* slot = sums + 4 * kSums * row;
+    float top = slot[0], s = 0.f, q = 0.f;
 #pragma unroll
-    for (int w = 1; w < 4; ++w) top = fmaxf(top, sums[8 * row + 2 * w]);
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, slot[kSums * w]);
     const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) s += sums[8 * row + 2 * w + 1] * fast_exp(sums[8 * row + 2 * w] - base);
+    for (int w = 0; w < 4; ++w) {
+      const float d = slot[kSums * w] - base, f = fast_exp(d), sw = slot[kSums * w + 1];
+      s += sw * f;
+      if constexpr (LOGP) q = __builtin_fmaf(__builtin_fmaf(sw, fmaxf(d, kLogFloor), slot[kSums * w + 2]), f, q);
+    }
     a.part[column * a.T + m0 + row] = make_float2(top, s);
+    if constexpr (LOGP) a.part_q[column * a.T + m0 + row] = q;
   }
 }
 
@@ -200,6 +237,37 @@ __global__ __launch_bounds__(1024) void ce_finish_kernel(CeArgs a, float* loss, 
     const int64_t y = a.targets[t];
     lse[t] = l;
     loss[t] = y >= 0 && y < a.vocab ? l - a.zt[t] : 0.f;
+  }
+}
+
+// The same join for log probabilities, with the third sums:
+//   H = lse - sum p z = log s - q / s,  s = sum exp(z - m), q = sum exp(z - m) (z - m)
+__global__ __launch_bounds__(1024) void lp_finish_kernel(CeArgs a, float* logp, float* entropy, float* lse) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6);
+  if (t >= a.T) return;
+  float top = -INFINITY, s = 0.f, q = 0.f;
+  const auto join = [&](float x, float y, float z) {
+    const float m = fmaxf(top, x), base = m == -INFINITY ? 0.f : m;
+    const float d0 = top - base, d1 = x - base, f0 = fast_exp(d0), f1 = fast_exp(d1);
+    q = __builtin_fmaf(s, fmaxf(d0, kLogFloor), q) * f0 + __builtin_fmaf(y, fmaxf(d1, kLogFloor), z) * f1;
+    s = s * f0 + y * f1;
+    top = m;
+  };
+#pragma unroll 4
+  for (int64_t j = lane; j < a.grid.ntiles; j += 64) {
+    const float2 p = a.part[j * a.T + t];
+    join(p.x, p.y, a.part_q[j * a.T + t]);
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) join(__shfl_xor(top, off, 64), __shfl_xor(s, off, 64), __shfl_xor(q, off, 64));
+  if (lane == 0) {
+    const float l = top + logf(s), h = logf(s) - q / s;
+    const int64_t y = a.targets[t];
+    const bool live = y >= 0 && y < a.vocab;
+    lse[t] = l;
+    logp[t] = live ? a.zt[t] - l : 0.f;
+    entropy[t] = live ? (h < 0.f ? 0.f : h) : 0.f;  // (rounding can take it below 0; NaN stays)
   }
 }
 
@@ -268,11 +336,12 @@ __device__ __forceinline__ void sketch_tile(const CeArgs& a, const Tile& t, int6
 // whole rows (16-byte chunk q of row t at place q ^ (t % 16)). The
 // lo pass forms D - hi from the fp32 values, which stay in the registers. Without
 // lo (a fused sketch and no dX) nothing is stored.
-template <int MI, int NI, int STAGES>
-__device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, char* smem, CeRows* rows) {
+// LOGP: D of the log probabilities and entropies; all that follows is the same.
+template <bool LOGP, int MI, int NI, int STAGES>
+__device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, char* smem, RowsOf<LOGP>* rows) {
   typedef GtTile<MI, NI, STAGES, false> Tile;
   constexpr int kRowChunks = Tile::kCols / 8;  // 16-byte chunks of a row
-  load_rows<Tile>(a, m0, n0, true, rows);
+  load_rows<Tile, LOGP>(a, m0, n0, true, rows);
   Tile t;
   t.init(a.X + m0 * a.ldx, a.ldx, a.W + n0 * a.ldw, a.ldw, a.T - m0, a.V - n0, a.k, smem);
   t.run();
@@ -285,11 +354,14 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
     const int row = 16 * MI * wm + 16 * mt + li;
     const int target = rows->at[row], at = target - first;
     const float lse = rows->lse[row], gr = rows->grad[row];
+    float flat = 0.f, slope = 0.f;
+    if constexpr (LOGP) flat = rows->flat[row], slope = rows->slope[row];
 #pragma unroll
     for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float p = fast_exp(t.acc[mt][nt][e] - lse) * gr;
+        const float d = t.acc[mt][nt][e] - lse;
+        const float p = fast_exp(d) * (LOGP ? __builtin_fmaf(slope, fmaxf(d, kLogFloor), flat) : gr);
         t.acc[mt][nt][e] = target == -2 ? 0.f : p;
       }
     if (__any(at >= 0 && at < 16 * NI)) {
@@ -297,7 +369,7 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
       for (int nt = 0; nt < NI; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (16 * nt + e == at) t.acc[mt][nt][e] -= gr;
+          if (16 * nt + e == at) t.acc[mt][nt][e] += LOGP ? gr : -gr;
     }
     if (__builtin_expect(width < Tile::kCols, 0)) {
 #pragma unroll
@@ -356,16 +428,16 @@ __device__ __forceinline__ void d_tile(const CeArgs& a, int64_t m0, int64_t n0, 
 }
 
 // The logits' kernel of both directions: the tile of this workgroup.
-template <bool BACKWARD, bool FEW>
+template <bool BACKWARD, bool FEW, bool LOGP>
 __global__ __launch_bounds__(kGtThreads, FEW ? 4 : 1) void ce_logits_kernel(CeArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[FEW ? FlatTile::kLds : LargeTile::kLds];
-  __shared__ CeRows rows;
+  __shared__ RowsOf<LOGP> rows;
   int64_t i, j;
   if (!FEW && (int64_t)blockIdx.x < a.grid.large) {
     const int64_t columns = a.grid.split / kGtTile + (a.grid.split % kGtTile != 0);
     gt_place(gt_logical(blockIdx.x, a.grid.large), (a.T + kGtTile - 1) / kGtTile, columns, kCeDown, &i, &j);
-    if constexpr (BACKWARD) d_tile<8, 4, 2>(a, i * kGtTile, j * kGtTile, smem, &rows);
-    else forward_tile<8, 4, 2>(a, i * kGtTile, j * kGtTile, j, smem, &rows);
+    if constexpr (BACKWARD) d_tile<LOGP, 8, 4, 2>(a, i * kGtTile, j * kGtTile, smem, &rows);
+    else forward_tile<LOGP, 8, 4, 2>(a, i * kGtTile, j * kGtTile, j, smem, &rows);
     return;
   }
   typedef std::conditional_t<FEW, FlatTile, SmallTile> Tile;
@@ -374,23 +446,23 @@ __global__ __launch_bounds__(kGtThreads, FEW ? 4 : 1) void ce_logits_kernel(CeAr
            a.grid.ntiles - before, 2 * kCeDown, &i, &j);
   const int64_t m0 = i * Tile::kRows, n0 = a.grid.split + j * Tile::kCols;
   if constexpr (BACKWARD) {
-    if constexpr (FEW) d_tile<2, 2, 3>(a, m0, n0, smem, &rows);
-    else d_tile<4, 2, 4>(a, m0, n0, smem, &rows);
+    if constexpr (FEW) d_tile<LOGP, 2, 2, 3>(a, m0, n0, smem, &rows);
+    else d_tile<LOGP, 4, 2, 4>(a, m0, n0, smem, &rows);
   } else {
-    if constexpr (FEW) forward_tile<2, 2, 3>(a, m0, n0, before + j, smem, &rows);
-    else forward_tile<4, 2, 4>(a, m0, n0, before + j, smem, &rows);
+    if constexpr (FEW) forward_tile<LOGP, 2, 2, 3>(a, m0, n0, before + j, smem, &rows);
+    else forward_tile<LOGP, 4, 2, 4>(a, m0, n0, before + j, smem, &rows);
   }
 }
 
-template <bool BACKWARD>
+template <bool BACKWARD, bool LOGP>
 __global__ __launch_bounds__(kGtThreads, 4) void ce_pair_kernel(CeArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[PairTile::kLds];
-  __shared__ CeRows rows;
+  __shared__ RowsOf<LOGP> rows;
   int64_t i, j;
   gt_place(gt_logical(blockIdx.x, gridDim.x), (a.T + PairTile::kRows - 1) / PairTile::kRows, a.grid.ntiles, 2 * kCeDown, &i, &j);
   const int64_t m0 = i * PairTile::kRows, n0 = j * PairTile::kCols;
-  if constexpr (BACKWARD) d_tile<4, 2, 2>(a, m0, n0, smem, &rows);
-  else forward_tile<4, 2, 2>(a, m0, n0, j, smem, &rows);
+  if constexpr (BACKWARD) d_tile<LOGP, 4, 2, 2>(a, m0, n0, smem, &rows);
+  else forward_tile<LOGP, 4, 2, 2>(a, m0, n0, j, smem, &rows);
 }
 
 // C_y += sum of rest_t XP_t over the tokens with target y, in token order. A
@@ -663,14 +735,14 @@ bool pair_tiles(const CeArgs& a, int64_t blocks, bool backward) {
   return a.grid.large == 0 && !a.C && blocks > cus && (backward || blocks <= 2 * cus || a.k <= 1024);
 }
 
-template <bool BACKWARD>
+template <bool BACKWARD, bool LOGP>
 rgc_status_t logits_launch(CeArgs& a, hipStream_t s) {
   a.grid = grid_of(a.T, a.V);
   const int64_t blocks = blocks_of(a.T, a.V, a.grid);
   const dim3 grid((unsigned)blocks), threads(kGtThreads);
-  if (few_tokens(a.T)) hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, true>), grid, threads, 0, s, a);
-  else if (pair_tiles(a, blocks, BACKWARD)) hipLaunchKernelGGL((ce_pair_kernel<BACKWARD>), grid, threads, 0, s, a);
-  else hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, false>), grid, threads, 0, s, a);
+  if (few_tokens(a.T)) hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, true, LOGP>), grid, threads, 0, s, a);
+  else if (pair_tiles(a, blocks, BACKWARD)) hipLaunchKernelGGL((ce_pair_kernel<BACKWARD, LOGP>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((ce_logits_kernel<BACKWARD, false, LOGP>), grid, threads, 0, s, a);
   return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP;
 }
 
@@ -748,37 +820,40 @@ bool forward_fits(int64_t T, int64_t V) { return blocks_of(T, V, grid_of(T, V)) 
 
 // A token's partial sums, one for each column of tiles.
 size_t part_bytes(int64_t T, int64_t V) { return up256((size_t)grid_of(T, V).ntiles * (size_t)T * 8); }
+size_t part_q_bytes(int64_t T, int64_t V) { return up256((size_t)grid_of(T, V).ntiles * (size_t)T * 4); }
 
-}  // namespace
-}  // namespace rgc
-
-using namespace rgc;
-
-extern "C" size_t rgc_linear_cross_entropy_forward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r) {
+template <bool LOGP>
+size_t forward_workspace(int64_t T, int64_t V, int64_t k, int64_t r) {
   if (!shape_ok(T, V, k, r) || !forward_fits(T, V)) return 0;
-  return part_bytes(T, V) + up256((size_t)T * 4) + (r > 0 ? rgc_project_workspace_size(T, k, r) : 0);
+  return part_bytes(T, V) + (LOGP ? part_q_bytes(T, V) : 0) + up256((size_t)T * 4) +
+         (r > 0 ? rgc_project_workspace_size(T, k, r) : 0);
 }
 
-extern "C" rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
-                                                         const uint16_t* P, const int64_t* targets, float* loss,
-                                                         float* lse, uint16_t* XP, int64_t T, int64_t V, int64_t k,
-                                                         int64_t r, void* ws, size_t ws_bytes, void* stream) {
+// value: the losses or the log probabilities; entropy: with LOGP.
+template <bool LOGP>
+rgc_status_t forward_impl(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const uint16_t* P,
+                          const int64_t* targets, float* value, float* entropy, float* lse, uint16_t* XP, int64_t T,
+                          int64_t V, int64_t k, int64_t r, void* ws, size_t ws_bytes, void* stream) {
   rgc_status_t st = check_shape(T, V, k, r);
   if (st != RGC_OK || T == 0) return st;
   if (!forward_fits(T, V)) return RGC_ERR_UNSUPPORTED;
   if ((st = check_rows(X, ldx, k)) != RGC_OK) return st;
   if ((st = check_rows(W, ldw, k)) != RGC_OK) return st;
-  if (!targets || !loss || !lse || (r > 0 && (!P || !XP))) return RGC_ERR_NULL;
-  if (!aligned_to(targets, 8) || !aligned_to(loss, 4) || !aligned_to(lse, 4) ||
+  if (!targets || !value || (LOGP && !entropy) || !lse || (r > 0 && (!P || !XP))) return RGC_ERR_NULL;
+  if (!aligned_to(targets, 8) || !aligned_to(value, 4) || !aligned_to(entropy, 4) || !aligned_to(lse, 4) ||
       (r > 0 && (!aligned16(P) || !aligned16(XP))))
     return RGC_ERR_ALIGN;
-  if (!ws || ws_bytes < rgc_linear_cross_entropy_forward_workspace_size(T, V, k, r)) return RGC_ERR_WORKSPACE;
+  if (!ws || ws_bytes < forward_workspace<LOGP>(T, V, k, r)) return RGC_ERR_WORKSPACE;
   if (!aligned_to(ws, 256)) return RGC_ERR_ALIGN;
   char* at = static_cast<char*>(ws);
   CeArgs a{};
   a.X = X, a.W = W, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = T, a.V = a.vocab = V, a.k = k;
   a.part = reinterpret_cast<float2*>(at);
   at += part_bytes(T, V);
+  if (LOGP) {
+    a.part_q = reinterpret_cast<float*>(at);
+    at += part_q_bytes(T, V);
+  }
   a.zt = reinterpret_cast<float*>(at);
   at += up256((size_t)T * 4);
   const hipStream_t s = static_cast<hipStream_t>(stream);
@@ -786,29 +861,33 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int6
     st = rgc_project(X, ldx, P, XP, T, k, r, at, ws_bytes - (size_t)(at - static_cast<char*>(ws)), stream);
     if (st != RGC_OK) return st;
   }
-  if ((st = logits_launch<false>(a, s)) != RGC_OK) return st;
-  hipLaunchKernelGGL(ce_finish_kernel, dim3((unsigned)((T + 15) / 16)), dim3(1024), 0, s, a, loss, lse);
+  if ((st = logits_launch<false, LOGP>(a, s)) != RGC_OK) return st;
+  const dim3 tokens((unsigned)((T + 15) / 16));
+  if (LOGP) hipLaunchKernelGGL(lp_finish_kernel, tokens, dim3(1024), 0, s, a, value, entropy, lse);
+  else hipLaunchKernelGGL(ce_finish_kernel, tokens, dim3(1024), 0, s, a, value, lse);
   return launched();
 }
 
-extern "C" size_t rgc_linear_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r) {
-  if (!shape_ok(T, V, k, r)) return 0;
-  return plan_of(T, V, k, r).total();
+size_t backward_workspace(int64_t T, int64_t V, int64_t k, int64_t r) {
+  return shape_ok(T, V, k, r) ? plan_of(T, V, k, r).total() : 0;
 }
 
-extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
-                                                          const int64_t* targets, const float* lse, const float* grad,
-                                                          const uint16_t* XP, float* C, uint16_t* dX, int64_t lddx,
-                                                          int64_t T, int64_t V, int64_t k, int64_t r, void* ws,
-                                                          size_t ws_bytes, void* stream) {
+// grad: of the losses, or with LOGP of the log probabilities, beside grad_entropy (one of the two may be null).
+template <bool LOGP>
+rgc_status_t backward_impl(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const int64_t* targets,
+                           const float* lse, const float* entropy, const float* grad, const float* grad_entropy,
+                           const uint16_t* XP, float* C, uint16_t* dX, int64_t lddx, int64_t T, int64_t V, int64_t k,
+                           int64_t r, void* ws, size_t ws_bytes, void* stream) {
   rgc_status_t st = check_shape(T, V, k, r);
   if (st != RGC_OK || T == 0) return st;
   if (r > 0 && V % 8 != 0) return RGC_ERR_UNSUPPORTED;  // the sketch has a layer's widths
   if ((st = check_rows(X, ldx, k)) != RGC_OK) return st;
   if ((st = check_rows(W, ldw, k)) != RGC_OK) return st;
   if ((dX || r == 0) && (st = check_rows(dX, lddx, k)) != RGC_OK) return st;
-  if (!targets || !lse || !grad || (r > 0 && (!XP || !C))) return RGC_ERR_NULL;
-  if (!aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(grad, 4) ||
+  if (!targets || !lse || (r > 0 && (!XP || !C))) return RGC_ERR_NULL;
+  if (LOGP ? (!grad && !grad_entropy) || (grad_entropy && !entropy) : !grad) return RGC_ERR_NULL;
+  if (!aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(grad, 4) || !aligned_to(entropy, 4) ||
+      !aligned_to(grad_entropy, 4) ||
       (r > 0 && (!aligned16(XP) || !aligned16(C))))
     return RGC_ERR_ALIGN;
   const Plan p = plan_of(T, V, k, r);
@@ -829,7 +908,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
   }
   CeArgs a{};
   a.X = X, a.targets = targets, a.ldx = ldx, a.ldw = ldw, a.T = T, a.vocab = V, a.k = k;
-  a.lse = lse, a.grad = grad;
+  a.lse = lse, a.grad = grad, a.entropy = entropy, a.grad_entropy = grad_entropy;
   a.rest = reinterpret_cast<float*>(at + p.d + p.xp);
   DxArgs x{};
   x.ldw = ldw, x.T = T, x.k = k, x.mtiles = dx_rows(T), x.ntiles = tiles_of(k), x.slab = slab, x.lddx = lddx;
@@ -840,7 +919,7 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
     a.ldd = tiles_of(rows) * kGtTile;
     a.hi = D, a.lo = dX || accumulate ? D + T * a.ldd : nullptr;
     if (p.fused) a.C = C + v0 * r, a.XP = XP, a.r = (int)r;
-    if ((st = logits_launch<true>(a, s)) != RGC_OK) return st;
+    if ((st = logits_launch<true, LOGP>(a, s)) != RGC_OK) return st;
     if (dX) {
       x.D = a.hi, x.W = a.W, x.ldd = a.ldd, x.K = rows, x.first = q == 0;
       x.steps = ((rows + kGtStep - 1) / kGtStep + p.splits - 1) / p.splits;
@@ -874,4 +953,58 @@ extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int
     st = launched();
   }
   return st;
+}
+
+}  // namespace
+}  // namespace rgc
+
+using namespace rgc;
+
+extern "C" size_t rgc_linear_cross_entropy_forward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r) {
+  return forward_workspace<false>(T, V, k, r);
+}
+
+extern "C" rgc_status_t rgc_linear_cross_entropy_forward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                                         const uint16_t* P, const int64_t* targets, float* loss,
+                                                         float* lse, uint16_t* XP, int64_t T, int64_t V, int64_t k,
+                                                         int64_t r, void* ws, size_t ws_bytes, void* stream) {
+  return forward_impl<false>(X, ldx, W, ldw, P, targets, loss, nullptr, lse, XP, T, V, k, r, ws, ws_bytes, stream);
+}
+
+extern "C" size_t rgc_linear_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r) {
+  return backward_workspace(T, V, k, r);
+}
+
+extern "C" rgc_status_t rgc_linear_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                                          const int64_t* targets, const float* lse, const float* grad,
+                                                          const uint16_t* XP, float* C, uint16_t* dX, int64_t lddx,
+                                                          int64_t T, int64_t V, int64_t k, int64_t r, void* ws,
+                                                          size_t ws_bytes, void* stream) {
+  return backward_impl<false>(X, ldx, W, ldw, targets, lse, nullptr, grad, nullptr, XP, C, dX, lddx, T, V, k, r, ws,
+                              ws_bytes, stream);
+}
+
+extern "C" size_t rgc_linear_log_prob_forward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r) {
+  return forward_workspace<true>(T, V, k, r);
+}
+
+extern "C" rgc_status_t rgc_linear_log_prob_forward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                                    const uint16_t* P, const int64_t* tokens, float* logp,
+                                                    float* entropy, float* lse, uint16_t* XP, int64_t T, int64_t V,
+                                                    int64_t k, int64_t r, void* ws, size_t ws_bytes, void* stream) {
+  return forward_impl<true>(X, ldx, W, ldw, P, tokens, logp, entropy, lse, XP, T, V, k, r, ws, ws_bytes, stream);
+}
+
+extern "C" size_t rgc_linear_log_prob_backward_workspace_size(int64_t T, int64_t V, int64_t k, int64_t r) {
+  return backward_workspace(T, V, k, r);
+}
+
+extern "C" rgc_status_t rgc_linear_log_prob_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                                     const int64_t* tokens, const float* lse, const float* entropy,
+                                                     const float* grad_logp, const float* grad_entropy,
+                                                     const uint16_t* XP, float* C, uint16_t* dX, int64_t lddx, int64_t T,
+                                                     int64_t V, int64_t k, int64_t r, void* ws, size_t ws_bytes,
+                                                     void* stream) {
+  return backward_impl<true>(X, ldx, W, ldw, tokens, lse, entropy, grad_logp, grad_entropy, XP, C, dX, lddx, T, V, k, r,
+                             ws, ws_bytes, stream);
 }

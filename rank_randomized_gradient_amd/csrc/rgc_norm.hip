@@ -47,7 +47,9 @@ constexpr int kBwdThreads = 1024;           // of the wide rows' dx launch
 constexpr int kPanel = 256;  // columns of a workgroup of the column-sum launch
 
 struct NormArgs {
-  const void* x;
+  const void* x;    // backward of a residual norm: the sum
+  const void* r;    // residual norm: forward, the residual; backward, the sum's own gradient
+  void* sum;        // residual norm: x + r (forward)
   const void* dy;   // backward
   const void* w;    // null: ones
   const void* b;    // null: none (forward)
@@ -55,7 +57,7 @@ struct NormArgs {
   float* mean;      // forward: written unless null; backward: read (layer)
   float* rstd;
   float* part;      // backward: partial rows
-  int64_t ldx, lddy, ldo;
+  int64_t ldx, lddy, ldo, ldr, lds;
   int64_t rows, n;
   float eps;
   int w_f32;
@@ -81,6 +83,20 @@ struct Raw<uint16_t> {
       if (i < count) v[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
   }
   __device__ __forceinline__ float get(int i) const { return __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16); }
+  __device__ __forceinline__ void add(const Raw& o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f32x2_to_bf16x2_rne(get(2 * i) + o.get(2 * i), get(2 * i + 1) + o.get(2 * i + 1));
+  }
+  // stores the elements as they are
+  template <bool RAGGED>
+  __device__ __forceinline__ void keep(uint16_t* row, int c, int n) const {
+    if (c + 8 <= n) *reinterpret_cast<any_t*>(row + c) = v;
+    else if (RAGGED && c < n) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (c + i < n) row[c + i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+    }
+  }
   static __device__ __forceinline__ void store(uint16_t* p, const float (&f)[8]) {
     *reinterpret_cast<any_t*>(p) = u32x4v_t{f32x2_to_bf16x2_rne(f[0], f[1]), f32x2_to_bf16x2_rne(f[2], f[3]),
                                             f32x2_to_bf16x2_rne(f[4], f[5]), f32x2_to_bf16x2_rne(f[6], f[7])};
@@ -107,6 +123,21 @@ struct Raw<float> {
       if (i < count) (i < 4 ? a : b)[i & 3] = p[i];
   }
   __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
+  __device__ __forceinline__ void add(const Raw& o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] += o.a[i], b[i] += o.b[i];
+  }
+  template <bool RAGGED>
+  __device__ __forceinline__ void keep(float* row, int c, int n) const {
+    if (c + 8 <= n) {
+      reinterpret_cast<any_t*>(row + c)[0] = a;
+      reinterpret_cast<any_t*>(row + c)[1] = b;
+    } else if (RAGGED && c < n) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (c + i < n) row[c + i] = get(i);
+    }
+  }
   static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
     reinterpret_cast<any_t*>(p)[0] = f32x4_t{f[0], f[1], f[2], f[3]};
     reinterpret_cast<any_t*>(p)[1] = f32x4_t{f[4], f[5], f[6], f[7]};
@@ -193,7 +224,8 @@ __device__ __forceinline__ void group_sum(float (&a)[N], float* slots) {
 }
 
 // Forward: a workgroup of THREADS threads takes THREADS / TPR rows at a time.
-template <typename XT, bool RAGGED, int NV, int TPR, int THREADS>
+// ADD: of x + r, which is stored and taken further as stored.
+template <typename XT, bool RAGGED, int NV, int TPR, int THREADS, bool ADD>
 __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
   constexpr int GROUPS = THREADS / TPR;
   __shared__ float slots[2][THREADS / 64];
@@ -206,6 +238,18 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
     Raw<XT> raw[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) load_at<RAGGED>(raw[j], x, (j * TPR + t) * 8, n);
+    if constexpr (ADD) {
+      const XT* r = static_cast<const XT*>(a.r) + (live ? row : row0) * a.ldr;
+      XT* sum = static_cast<XT*>(a.sum) + row * a.lds;
+      Raw<XT> other[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) load_at<RAGGED>(other[j], r, (j * TPR + t) * 8, n);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        raw[j].add(other[j]);
+        if (live) raw[j].template keep<RAGGED>(sum, (j * TPR + t) * 8, n);
+      }
+    }
     float mu = 0.f;
     if (a.centre) {
       float s[1] = {0.f};
@@ -261,7 +305,8 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
 // Backward with the row in registers; see the head of the file. The weight is
 // kept in LDS. With c = x - mu: dw += (g rstd) c, and dx = rstd h - rstd c1 -
 // c (rstd^2 c2), c1 = mean(h) and c2 = mean(h c).
-template <typename XT, bool RAGGED, int NV, int TPR, int THREADS>
+// ADD: dx += r, the sum's own gradient, before it is rounded.
+template <typename XT, bool RAGGED, int NV, int TPR, int THREADS, bool ADD>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
   constexpr int GROUPS = THREADS / TPR, COLS = TPR * NV * 8;
   __shared__ float slots[2][2 * THREADS / 64];
@@ -309,6 +354,12 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(dw[j][e]), "+v"(db[j][e]));
     }
+    Raw<XT> rs[ADD ? NV : 1];
+    if constexpr (ADD) {
+      const XT* r = static_cast<const XT*>(a.r) + (live ? row : 0) * a.ldr;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) load_at<RAGGED>(rs[j], r, live ? (j * TPR + t) * 8 : n, n);
+    }
     group_sum<TPR>(sum, slots[parity]);
     const float k1 = a.centre ? sum[0] * inv_n * rstd : 0.f, k2 = sum[1] * inv_n * rstd * rstd * rstd;
     XT* dx = static_cast<XT*>(a.out) + row * a.ldo;
@@ -323,6 +374,10 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         f[e] = __builtin_fmaf(rg[j].get(e) * w[e], rstd, -__builtin_fmaf(rx[j].get(e) - mu, k2, k1));
+      if constexpr (ADD) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] += rs[j].get(e);
+      }
       store_at<RAGGED>(dx, c, n, f);
     }
   }
@@ -345,7 +400,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
 }
 
 // Wide rows, second launch: dx, one row per workgroup, each row read twice.
-template <typename XT>
+template <typename XT, bool ADD>
 __global__ __launch_bounds__(kBwdThreads) void norm_wide_dx_kernel(NormArgs a) {
   __shared__ float slots[2 * kBwdThreads / 64];
   const float inv_n = 1.0f / (float)a.n;
@@ -366,7 +421,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_wide_dx_kernel(NormArgs a) {
     for (int64_t c = threadIdx.x; c < a.n; c += kBwdThreads) {
       const float xv = load_param(x, sizeof(XT) == 4, c), gv = load_param(g, sizeof(XT) == 4, c);
       const float h = gv * (a.w ? load_param(a.w, a.w_f32, c) : 1.f);
-      const float f = (h - c1 - (xv - mu) * rstd * c2) * rstd;
+      float f = (h - c1 - (xv - mu) * rstd * c2) * rstd;
+      if constexpr (ADD) f += load_param(static_cast<const XT*>(a.r) + row * a.ldr, sizeof(XT) == 4, c);
       if constexpr (sizeof(XT) == 4) dx[c] = f;
       else dx[c] = (uint16_t)f32_to_bf16_rne(f);
     }
@@ -439,7 +495,7 @@ rgc_status_t check_shape(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, i
 
 rgc_status_t launched() { return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP; }
 
-template <typename XT, int NV, int TPR, int THREADS>
+template <bool ADD, typename XT, int NV, int TPR, int THREADS>
 void forward_launch(const NormArgs& a, hipStream_t s) {
   // bf16 rows of up to 256 threads: a workgroup to each group of rows (32768 x
   // 4096: 104 us; walking four groups each 112). Others: four rounds of
@@ -448,23 +504,23 @@ void forward_launch(const NormArgs& a, hipStream_t s) {
   const int64_t groups = (a.rows + THREADS / TPR - 1) / (THREADS / TPR);
   const int64_t most = sizeof(XT) == 2 && THREADS == 256 ? int64_t(1) << 20 : (int64_t)device_compute_units() * (2048 / THREADS) * 4;
   const dim3 grid((unsigned)(groups < most ? groups : most));
-  if (a.n % 8) hipLaunchKernelGGL((norm_forward_kernel<XT, true, NV, TPR, THREADS>), grid, dim3(THREADS), 0, s, a);
-  else hipLaunchKernelGGL((norm_forward_kernel<XT, false, NV, TPR, THREADS>), grid, dim3(THREADS), 0, s, a);
+  if (a.n % 8) hipLaunchKernelGGL((norm_forward_kernel<XT, true, NV, TPR, THREADS, ADD>), grid, dim3(THREADS), 0, s, a);
+  else hipLaunchKernelGGL((norm_forward_kernel<XT, false, NV, TPR, THREADS, ADD>), grid, dim3(THREADS), 0, s, a);
 }
 
-template <typename XT>
+template <bool ADD, typename XT>
 void forward_pick(const NormArgs& a, hipStream_t s) {
-  if (a.n <= 128) forward_launch<XT, 1, 16, 256>(a, s);
-  else if (a.n <= 512) forward_launch<XT, 1, 64, 256>(a, s);
-  else if (a.n <= 1024) forward_launch<XT, 2, 64, 256>(a, s);
-  else if (a.n <= 2048) forward_launch<XT, 4, 64, 256>(a, s);
+  if (a.n <= 128) forward_launch<ADD, XT, 1, 16, 256>(a, s);
+  else if (a.n <= 512) forward_launch<ADD, XT, 1, 64, 256>(a, s);
+  else if (a.n <= 1024) forward_launch<ADD, XT, 2, 64, 256>(a, s);
+  else if (a.n <= 2048) forward_launch<ADD, XT, 4, 64, 256>(a, s);
   else if (a.n <= 4096) {  // bf16 4096 x 4096: 14.8 us on 256 threads a row, 16.1 on 128; fp32 16384 x 4096: 107 and 103
-    if constexpr (sizeof(XT) == 2) forward_launch<XT, 2, 256, 256>(a, s);
-    else forward_launch<XT, 4, 128, 256>(a, s);
+    if constexpr (sizeof(XT) == 2) forward_launch<ADD, XT, 2, 256, 256>(a, s);
+    else forward_launch<ADD, XT, 4, 128, 256>(a, s);
   }
-  else if (a.n <= 8192) forward_launch<XT, 4, 256, 256>(a, s);
-  else if (a.n <= 16384) forward_launch<XT, 2, 1024, 1024>(a, s);
-  else forward_launch<XT, 8, 1024, 1024>(a, s);
+  else if (a.n <= 8192) forward_launch<ADD, XT, 4, 256, 256>(a, s);
+  else if (a.n <= 16384) forward_launch<ADD, XT, 2, 1024, 1024>(a, s);
+  else forward_launch<ADD, XT, 8, 1024, 1024>(a, s);
 }
 
 // Rows a workgroup of the backward holds at a time (as backward_pick).
@@ -484,79 +540,81 @@ int64_t backward_groups(int64_t rows, int64_t n, rgc_dtype_t xt) {
   return need < cus ? need : cus;
 }
 
-template <typename XT, int NV, int TPR, int THREADS>
+template <bool ADD, typename XT, int NV, int TPR, int THREADS>
 void backward_launch(const NormArgs& a, int64_t G, hipStream_t s) {
   const dim3 grid((unsigned)G);
-  if (a.n % 8) hipLaunchKernelGGL((norm_backward_kernel<XT, true, NV, TPR, THREADS>), grid, dim3(THREADS), 0, s, a);
-  else hipLaunchKernelGGL((norm_backward_kernel<XT, false, NV, TPR, THREADS>), grid, dim3(THREADS), 0, s, a);
+  if (a.n % 8) hipLaunchKernelGGL((norm_backward_kernel<XT, true, NV, TPR, THREADS, ADD>), grid, dim3(THREADS), 0, s, a);
+  else hipLaunchKernelGGL((norm_backward_kernel<XT, false, NV, TPR, THREADS, ADD>), grid, dim3(THREADS), 0, s, a);
 }
 
-template <typename XT>
+template <bool ADD, typename XT>
 void backward_pick(const NormArgs& a, int64_t G, hipStream_t s) {
   if (a.n > kNormHeldBackward) {
     // (the columns first: dX may take the place of X or dY)
     hipLaunchKernelGGL(norm_wide_columns_kernel<XT>, dim3((unsigned)((a.n + kPanel - 1) / kPanel), (unsigned)G),
                        dim3(kPanel), 0, s, a);
     const int64_t most = (int64_t)device_compute_units() * 4;
-    hipLaunchKernelGGL(norm_wide_dx_kernel<XT>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(kBwdThreads), 0, s,
+    hipLaunchKernelGGL((norm_wide_dx_kernel<XT, ADD>), dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(kBwdThreads), 0, s,
                        a);
     return;
   }
-  if (a.n <= 128) return backward_launch<XT, 1, 16, 1024>(a, G, s);
-  if (a.n <= 512) return backward_launch<XT, 1, 64, 1024>(a, G, s);
-  if (a.n <= 1024) return backward_launch<XT, 2, 64, 1024>(a, G, s);
+  if (a.n <= 128) return backward_launch<ADD, XT, 1, 16, 1024>(a, G, s);
+  if (a.n <= 512) return backward_launch<ADD, XT, 1, 64, 1024>(a, G, s);
+  if (a.n <= 1024) return backward_launch<ADD, XT, 2, 64, 1024>(a, G, s);
   if constexpr (sizeof(XT) == 2) {  // up to 64 elements to a lane
-    if (a.n <= 2048) return backward_launch<XT, 4, 64, 1024>(a, G, s);
-    if (a.n <= 4096) return backward_launch<XT, 8, 64, 512>(a, G, s);
-    if (a.n <= 8192) return backward_launch<XT, 8, 128, 512>(a, G, s);
-    backward_launch<XT, 8, 256, 512>(a, G, s);
+    if (a.n <= 2048) return backward_launch<ADD, XT, 4, 64, 1024>(a, G, s);
+    if (a.n <= 4096) return backward_launch<ADD, XT, 8, 64, 512>(a, G, s);
+    if (a.n <= 8192) return backward_launch<ADD, XT, 8, 128, 512>(a, G, s);
+    backward_launch<ADD, XT, 8, 256, 512>(a, G, s);
   } else {  // up to 32
-    if (a.n <= 2048) return backward_launch<XT, 4, 64, 512>(a, G, s);
-    if (a.n <= 4096) return backward_launch<XT, 4, 128, 512>(a, G, s);
-    if (a.n <= 8192) return backward_launch<XT, 4, 256, 512>(a, G, s);
-    backward_launch<XT, 4, 512, 512>(a, G, s);
+    if (a.n <= 2048) return backward_launch<ADD, XT, 4, 64, 512>(a, G, s);
+    if (a.n <= 4096) return backward_launch<ADD, XT, 4, 128, 512>(a, G, s);
+    if (a.n <= 8192) return backward_launch<ADD, XT, 4, 256, 512>(a, G, s);
+    backward_launch<ADD, XT, 4, 512, 512>(a, G, s);
   }
 }
 
-}  // namespace
-}  // namespace rgc
-
-using namespace rgc;
-
-extern "C" rgc_status_t rgc_layer_norm_forward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* X,
-                                               int64_t ldx, const void* weight, const void* bias, double eps, void* Y,
-                                               int64_t ldy, float* mean, float* rstd, int64_t rows, int64_t n,
-                                               void* stream) {
+// R null: a plain norm; else of X + R, which goes to S.
+rgc_status_t forward_impl(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* X, int64_t ldx, const void* R,
+                          int64_t ldr, const void* weight, const void* bias, double eps, void* S, int64_t lds, void* Y,
+                          int64_t ldy, float* mean, float* rstd, int64_t rows, int64_t n, bool add, void* stream) {
   rgc_status_t st = check_shape(kind, xt, wt, rows, n);
   if (st != RGC_OK) return st;
   if (!(eps >= 0) || !((float)eps <= 3e38f)) return RGC_ERR_VALUE;
   if (rows == 0) return RGC_OK;
   if ((st = check_rows(X, ldx, n, xt)) != RGC_OK) return st;
+  if (add && (st = check_rows(R, ldr, n, xt)) != RGC_OK) return st;
+  if (add && (st = check_rows(S, lds, n, xt)) != RGC_OK) return st;
   if ((st = check_rows(Y, ldy, n, xt)) != RGC_OK) return st;
   if (!aligned_to(weight, elem(wt)) || !aligned_to(bias, elem(wt)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
     return RGC_ERR_ALIGN;
   NormArgs a{};
-  a.x = X, a.w = weight, a.b = bias, a.out = Y, a.mean = mean, a.rstd = rstd;
-  a.ldx = ldx, a.ldo = ldy, a.rows = rows, a.n = n, a.eps = (float)eps;
+  a.x = X, a.r = R, a.sum = S, a.w = weight, a.b = bias, a.out = Y, a.mean = mean, a.rstd = rstd;
+  a.ldx = ldx, a.ldr = ldr, a.lds = lds, a.ldo = ldy, a.rows = rows, a.n = n, a.eps = (float)eps;
   a.w_f32 = wt == RGC_F32, a.centre = kind == RGC_NORM_LAYER;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (xt == RGC_F32) forward_pick<float>(a, s);
-  else forward_pick<uint16_t>(a, s);
+  if (add) {
+    if (xt == RGC_F32) forward_pick<true, float>(a, s);
+    else forward_pick<true, uint16_t>(a, s);
+  } else {
+    if (xt == RGC_F32) forward_pick<false, float>(a, s);
+    else forward_pick<false, uint16_t>(a, s);
+  }
   return launched();
 }
 
 // The partial rows of whichever type X will have.
-extern "C" size_t rgc_layer_norm_backward_workspace_size(int64_t rows, int64_t n) {
+size_t backward_workspace(int64_t rows, int64_t n) {
   if (rows <= 0 || n <= 0 || rows > kNormMaxRows || n > kNormMaxWidth) return 0;
   const int64_t a = backward_groups(rows, n, RGC_BF16), b = backward_groups(rows, n, RGC_F32);
   return (size_t)(a > b ? a : b) * 2 * (size_t)n * 4;
 }
 
-extern "C" rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* dY,
-                                                int64_t lddy, const void* X, int64_t ldx, const void* weight,
-                                                const float* mean, const float* rstd, void* dX, int64_t lddx,
-                                                void* dweight, void* dbias, int64_t rows, int64_t n, void* ws,
-                                                size_t ws_bytes, void* stream) {
+// dS null: a plain norm's; else added to dX.
+rgc_status_t backward_impl(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* dY, int64_t lddy,
+                           const void* dS, int64_t ldds, const void* X, int64_t ldx, const void* weight,
+                           const float* mean, const float* rstd, void* dX, int64_t lddx, void* dweight, void* dbias,
+                           int64_t rows, int64_t n, void* ws, size_t ws_bytes, void* stream) {
   rgc_status_t st = check_shape(kind, xt, wt, rows, n);
   if (st != RGC_OK) return st;
   if (!dweight) return RGC_ERR_NULL;
@@ -571,19 +629,67 @@ extern "C" rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_
   if ((st = check_rows(dY, lddy, n, xt)) != RGC_OK) return st;
   if ((st = check_rows(X, ldx, n, xt)) != RGC_OK) return st;
   if ((st = check_rows(dX, lddx, n, xt)) != RGC_OK) return st;
+  if (dS && (st = check_rows(dS, ldds, n, xt)) != RGC_OK) return st;
   if (!rstd || (kind == RGC_NORM_LAYER && !mean)) return RGC_ERR_NULL;
   if (!aligned_to(weight, elem(wt)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4)) return RGC_ERR_ALIGN;
-  if (!ws || ws_bytes < rgc_layer_norm_backward_workspace_size(rows, n)) return RGC_ERR_WORKSPACE;
+  if (!ws || ws_bytes < backward_workspace(rows, n)) return RGC_ERR_WORKSPACE;
   if (!aligned_to(ws, 256)) return RGC_ERR_ALIGN;
   NormArgs a{};
-  a.x = X, a.dy = dY, a.w = weight, a.out = dX, a.part = static_cast<float*>(ws);
+  a.x = X, a.r = dS, a.dy = dY, a.w = weight, a.out = dX, a.part = static_cast<float*>(ws);
   a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
-  a.ldx = ldx, a.lddy = lddy, a.ldo = lddx, a.rows = rows, a.n = n;
+  a.ldx = ldx, a.ldr = ldds, a.lddy = lddy, a.ldo = lddx, a.rows = rows, a.n = n;
   a.w_f32 = wt == RGC_F32, a.centre = kind == RGC_NORM_LAYER, a.db = dbias != nullptr;
   const int64_t G = backward_groups(rows, n, xt);
-  if (xt == RGC_F32) backward_pick<float>(a, G, s);
-  else backward_pick<uint16_t>(a, G, s);
+  if (dS) {
+    if (xt == RGC_F32) backward_pick<true, float>(a, G, s);
+    else backward_pick<true, uint16_t>(a, G, s);
+  } else {
+    if (xt == RGC_F32) backward_pick<false, float>(a, G, s);
+    else backward_pick<false, uint16_t>(a, G, s);
+  }
   if ((st = launched()) != RGC_OK) return st;
   hipLaunchKernelGGL(norm_params_kernel, params, dim3(1024), 0, s, a.part, G, n, a.w_f32, dweight, dbias);
   return launched();
+}
+
+}  // namespace
+}  // namespace rgc
+
+using namespace rgc;
+
+extern "C" rgc_status_t rgc_layer_norm_forward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* X,
+                                               int64_t ldx, const void* weight, const void* bias, double eps, void* Y,
+                                               int64_t ldy, float* mean, float* rstd, int64_t rows, int64_t n,
+                                               void* stream) {
+  return forward_impl(kind, xt, wt, X, ldx, nullptr, 0, weight, bias, eps, nullptr, 0, Y, ldy, mean, rstd, rows, n, false,
+                      stream);
+}
+
+extern "C" size_t rgc_layer_norm_backward_workspace_size(int64_t rows, int64_t n) { return backward_workspace(rows, n); }
+
+extern "C" rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* dY,
+                                                int64_t lddy, const void* X, int64_t ldx, const void* weight,
+                                                const float* mean, const float* rstd, void* dX, int64_t lddx,
+                                                void* dweight, void* dbias, int64_t rows, int64_t n, void* ws,
+                                                size_t ws_bytes, void* stream) {
+  return backward_impl(kind, xt, wt, dY, lddy, nullptr, 0, X, ldx, weight, mean, rstd, dX, lddx, dweight, dbias, rows, n,
+                       ws, ws_bytes, stream);
+}
+
+extern "C" rgc_status_t rgc_add_norm_forward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* X,
+                                             int64_t ldx, const void* R, int64_t ldr, const void* weight,
+                                             const void* bias, double eps, void* S, int64_t lds, void* Y, int64_t ldy,
+                                             float* mean, float* rstd, int64_t rows, int64_t n, void* stream) {
+  return forward_impl(kind, xt, wt, X, ldx, R, ldr, weight, bias, eps, S, lds, Y, ldy, mean, rstd, rows, n, true, stream);
+}
+
+extern "C" size_t rgc_add_norm_backward_workspace_size(int64_t rows, int64_t n) { return backward_workspace(rows, n); }
+
+extern "C" rgc_status_t rgc_add_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* dY,
+                                              int64_t lddy, const void* dS, int64_t ldds, const void* S, int64_t lds,
+                                              const void* weight, const float* mean, const float* rstd, void* dX,
+                                              int64_t lddx, void* dweight, void* dbias, int64_t rows, int64_t n, void* ws,
+                                              size_t ws_bytes, void* stream) {
+  return backward_impl(kind, xt, wt, dY, lddy, dS, ldds, S, lds, weight, mean, rstd, dX, lddx, dweight, dbias, rows, n, ws,
+                       ws_bytes, stream);
 }

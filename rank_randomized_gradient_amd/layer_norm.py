@@ -39,10 +39,39 @@ class LayerNormFunction(torch.autograd.Function):
                 None if db is None else db.to(ctx.bias_dtype), None, None)
 
 
+class AddNormFunction(torch.autograd.Function):
+    """(norm of x + residual, x + residual); saves the sum and each row's mean and rstd."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, eps, kind):
+        ctx.set_materialize_grads(False)
+        s, y, mean, rstd = rgc.rgc_add_norm_forward(_row_major(x), _row_major(residual), weight, bias, eps=eps, kind=kind)
+        ctx.save_for_backward(s, weight, mean, rstd)
+        ctx.kind = kind
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        ctx.shape = x.shape
+        return y.reshape(x.shape), s.reshape(x.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dsum):
+        s, weight, mean, rstd = ctx.saved_tensors
+        if dy is None:  # the sum alone was used
+            return dsum, dsum, None, None, None, None
+        rows = lambda g: None if g is None else _row_major(g if g.dtype == s.dtype else g.to(s.dtype))  # noqa: E731
+        dx, dw, db = rgc.rgc_add_norm_backward(rows(dy), rows(dsum), s, weight, mean, rstd, bias=ctx.bias_dtype is not None,
+                                               kind=ctx.kind)
+        dx = dx.reshape(ctx.shape)
+        return dx, dx, dw if weight is not None else None, None if db is None else db.to(ctx.bias_dtype), None, None
+
+
 class LayerNorm(torch.nn.Module):
     """Norm of the last dimension (kind "layer", or "rms" for the root-mean-square
     norm, which has no bias). Gains in float32 unless told otherwise: beside
     bf16 activations they cost nothing and their gradients stay float32.
+
+    forward(x, residual) takes a block's output and the stream that it is added to, and
+    gives (norm of the sum, the sum), in one pass over both.
 
     As with every torch parameter, a backward pass is captured into a graph
     only while no eager autograd graph over the same parameters is alive: torch
@@ -59,7 +88,11 @@ class LayerNorm(torch.nn.Module):
         with_bias = bias and kind == "layer"
         self.bias = torch.nn.Parameter(torch.zeros(features, dtype=dtype, device=device)) if with_bias else None
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
         if x.shape[-1] != self.features:
             raise rgc.RgcError(f"the last dimension must be {self.features}")
-        return LayerNormFunction.apply(x, self.weight, self.bias, self.eps, self.kind)
+        if residual is None:
+            return LayerNormFunction.apply(x, self.weight, self.bias, self.eps, self.kind)
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise rgc.RgcError("the residual must have x's shape and type")
+        return AddNormFunction.apply(x, residual, self.weight, self.bias, self.eps, self.kind)

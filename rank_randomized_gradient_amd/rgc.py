@@ -23,6 +23,18 @@ Names mirror the C ABI in include/rgc.h:
   rgc_layer_norm_forward(X, weight, bias)   (Y, mean, rstd) of a layer or root-mean-square norm
   rgc_layer_norm_backward(dY, X, weight, mean, rstd)
                                             (dX, dweight, dbias)
+  rgc_add_norm_forward(X, R, weight, bias)  (S, Y, mean, rstd): S = X + R and its norm
+  rgc_add_norm_backward(dY, dS, S, weight, mean, rstd)
+                                            (dX, dweight, dbias), dX the gradient of X and of R
+  rgc_linear_log_prob_forward(X, W, tokens, P)
+                                            (logp, entropy, lse, XP) of the softmax of X W^T, which is not kept
+  rgc_linear_log_prob_backward(X, W, tokens, lse, entropy, grad_logp, grad_entropy, XP, C)
+                                            dX, and C += D^T XP of the same
+  rgc_log_prob_forward(Z, tokens, top)      (logp, entropy, lse, top_logp, top_ids) of rows of logits
+  rgc_log_prob_backward(Z, tokens, lse, entropy, grad_logp, grad_entropy)
+                                            dZ
+  rgc_grad_norm_batch(Gs, max_norm)         (norm, scale): all gradients' norm and the factor that clips them
+  rgc_scale_batch(Gs, scale)                the gradients times scale (in place)
   rgc_adamw_batch(Ps, Gs, Ms, Vs, lr, step) one AdamW step over many tensors (in place)
 """
 from __future__ import annotations
@@ -128,6 +140,27 @@ SIGNATURES = {
     "rgc_layer_norm_backward_workspace_size": (_sz, [_i64, _i64]),
     "rgc_layer_norm_backward": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _vp,
                                                _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "rgc_add_norm_forward": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _vp,
+                                            _f64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
+    "rgc_add_norm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "rgc_add_norm_backward": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _i64,
+                                             _vp, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "rgc_linear_log_prob_forward_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
+    "rgc_linear_log_prob_forward": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                                                   _i64, _vp, _sz, _vp]),
+    "rgc_linear_log_prob_backward_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
+    "rgc_linear_log_prob_backward": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                                    _i64, _i64, _i64, _i64, _vp, _sz, _vp]),
+    "rgc_log_prob_forward_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "rgc_log_prob_forward": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp,
+                                            _sz, _vp]),
+    "rgc_log_prob_backward": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                                             _vp]),
+    "rgc_grad_norm_batch_workspace_size": (_sz, [_i64, ctypes.POINTER(_i64)]),
+    "rgc_grad_norm_batch": (ctypes.c_int, [_i64, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(_vp), ctypes.POINTER(_i64),
+                                           _f64, _vp, _vp, _vp, _sz, _vp]),
+    "rgc_scale_batch": (ctypes.c_int, [_i64, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(_vp), ctypes.POINTER(_i64),
+                                       _vp, _vp]),
     "rgc_adamw_batch_with": (ctypes.c_int, [ctypes.c_uint, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                             ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_vp),
                                             ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_vp),
@@ -695,13 +728,13 @@ def _scratch(workspace: Workspace | None, nbytes: int, dev: torch.device):
     return ctypes.c_void_p(buf.data_ptr()), nbytes, buf
 
 
-def _head_args(X, W, targets):
+def _head_args(X, W, targets, name="targets"):
     ldx = _rows(X, torch.bfloat16, "X")
     ldw = _rows(W, torch.bfloat16, "W")
-    _dense(targets, torch.int64, "targets")
+    _dense(targets, torch.int64, name)
     T, k = X.shape
     if W.shape[1] != k or tuple(targets.shape) != (T,):
-        raise RgcError("shapes must be X: T x k, W: V x k, targets: T")
+        raise RgcError(f"shapes must be X: T x k, W: V x k, {name}: T")
     return ldx, ldw, T, W.shape[0], k
 
 
@@ -771,6 +804,151 @@ def rgc_linear_cross_entropy_backward(X: torch.Tensor, W: torch.Tensor, targets:
                                                      lddx, T, V, k, r, wp, wn,
                                                      _stream(dev)))
     return dX
+
+
+def rgc_linear_log_prob_forward(X: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, P: torch.Tensor | None = None,
+                                workspace: Workspace | None = None):
+    """(logp, entropy, lse, XP): per token t the log probability of tokens[t] under
+    the softmax of X W^T, that softmax's entropy (both 0 where the token lies outside
+    0 .. V-1) and the logits' log sum of exponentials, all float32, with the logits
+    never stored; XP = bf16(X P), or None without P. X: T x k, W: V x k bf16, tokens: int64."""
+    lib = load_library()
+    dev = _need_gpu(X, W, tokens, *([P] if P is not None else []))
+    ldx, ldw, T, V, k = _head_args(X, W, tokens, "tokens")
+    r, XP = 0, None
+    if P is not None:
+        _dense(P, torch.bfloat16, "P")
+        if P.dim() != 2 or P.shape[0] != k or P.shape[1] == 0:
+            raise RgcError("P must be k x r with k = X.shape[1]")
+        r = P.shape[1]
+        XP = torch.empty((T, r), dtype=torch.bfloat16, device=dev)
+    logp, entropy, lse = (torch.empty(T, dtype=torch.float32, device=dev) for _ in range(3))
+    with _on(dev):
+        wp, wn, _keep = _scratch(workspace, lib.rgc_linear_log_prob_forward_workspace_size(T, V, k, r), dev)
+        _check(lib.rgc_linear_log_prob_forward(X.data_ptr(), ldx, W.data_ptr(), ldw, P.data_ptr() if r else None,
+                                               tokens.data_ptr(), logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+                                               XP.data_ptr() if r else None, T, V, k, r, wp, wn, _stream(dev)))
+    return logp, entropy, lse, XP
+
+
+def _row_values(n: int, lse, entropy, grad_logp, grad_entropy) -> None:
+    """Checks the float32 values of each row that the log probabilities' backward takes."""
+    if grad_logp is None and grad_entropy is None:
+        raise RgcError("grad_logp or grad_entropy must be given")
+    if grad_entropy is not None and entropy is None:
+        raise RgcError("the entropy's gradient needs the forward's entropy")
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (grad_logp, "grad_logp"), (grad_entropy, "grad_entropy")):
+        if t is not None:
+            _dense(t, torch.float32, name)
+            if tuple(t.shape) != (n,):
+                raise RgcError(f"{name} must have one value per token")
+
+
+def _pointer(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def rgc_linear_log_prob_backward(X: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor,
+                                 entropy: torch.Tensor | None, grad_logp: torch.Tensor | None,
+                                 grad_entropy: torch.Tensor | None = None, XP: torch.Tensor | None = None,
+                                 C: torch.Tensor | None = None, dX: torch.Tensor | None = None, input_grad: bool = True,
+                                 workspace: Workspace | None = None) -> torch.Tensor | None:
+    """dX = bf16(D W) with D_tv = grad_logp[t] ([v = tokens[t]] - p_tv) - grad_entropy[t] p_tv (log p_tv + entropy[t]),
+    p = softmax(X W^T), and, with XP and C, C += D^T XP (V x r float32). lse and
+    entropy are the forward's; a gradient that is None is zero. D exists a piece of the
+    vocabulary at a time. input_grad False leaves dX out (C alone; returns None)."""
+    lib = load_library()
+    dev = _need_gpu(X, W, tokens, lse, *[t for t in (entropy, grad_logp, grad_entropy, XP, C, dX) if t is not None])
+    ldx, ldw, T, V, k = _head_args(X, W, tokens, "tokens")
+    _row_values(T, lse, entropy, grad_logp, grad_entropy)
+    if (XP is None) != (C is None):
+        raise RgcError("XP and C go together")
+    r = 0
+    if C is not None:
+        _dense(XP, torch.bfloat16, "XP")
+        _dense(C, torch.float32, "C")
+        r = C.shape[-1]
+        if r == 0 or tuple(C.shape) != (V, r) or tuple(XP.shape) != (T, r):
+            raise RgcError("shapes must be XP: T x r, C: V x r")
+    if input_grad:
+        if dX is None:
+            dX = torch.empty((T, k), dtype=torch.bfloat16, device=dev)
+        if tuple(dX.shape) != (T, k):
+            raise RgcError("dX must be T x k")
+    elif dX is not None or C is None:
+        raise RgcError("without the input's gradient there must be a sketch, and no dX")
+    lddx = _rows(dX, torch.bfloat16, "dX") if input_grad else k
+    with _on(dev):
+        wp, wn, _keep = _scratch(workspace, lib.rgc_linear_log_prob_backward_workspace_size(T, V, k, r), dev)
+        _check(lib.rgc_linear_log_prob_backward(X.data_ptr(), ldx, W.data_ptr(), ldw, tokens.data_ptr(), lse.data_ptr(),
+                                                _pointer(entropy), _pointer(grad_logp), _pointer(grad_entropy),
+                                                XP.data_ptr() if r else None, C.data_ptr() if r else None,
+                                                dX.data_ptr() if input_grad else None, lddx, T, V, k, r, wp, wn,
+                                                _stream(dev)))
+    return dX
+
+
+def _logit_rows(t: torch.Tensor, like: torch.Tensor, name: str) -> int:
+    if t.dtype not in _DTYPES or t.dtype != like.dtype:
+        raise RgcError(f"{name} must be bf16 or float32, and of Z's type")
+    if t.shape != like.shape:
+        raise RgcError(f"{name} must have Z's shape")
+    return _rows(t, t.dtype, name)
+
+
+def rgc_log_prob_forward(Z: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0,
+                         workspace: Workspace | None = None):
+    """(logp, entropy, lse, top_logp, top_ids) of rows of logits Z (rows x V, bf16 or
+    float32): the log probability of each row's token and the entropy of its softmax
+    (both 0 where the token lies outside 0 .. V-1), the log sum of exponentials,
+    and the `top` (up to 64) most likely entries, of equal ones the lowest first:
+    log probabilities float32 and indices int64, rows x top. Without tokens logp is
+    None and every row's entropy is given; with top 0 the last two are None. Entries
+    of -inf are forbidden ones."""
+    lib = load_library()
+    dev = _need_gpu(Z, *([tokens] if tokens is not None else []))
+    ldz = _logit_rows(Z, Z, "Z")
+    rows, V = Z.shape
+    if tokens is not None:
+        _dense(tokens, torch.int64, "tokens")
+        if tuple(tokens.shape) != (rows,):
+            raise RgcError("tokens must have one value per row of Z")
+    if not 0 <= top <= 64:
+        raise RgcError("top must lie in 0 .. 64")
+    logp = torch.empty(rows, dtype=torch.float32, device=dev) if tokens is not None else None
+    entropy, lse = (torch.empty(rows, dtype=torch.float32, device=dev) for _ in range(2))
+    top_logp = torch.empty((rows, top), dtype=torch.float32, device=dev) if top else None
+    top_ids = torch.empty((rows, top), dtype=torch.int64, device=dev) if top else None
+    with _on(dev):
+        wp, wn, _keep = _scratch(workspace, lib.rgc_log_prob_forward_workspace_size(rows, V, top), dev)
+        _check(lib.rgc_log_prob_forward(_DTYPES[Z.dtype], Z.data_ptr(), ldz, _pointer(tokens), _pointer(logp),
+                                        entropy.data_ptr(), lse.data_ptr(), top, _pointer(top_logp), _pointer(top_ids),
+                                        rows, V, wp, wn, _stream(dev)))
+    return logp, entropy, lse, top_logp, top_ids
+
+
+def rgc_log_prob_backward(Z: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor, entropy: torch.Tensor | None,
+                          grad_logp: torch.Tensor | None, grad_entropy: torch.Tensor | None = None,
+                          dZ: torch.Tensor | None = None) -> torch.Tensor:
+    """dZ, of Z's type, from the gradients of rgc_log_prob_forward's logp and entropy
+    (None for zeros) and its lse and entropy; dZ may be Z."""
+    lib = load_library()
+    dev = _need_gpu(Z, tokens, lse, *[t for t in (entropy, grad_logp, grad_entropy, dZ) if t is not None])
+    ldz = _logit_rows(Z, Z, "Z")
+    rows, V = Z.shape
+    _dense(tokens, torch.int64, "tokens")
+    if tuple(tokens.shape) != (rows,):
+        raise RgcError("tokens must have one value per row of Z")
+    _row_values(rows, lse, entropy, grad_logp, grad_entropy)
+    if dZ is None:
+        dZ, lddz = torch.empty((rows, V), dtype=Z.dtype, device=dev), V
+    else:
+        lddz = _logit_rows(dZ, Z, "dZ")
+    with _on(dev):
+        _check(lib.rgc_log_prob_backward(_DTYPES[Z.dtype], Z.data_ptr(), ldz, tokens.data_ptr(), lse.data_ptr(),
+                                         _pointer(entropy), _pointer(grad_logp), _pointer(grad_entropy), dZ.data_ptr(),
+                                         lddz, rows, V, _stream(dev)))
+    return dZ
 
 
 def _norm_rows(t: torch.Tensor, like: torch.Tensor, name: str) -> int:
@@ -860,6 +1038,69 @@ def rgc_layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Ten
     return dX, dweight, dbias
 
 
+def rgc_add_norm_forward(X: torch.Tensor, R: torch.Tensor, weight: torch.Tensor | None = None,
+                         bias: torch.Tensor | None = None, eps: float = 1e-5, kind: str = "layer",
+                         S: torch.Tensor | None = None, Y: torch.Tensor | None = None):
+    """(S, Y, mean, rstd): S = X + R, rounded to their type, and the norm of S as
+    rgc_layer_norm_forward gives it (mean None for kind "rms"). X, R: rows x n, bf16
+    or float32; S may be X or R, and Y the other one."""
+    lib = load_library()
+    dev = _need_gpu(X, R, *[t for t in (weight, bias, S, Y) if t is not None])
+    ldx, ldr = _norm_rows(X, X, "X"), _norm_rows(R, X, "R")
+    rows, n = X.shape
+    kid = _norm_kind(kind)
+    wt = _norm_params(n, weight, bias)
+    if S is None:
+        S = torch.empty((rows, n), dtype=X.dtype, device=dev)
+    if Y is None:
+        Y = torch.empty((rows, n), dtype=X.dtype, device=dev)
+    lds, ldy = _norm_rows(S, X, "S"), _norm_rows(Y, X, "Y")
+    if S.data_ptr() == Y.data_ptr() and S.numel() > 0:
+        raise RgcError("S and Y must be two tensors")
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if kid == RGC_NORM_LAYER else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    with _on(dev):
+        _check(lib.rgc_add_norm_forward(kid, _DTYPES[X.dtype], wt, X.data_ptr(), ldx, R.data_ptr(), ldr,
+                                        _pointer(weight), _pointer(bias), eps, S.data_ptr(), lds, Y.data_ptr(), ldy,
+                                        _pointer(mean), rstd.data_ptr(), rows, n, _stream(dev)))
+    return S, Y, mean, rstd
+
+
+def rgc_add_norm_backward(dY: torch.Tensor, dS: torch.Tensor | None, S: torch.Tensor, weight: torch.Tensor | None,
+                          mean: torch.Tensor | None, rstd: torch.Tensor, bias: bool = True, kind: str = "layer",
+                          dX: torch.Tensor | None = None, workspace: Workspace | None = None):
+    """(dX, dweight, dbias) from the gradients of Y and S (dS None: zeros) and the
+    forward's S, mean and rstd. dX is the gradient of X and of R; the rest is as for
+    rgc_layer_norm_backward."""
+    lib = load_library()
+    dev = _need_gpu(dY, S, rstd, *[t for t in (dS, weight, mean, dX) if t is not None])
+    lds, lddy = _norm_rows(S, S, "S"), _norm_rows(dY, S, "dY")
+    ldds = _norm_rows(dS, S, "dS") if dS is not None else 0
+    rows, n = S.shape
+    kid = _norm_kind(kind)
+    wt = _norm_params(n, weight, None)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t is None:
+            if kid == RGC_NORM_LAYER:
+                raise RgcError("a layer norm's backward needs the forward's mean")
+            continue
+        _dense(t, torch.float32, name)
+        if tuple(t.shape) != (rows,):
+            raise RgcError(f"{name} must have one value per row")
+    if dX is None:
+        dX = torch.empty((rows, n), dtype=S.dtype, device=dev)
+    lddx = _norm_rows(dX, S, "dX")
+    pt = torch.float32 if weight is None else weight.dtype
+    dweight = torch.empty(n, dtype=pt, device=dev)
+    dbias = torch.empty(n, dtype=pt, device=dev) if bias else None
+    with _on(dev):
+        wp, wn, _keep = _scratch(workspace, lib.rgc_add_norm_backward_workspace_size(rows, n), dev)
+        _check(lib.rgc_add_norm_backward(kid, _DTYPES[S.dtype], wt, dY.data_ptr(), lddy, _pointer(dS), ldds, S.data_ptr(),
+                                         lds, _pointer(weight), _pointer(mean), rstd.data_ptr(), dX.data_ptr(), lddx,
+                                         dweight.data_ptr(), _pointer(dbias), rows, n, wp, wn, _stream(dev)))
+    return dX, dweight, dbias
+
+
 def _lists():
     """The compiled module that checks and unpacks lists of tensors."""
     try:
@@ -877,6 +1118,61 @@ def _adamw_list(ts, name: str, types, sizes, block: int = 1):
         raise RgcError(f"{name} must be contiguous tensors of one type ({' or '.join(types)}), on one device, of the "
                        "parameters' sizes")
     return got
+
+
+def _gradient_list(Gs):
+    """(count, types, pointers, sizes, device, ranges) of a list of dense gradients, bf16 and float32 in any order;
+    ranges: as _lists().disjoint takes them."""
+    got = _lists().pack_gradients(Gs)
+    if got is None:
+        raise RgcError("Gs must be contiguous bf16 or float32 tensors on one device")
+    n = len(Gs)
+    return (n, (ctypes.c_int * n).from_buffer_copy(got[2]), (_vp * n).from_buffer_copy(got[0]),
+            (_i64 * n).from_buffer_copy(got[1]), _need_gpu(Gs[0]), (got[0], got[3], 1))
+
+
+def _one_float(t: torch.Tensor, name: str) -> None:
+    _dense(t, torch.float32, name)
+    if t.numel() != 1:
+        raise RgcError(f"{name} must be one float32")
+
+
+def rgc_grad_norm_batch(Gs, max_norm: float = float("inf"), grad_scale: torch.Tensor | None = None,
+                        workspace: Workspace | None = None):
+    """(norm, scale), one float32 each on the device: the norm of all gradients Gs
+    (bf16 and float32) times grad_scale (a device float32, or None for 1), and
+    grad_scale min(1, max_norm / norm), the factor that clips them: rgc_adamw_batch's
+    grad_scale, or rgc_scale_batch's scale. A norm that is not finite gives a scale of NaN,
+    which skips the step. A tensor listed twice counts twice."""
+    lib = load_library()
+    if len(Gs) == 0:
+        raise RgcError("Gs must hold a tensor at least")
+    n, types, pointers, sizes, dev, _ = _gradient_list(Gs)
+    if grad_scale is not None:
+        _need_gpu(Gs[0], grad_scale)
+        _one_float(grad_scale, "grad_scale")
+    out = torch.empty(2, dtype=torch.float32, device=dev)
+    with _on(dev):
+        wp, wn, _keep = _scratch(workspace, lib.rgc_grad_norm_batch_workspace_size(n, sizes), dev)
+        _check(lib.rgc_grad_norm_batch(n, types, pointers, sizes, max_norm, _pointer(grad_scale), out.data_ptr(), wp, wn,
+                                       _stream(dev)))
+    return out[:1], out[1:]
+
+
+def rgc_scale_batch(Gs, scale: torch.Tensor):
+    """Gs times scale (a device float32), in place; a scale that is 1 or not finite
+    changes nothing. Returns Gs."""
+    lib = load_library()
+    if len(Gs) == 0:
+        return Gs
+    n, types, pointers, sizes, dev, ranges = _gradient_list(Gs)
+    _need_gpu(Gs[0], scale)
+    _one_float(scale, "scale")
+    if not _lists().disjoint((b"", b"", 1), ranges):
+        raise RgcError("a tensor is listed twice, or shares memory with another")
+    with _on(dev):
+        _check(lib.rgc_scale_batch(n, types, pointers, sizes, scale.data_ptr(), _stream(dev)))
+    return Gs
 
 
 def rgc_adamw_batch(Ps, Gs, Ms, Vs, lr: float, step: int, seed: int = 0, beta1: float = 0.9, beta2: float = 0.999,
