@@ -21,15 +21,17 @@
 // maximum and its two sums against it, brought to the new maximum once for every
 // batch of vectors it reads.
 //
-// Alternatives: each wave holds the largest entries it has met, in descending
-// order, one to a lane, as 64-bit keys: the value's bits in an order of unsigned
-// numbers, then the complement of the index, so that no two keys are equal and of equal
-// values the lowest index comes first. An entry is looked at only if it
-// reaches the threshold, the largest of the waves' `top`th keys, so that a row of n
-// entries makes about top (1 + log(n / top)) insertions in all: each a ballot for the
-// place and a shift by a lane. The first batch would insert nearly everything; its
-// threshold comes from the lanes' maxima, of which `top` lie at or above a number
-// found bit by bit. At the end the waves' lists are merged, two sorted lists of 64 at a time.
+// Alternatives: an entry's key is its value's bits in an order of unsigned numbers,
+// then the complement of its index, in 64 bits: no two keys are equal, and of equal values the
+// lowest index comes first. A wave keeps the keys that may be among the row's `top`
+// in a small list in LDS, in any order. An entry is looked at only if it reaches a
+// bar that `top` entries already reach: every lane's largest so far is an entry of its own, so
+// ceil(top / 4) of a wave's 64 lanes reach a number found bit by bit, and the least of the
+// four waves' numbers is the bar (below 4 alternatives the largest number that `top` of a wave's lanes reach). It is
+// raised after 1, 2, 4, .. batches, so that a row of n entries lists about top (1 +
+// log(n / 8192)) of them; where rows tie at the bar and the list fills, it
+// is cut down to its own `top`, and keys decide from then on. At the end
+// each listed key's place is the number of larger ones, counted by a thread of its own.
 #include <math.h>
 
 #include "rgc_internal.hpp"
@@ -46,6 +48,9 @@ constexpr int kLpWaves = kLpThreads / 64;
 constexpr int kLpBatch = 4;                              // vectors of eight that a thread reads together
 constexpr int kLpRound = kLpThreads * 8 * kLpBatch;      // entries of a workgroup's batch
 constexpr int64_t kLpMaxParts = 64;
+constexpr int kLpList = 128;                             // keys of a wave: `top` of them and one of each lane
+constexpr int kLpJoinThreads = 512;
+static_assert(kLpMaxTop + 64 <= kLpList, "a list cut down takes a key of every lane");
 constexpr float kLpFloor = -200.f;  // least z - m in a product with its exponential, which is 0 from -104 on
 constexpr float kLpFar = 1024.f;       // of lse: see above
 constexpr float kLpLog2e = 1.4426950408889634f;
@@ -90,6 +95,8 @@ struct LpVec<uint16_t> {
       if (i < count) v[i / 2] = i & 1 ? (v[i / 2] & 0xFFFFu) | (uint32_t)p[i] << 16 : (v[i / 2] & 0xFFFF0000u) | p[i];
   }
   __device__ __forceinline__ float get(int i) const { return __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16); }
+  // hides that the elements are those of before, so that they are unpacked anew and not kept
+  __device__ __forceinline__ void again() { asm volatile("" : "+v"(v)); }
   static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_bits_to_f32(*p); }
   static __device__ __forceinline__ void store(uint16_t* p, const float (&f)[8]) {
     *reinterpret_cast<any_t*>(p) = u32x4v_t{f32x2_to_bf16x2_rne(f[0], f[1]), f32x2_to_bf16x2_rne(f[2], f[3]),
@@ -112,6 +119,7 @@ struct LpVec<float> {
       if (i < count) (i < 4 ? a : b)[i & 3] = p[i];
   }
   __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
+  __device__ __forceinline__ void again() { asm volatile("" : "+v"(a), "+v"(b)); }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
   static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
     reinterpret_cast<any_t*>(p)[0] = f32x4_t{f[0], f[1], f[2], f[3]};
@@ -131,23 +139,44 @@ __device__ __forceinline__ float value_of(uint32_t order) {
 }
 __device__ __forceinline__ u64 key_of(float z, int index) { return (u64)order_of(z) << 32 | (uint32_t)~index; }
 
-__device__ __forceinline__ u64 read_lane(u64 v, int lane) {
-  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane), hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
-  return (u64)hi << 32 | lo;
+// How many of the keys list[0 .. count) are larger than a key.
+__device__ __forceinline__ int place_of(u64 key, const u64* list, int count) {
+  int place = 0;
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) place += list[i] > key;
+  return place;
 }
 
-// The 64 largest of two descending lists, in descending order: the pairwise
-// larger of one list and the other backwards, which rise and fall once, sorted by halving distances.
-__device__ __forceinline__ u64 merge_lists(u64 mine, u64 backwards) {
-  u64 v = mine > backwards ? mine : backwards;
+// Cuts a wave's list down to its `top` largest keys, in descending order; the last of them if there are as many, else 0.
+__device__ __forceinline__ u64 cut_list(u64* list, int& count, int top) {
   const int lane = threadIdx.x & 63;
+  const u64 a = lane < count ? list[lane] : 0, b = 64 + lane < count ? list[64 + lane] : 0;
+  const int pa = place_of(a, list, count), pb = place_of(b, list, count);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // every lane has read the list
+  if (lane < count && pa < top) list[pa] = a;
+  if (64 + lane < count && pb < top) list[pb] = b;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  count = count < top ? count : top;
+  return count == top ? list[top - 1] : 0;
+}
+
+// A number in LDS that other waves read or write meanwhile: whatever its latest value.
+__device__ __forceinline__ uint32_t get_shared(const uint32_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+__device__ __forceinline__ void put_shared(uint32_t* p, uint32_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+// The largest number of sixteen bits that `want` of the lanes' numbers reach (0 if there is none).
+__device__ __forceinline__ uint32_t reached(uint32_t mine, int want) {
+  uint32_t t = 0;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const u64 other = __shfl_xor(v, off, 64);
-    const bool upper = lane & off, greater = v > other;
-    v = upper != greater ? v : other;
+  for (int bit = 15; bit >= 0; --bit) {
+    const uint32_t next = t | 1u << bit;
+    if (__builtin_popcountll(__ballot(mine >= next)) >= want) t = next;
   }
-  return v;
+  return t;
 }
 
 // Joins (m, s, q) with another's: all sums against the larger maximum.
@@ -159,37 +188,32 @@ __device__ __forceinline__ void join_sums(float& m, float& s, float& q, float m1
   m = top;
 }
 
-// What a row gives, from its sums in every lane and its list, one key to a lane.
-template <typename ZT>
-__device__ __forceinline__ void finish_row(const LpArgs& a, int64_t row, float m, float s, float q, u64 list) {
-  const int lane = threadIdx.x & 63;
+// What a row gives beside its alternatives, from its sums; zy: its token's logit.
+__device__ __forceinline__ void finish_row(const LpArgs& a, int64_t row, int64_t y, float zy, float m, float s, float q) {
   const bool empty = m == -INFINITY && s == 0.f;
-  const float ls = logf(s), lse = empty ? -INFINITY : m + ls;
-  if (lane == 0) {
-    a.lse[row] = lse;
-    float h = ls - q / s;
-    h = empty || h < 0.f ? 0.f : h;  // (rounding can take it below 0; NaN stays)
-    if (a.tokens) {
-      const int64_t y = a.tokens[row];
-      const bool live = y >= 0 && y < a.V;
-      const float zy = live ? LpVec<ZT>::one(static_cast<const ZT*>(a.z) + row * a.ldz + y) : 0.f;
-      a.logp[row] = live ? (empty ? -INFINITY : zy - m - ls) : 0.f;
-      if (!live) h = 0.f;
-    }
-    a.entropy[row] = h;
-  }
-  if (lane < a.top) {
-    const float z = value_of((uint32_t)(list >> 32));
-    a.top_logp[row * a.top + lane] = empty ? -INFINITY : z - m - ls;
-    a.top_ids[row * a.top + lane] = (uint32_t)~(uint32_t)list;
-  }
+  const float ls = logf(s), h = ls - q / s;
+  const bool live = !a.tokens || (y >= 0 && y < a.V);
+  a.lse[row] = empty ? -INFINITY : m + ls;
+  if (a.tokens) a.logp[row] = live ? (empty ? -INFINITY : zy - m - ls) : 0.f;
+  a.entropy[row] = !live || empty || h < 0.f ? 0.f : h;  // (rounding can take it below 0; NaN stays)
+}
+__device__ __forceinline__ void put_alternative(const LpArgs& a, int64_t row, int place, u64 key, float m, float s) {
+  const bool empty = m == -INFINITY && s == 0.f;
+  a.top_logp[row * a.top + place] = empty ? -INFINITY : value_of((uint32_t)(key >> 32)) - m - logf(s);
+  a.top_ids[row * a.top + place] = (uint32_t)~(uint32_t)key;
+}
+
+template <typename ZT>
+__device__ __forceinline__ float token_logit(const LpArgs& a, int64_t row, int64_t y) {
+  return y >= 0 && y < a.V ? LpVec<ZT>::one(static_cast<const ZT*>(a.z) + row * a.ldz + y) : 0.f;
 }
 
 template <typename ZT, bool TOP>
-__global__ __launch_bounds__(kLpThreads) void lp_forward_kernel(LpArgs a) {
-  __shared__ u64 lists[kLpWaves][64];
+__global__ __launch_bounds__(kLpThreads, TOP ? 6 : 1) void lp_forward_kernel(LpArgs a) {
+  __shared__ __attribute__((aligned(16))) u64 lists[TOP ? kLpWaves : 1][kLpList];
+  __shared__ int counts[kLpWaves];
+  __shared__ uint32_t reach[kLpWaves];  // what ceil(top / 4) of each wave's lanes reach (below 4 alternatives, `top`)
   __shared__ f32x4_t sums[kLpWaves];
-  __shared__ u64 bar;  // the largest of the waves' thresholds: a key at or below it is not among the row's `top`
   const int lane = threadIdx.x & 63, wave = wave_index();
   const int64_t jobs = a.rows * a.parts;
   for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
@@ -197,12 +221,15 @@ __global__ __launch_bounds__(kLpThreads) void lp_forward_kernel(LpArgs a) {
     const int first = (int)(job - row * a.parts) * a.part;
     const int end = a.V - first < a.part ? a.V : first + a.part;
     const ZT* z = static_cast<const ZT*>(a.z) + row * a.ldz;
-    float m = -INFINITY, s = 0.f, q = 0.f;
-    u64 list = 0, limit = 0;  // limit: this wave's view of the bar
-    if (TOP) {
-      if (threadIdx.x == 0) bar = 0;
-      __syncthreads();
+    int64_t y = -1;
+    float zy = 0.f;
+    if (threadIdx.x == 0 && a.parts == 1 && a.tokens) {  // (here, so that nothing waits for it at the end)
+      y = a.tokens[row];
+      zy = token_logit<ZT>(a, row, y);
     }
+    float m = -INFINITY, s = 0.f, q = 0.f;
+    u64 limit = 0;  // a key at or below it is not among the row's `top`
+    int count = 0;
     for (int c0 = first; c0 < end; c0 += kLpRound) {
       LpVec<ZT> v[kLpBatch];
       const int c = c0 + 8 * (int)threadIdx.x;
@@ -218,16 +245,16 @@ __global__ __launch_bounds__(kLpThreads) void lp_forward_kernel(LpArgs a) {
           else if (at < end) v[u].load_some(z + at, end - at);
         }
       }
-      float high[kLpBatch], batch = -INFINITY;
+      float high[kLpBatch], top = m;
 #pragma unroll
       for (int u = 0; u < kLpBatch; ++u) {
         high[u] = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 8; ++e) high[u] = fmaxf(high[u], v[u].get(e));
-        batch = fmaxf(batch, high[u]);
+        top = fmaxf(top, high[u]);
       }
       {
-        const float top = fmaxf(m, batch), base = top == -INFINITY ? 0.f : top;
+        const float base = top == -INFINITY ? 0.f : top;
         const float d0 = m - base, f0 = lp_exp(d0);
         q = __builtin_fmaf(s, fmaxf(d0, kLpFloor), q) * f0;
         s *= f0;
@@ -244,101 +271,150 @@ __global__ __launch_bounds__(kLpThreads) void lp_forward_kernel(LpArgs a) {
           s += s8;
           q += q8;
         }
+        // the sums here: the compiler would take q's behind the alternatives, with all the terms they need
+        if (TOP) asm volatile("" : "+v"(s), "+v"(q));
       }
       if constexpr (TOP) {
-        if (c0 == first) {
-          // the largest number of sixteen bits that `top` of the lanes' maxima reach
-          const uint32_t mine = order_of(batch) >> 16;
-          uint32_t reach = 0;
+        const int batch = (c0 - first) / kLpRound + 1;
+        if ((batch & (batch - 1)) == 0) {
+          const uint32_t mine = reached(order_of(m) >> 16, a.top < kLpWaves ? a.top : (a.top + kLpWaves - 1) / kLpWaves);
+          if (lane == 0) put_shared(&reach[wave], mine);
+        }
+        if (c0 == first) __syncthreads();
+        uint32_t all = get_shared(&reach[0]);
 #pragma unroll
-          for (int bit = 15; bit >= 0; --bit) {
-            const uint32_t t = reach | 1u << bit;
-            if (__builtin_popcountll(__ballot(mine >= t)) >= a.top) reach = t;
-          }
-          limit = reach ? ((u64)reach << 48) - 1 : 0;
-          if (lane == 0 && limit) atomicMax(&bar, limit);
+        for (int w = 1; w < kLpWaves; ++w) {
+          const uint32_t other = get_shared(&reach[w]);
+          all = (other < all) != (a.top < kLpWaves) ? other : all;
         }
-        {
-          const u64 seen = *(volatile u64*)&bar;
-          limit = seen > limit ? seen : limit;
-          limit = uniform_u64(limit);
-        }
-        const u64 before = limit;
-        float reach = limit ? value_of((uint32_t)(limit >> 32)) : -INFINITY;  // (a NaN where the limit is one)
+        all = __builtin_amdgcn_readfirstlane(all);
+        const u64 barrier = all ? ((u64)all << 48) - 1 : 0;
+        limit = barrier > limit ? barrier : limit;
+        // the least value with a key above the limit: of the limit's own value all entries from here on have lower keys
+        // than those of a list that was cut down to it (a NaN above NaN and infinity: all pass, and keys decide)
+        const float bar = limit ? value_of((uint32_t)(limit >> 32) + 1) : -INFINITY;
         const bool odd = !(s - s == 0.f);  // NaN or infinities among this thread's entries
+        uint32_t bits = 0;                 // the entries of this thread's batch that reach the bar
 #pragma unroll
         for (int u = 0; u < kLpBatch; ++u) {
-          if (!__any(odd || !(high[u] < reach))) continue;
-          const int at = c + u * (8 * kLpThreads);
+          if (!__any(odd || !(high[u] < bar))) continue;
+          v[u].again();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = v[u].get(e);
-            if (!__any(!(x < reach))) continue;
-            const u64 key = at + e < end ? key_of(x, at + e) : 0;
-            u64 todo = __ballot(key > limit);
-            while (todo) {
-              const int from = __builtin_ctzll(todo);
-              const u64 k = read_lane(key, from);
-              const int place = __builtin_popcountll(__ballot(list > k));
-              const u64 above = __shfl_up(list, 1, 64);
-              list = lane < place ? list : lane == place ? k : above;
-              const u64 last = read_lane(list, a.top - 1);
-              limit = last > limit ? last : limit;
-              todo &= todo - 1;
-              todo &= __ballot(key > limit);
-            }
-            reach = limit ? value_of((uint32_t)(limit >> 32)) : -INFINITY;
-          }
+          for (int e = 0; e < 8; ++e) bits |= (v[u].get(e) < bar ? 0u : 1u) << (8 * u + e);
         }
-        if (lane == 0 && limit > before) atomicMax(&bar, limit);
+        // an entry of each thread at a time, loaded again: the place of a vector's element is no register's name
+        while (__any(bits != 0)) {
+          const int which = bits ? __builtin_ctz(bits) : 0, at = c + (which >> 3) * (8 * kLpThreads) + (which & 7);
+          const bool here = bits != 0 && at < end;
+          bits &= bits - 1;
+          const u64 key = here ? key_of(LpVec<ZT>::one(z + at), at) : 0;
+          u64 take = __ballot(key > limit);
+          if (count + __builtin_popcountll(take) > kLpList) {
+            const u64 last = cut_list(lists[wave], count, a.top);
+            limit = uniform_u64(last > limit ? last : limit);
+            take = __ballot(key > limit);
+          }
+          if (key > limit) lists[wave][count + __builtin_popcountll(take & ((u64(1) << lane) - 1))] = key;
+          count += __builtin_popcountll(take);
+        }
       }
     }
     // the lanes' sums, then the waves'
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1)
       join_sums(m, s, q, __shfl_xor(m, off, 64), __shfl_xor(s, off, 64), __shfl_xor(q, off, 64));
-    if (lane == 0) sums[wave] = f32x4_t{m, s, q, 0.f};
-    if (TOP) lists[wave][lane] = list;
+    if (lane == 0) {
+      sums[wave] = f32x4_t{m, s, q, 0.f};
+      counts[wave] = count;
+    }
     __syncthreads();
-    if (wave == 0) {
+    if (TOP || wave == 0) {
+      // (in one order in every wave)
+      m = sums[0].x, s = sums[0].y, q = sums[0].z;
 #pragma unroll
-      for (int w = 1; w < kLpWaves; ++w) {
-        join_sums(m, s, q, sums[w].x, sums[w].y, sums[w].z);
-        if (TOP) list = merge_lists(list, lists[w][63 - lane]);
-      }
-      if (a.parts == 1) {
-        finish_row<ZT>(a, row, m, s, q, list);
-      } else {
-        if (lane == 0) a.sums[job] = f32x4_t{m, s, q, 0.f};
-        if (TOP && lane < a.top) a.keys[job * a.top + lane] = list;
+      for (int w = 1; w < kLpWaves; ++w) join_sums(m, s, q, sums[w].x, sums[w].y, sums[w].z);
+      if (threadIdx.x == 0) {
+        if (a.parts == 1) finish_row(a, row, y, zy, m, s, q);
+        else a.sums[job] = f32x4_t{m, s, q, 0.f};
       }
     }
-    __syncthreads();  // before the next row's bar, sums and lists
+    if constexpr (TOP) {
+#pragma unroll 1
+      for (int i = threadIdx.x; i < kLpWaves * kLpList; i += kLpThreads) {
+        if (i % kLpList >= counts[i / kLpList]) continue;
+        const u64 key = lists[i / kLpList][i % kLpList];
+        int place = 0;
+#pragma unroll 1
+        for (int w = 0; w < kLpWaves; ++w) place += place_of(key, lists[w], counts[w]);
+        if (place >= a.top) continue;
+        if (a.parts == 1) put_alternative(a, row, place, key, m, s);
+        else a.keys[job * a.top + place] = key;
+      }
+      // a part of fewer entries than `top` fills up with keys below all others
+      if (a.parts > 1) {
+        int all = 0;
+        for (int w = 0; w < kLpWaves; ++w) all += counts[w];
+        for (int i = all + (int)threadIdx.x; i < a.top; i += kLpThreads) a.keys[job * a.top + i] = 0;
+      }
+    }
+    __syncthreads();  // before the next row's sums and lists
   }
 }
 
-// Joins a row's parts: a wave per row.
+// Joins a row's parts: a workgroup per row. The parts' lists are in descending order, so `top`
+// keys reach the least of their ceil(top / parts)th ones, and the largest of their last: only keys that
+// reach both are ranked, about twice `top` of them.
 template <typename ZT, bool TOP>
-__global__ __launch_bounds__(64) void lp_join_kernel(LpArgs a) {
-  const int lane = threadIdx.x;
+__global__ __launch_bounds__(kLpJoinThreads) void lp_join_kernel(LpArgs a) {
+  __shared__ __attribute__((aligned(16))) u64 list[TOP ? kLpMaxParts * kLpMaxTop : 1];
+  __shared__ int kept;
+  const int lane = threadIdx.x & 63;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    int64_t y = -1;
+    float zy = 0.f;
+    if (threadIdx.x == 0 && a.tokens) {
+      y = a.tokens[row];
+      zy = token_logit<ZT>(a, row, y);
+    }
     float m = -INFINITY, s = 0.f, q = 0.f;
     if (lane < a.parts) {
       const f32x4_t x = a.sums[row * a.parts + lane];
       m = x.x, s = x.y, q = x.z;
     }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-      join_sums(m, s, q, __shfl_xor(m, off, 64), __shfl_xor(s, off, 64), __shfl_xor(q, off, 64));
-    u64 list = 0;
+    u64 bar = ~u64(0), last = 0;
+    const u64* keys = a.keys + row * a.parts * a.top;
     if constexpr (TOP) {
-      const u64* keys = a.keys + row * a.parts * a.top;
-      for (int p = 0; p < a.parts; ++p) {
-        const int back = 63 - lane;
-        list = merge_lists(list, back < a.top ? keys[(int64_t)p * a.top + back] : 0);
+      if (lane < a.parts) {
+        bar = keys[lane * a.top + (a.top + a.parts - 1) / a.parts - 1];
+        last = keys[lane * a.top + a.top - 1];
+      }
+      if (threadIdx.x == 0) kept = 0;
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      join_sums(m, s, q, __shfl_xor(m, off, 64), __shfl_xor(s, off, 64), __shfl_xor(q, off, 64));
+      if constexpr (TOP) {
+        const u64 b1 = __shfl_xor(bar, off, 64), l1 = __shfl_xor(last, off, 64);
+        bar = b1 < bar ? b1 : bar, last = l1 > last ? l1 : last;
       }
     }
-    finish_row<ZT>(a, row, m, s, q, list);
+    if (threadIdx.x == 0) finish_row(a, row, y, zy, m, s, q);
+    if constexpr (TOP) {
+      bar = last > bar ? last : bar;
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.parts * a.top; i += kLpJoinThreads) {
+        const u64 key = keys[i];
+        if (key != 0 && key >= bar) list[atomicAdd(&kept, 1)] = key;
+      }
+      __syncthreads();
+      const int count = kept;
+      for (int i = threadIdx.x; i < count; i += kLpJoinThreads) {
+        const u64 key = list[i];
+        const int place = place_of(key, list, count);
+        if (place < a.top) put_alternative(a, row, place, key, m, s);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -427,7 +503,7 @@ size_t elem(rgc_dtype_t t) { return t == RGC_F32 ? 4 : 2; }
 // Parts of a row of the forward: one where there are rows enough for eight workgroups to
 // each compute unit, else as many as make that, of at least half a batch.
 int64_t parts_of(int64_t rows, int64_t V) {
-  const int64_t want = ((int64_t)device_compute_units() * 8 + rows - 1) / rows;
+  const int64_t want = ((int64_t)device_compute_units() * 4 + rows / 2) / rows;
   const int64_t most = (V + kLpRound / 2 - 1) / (kLpRound / 2);
   int64_t parts = want < most ? want : most;
   if (parts > kLpMaxParts) parts = kLpMaxParts;
@@ -459,7 +535,7 @@ unsigned grid_of(int64_t jobs) {
 template <typename ZT, bool TOP>
 rgc_status_t forward_launch(const LpArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((lp_forward_kernel<ZT, TOP>), dim3(grid_of(a.rows * a.parts)), dim3(kLpThreads), 0, s, a);
-  if (a.parts > 1) hipLaunchKernelGGL((lp_join_kernel<ZT, TOP>), dim3(grid_of(a.rows)), dim3(64), 0, s, a);
+  if (a.parts > 1) hipLaunchKernelGGL((lp_join_kernel<ZT, TOP>), dim3(grid_of(a.rows)), dim3(TOP ? kLpJoinThreads : 64), 0, s, a);
   return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP;
 }
 

@@ -305,8 +305,9 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
 // Backward with the row in registers; see the head of the file. The weight is
 // kept in LDS. With c = x - mu: dw += (g rstd) c, and dx = rstd h - rstd c1 -
 // c (rstd^2 c2), c1 = mean(h) and c2 = mean(h c).
-// ADD: dx += r, the sum's own gradient, before it is rounded.
-template <typename XT, bool RAGGED, int NV, int TPR, int THREADS, bool ADD>
+// ADD: dx += r, the sum's own gradient, before it is rounded. DB: db is formed (its
+// sums take as many registers as dw's, which the rows of r need).
+template <typename XT, bool RAGGED, int NV, int TPR, int THREADS, bool ADD, bool DB>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
   constexpr int GROUPS = THREADS / TPR, COLS = TPR * NV * 8;
   __shared__ float slots[2][2 * THREADS / 64];
@@ -319,7 +320,10 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[j][e] = 0.f, db[j][e] = 0.f;
+    for (int e = 0; e < 8; ++e) {
+      dw[j][e] = 0.f;
+      if constexpr (DB) db[j][e] = 0.f;
+    }
   __syncthreads();
   const int64_t stride = (int64_t)gridDim.x * GROUPS;
   int parity = 0;
@@ -327,14 +331,16 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
     const int64_t row = row0 + grp;
     const bool live = row < a.rows;
     if (TPR <= 64 && !live) break;  // (wider groups meet at the barriers)
-    Raw<XT> rx[NV], rg[NV];
+    Raw<XT> rx[NV], rg[NV], rs[ADD ? NV : 1];
     const XT* x = static_cast<const XT*>(a.x) + (live ? row : 0) * a.ldx;
     const XT* g = static_cast<const XT*>(a.dy) + (live ? row : 0) * a.lddy;
+    const XT* r = ADD ? static_cast<const XT*>(a.r) + (live ? row : 0) * a.ldr : nullptr;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = live ? (j * TPR + t) * 8 : n;
       load_at<RAGGED>(rx[j], x, c, n);
       load_at<RAGGED>(rg[j], g, c, n);
+      if constexpr (ADD) load_at<RAGGED>(rs[j], r, c, n);
     }
     const float mu = live && a.centre ? a.mean[row] : 0.f, rstd = live ? a.rstd[row] : 0.f;
     float sum[2] = {0.f, 0.f};
@@ -348,17 +354,14 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
         sum[0] += h;
         sum[1] = __builtin_fmaf(h, c, sum[1]);
         dw[j][e] = __builtin_fmaf(gv * rstd, c, dw[j][e]);
-        db[j][e] += gv;
+        if constexpr (DB) db[j][e] += gv;
       }
       // the sums here and not behind the stores, where the compiler would take them with all they need
 #pragma unroll
-      for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(dw[j][e]), "+v"(db[j][e]));
-    }
-    Raw<XT> rs[ADD ? NV : 1];
-    if constexpr (ADD) {
-      const XT* r = static_cast<const XT*>(a.r) + (live ? row : 0) * a.ldr;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) load_at<RAGGED>(rs[j], r, live ? (j * TPR + t) * 8 : n, n);
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (DB) asm volatile("" : "+v"(dw[j][e]), "+v"(db[j][e]));
+        else asm volatile("" : "+v"(dw[j][e]));
+      }
     }
     group_sum<TPR>(sum, slots[parity]);
     const float k1 = a.centre ? sum[0] * inv_n * rstd : 0.f, k2 = sum[1] * inv_n * rstd * rstd * rstd;
@@ -375,20 +378,22 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
       for (int e = 0; e < 8; ++e)
         f[e] = __builtin_fmaf(rg[j].get(e) * w[e], rstd, -__builtin_fmaf(rx[j].get(e) - mu, k2, k1));
       if constexpr (ADD) {
+        rs[j].again();
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] += rs[j].get(e);
       }
       store_at<RAGGED>(dx, c, n, f);
+      if constexpr (ADD) __builtin_amdgcn_sched_barrier(0);
     }
   }
   // the workgroup's partial rows: dw, then db
-  for (int which = 0; which < 1 + a.db; ++which) {
+  for (int which = 0; which < (DB ? 1 + a.db : 1); ++which) {
     float* part = a.part + ((int64_t)which * gridDim.x + blockIdx.x) * a.n;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mem[grp * COLS + (j * TPR + t) * 8 + e] = which ? db[j][e] : dw[j][e];
+      for (int e = 0; e < 8; ++e) mem[grp * COLS + (j * TPR + t) * 8 + e] = DB && which ? db[j][e] : dw[j][e];
     __syncthreads();
     for (int64_t c = threadIdx.x; c < n; c += THREADS) {
       float s = 0.f;
@@ -540,14 +545,14 @@ int64_t backward_groups(int64_t rows, int64_t n, rgc_dtype_t xt) {
   return need < cus ? need : cus;
 }
 
-template <bool ADD, typename XT, int NV, int TPR, int THREADS>
+template <bool ADD, bool DB, typename XT, int NV, int TPR, int THREADS>
 void backward_launch(const NormArgs& a, int64_t G, hipStream_t s) {
   const dim3 grid((unsigned)G);
-  if (a.n % 8) hipLaunchKernelGGL((norm_backward_kernel<XT, true, NV, TPR, THREADS, ADD>), grid, dim3(THREADS), 0, s, a);
-  else hipLaunchKernelGGL((norm_backward_kernel<XT, false, NV, TPR, THREADS, ADD>), grid, dim3(THREADS), 0, s, a);
+  if (a.n % 8) hipLaunchKernelGGL((norm_backward_kernel<XT, true, NV, TPR, THREADS, ADD, DB>), grid, dim3(THREADS), 0, s, a);
+  else hipLaunchKernelGGL((norm_backward_kernel<XT, false, NV, TPR, THREADS, ADD, DB>), grid, dim3(THREADS), 0, s, a);
 }
 
-template <bool ADD, typename XT>
+template <bool ADD, bool DB, typename XT>
 void backward_pick(const NormArgs& a, int64_t G, hipStream_t s) {
   if (a.n > kNormHeldBackward) {
     // (the columns first: dX may take the place of X or dY)
@@ -558,19 +563,19 @@ void backward_pick(const NormArgs& a, int64_t G, hipStream_t s) {
                        a);
     return;
   }
-  if (a.n <= 128) return backward_launch<ADD, XT, 1, 16, 1024>(a, G, s);
-  if (a.n <= 512) return backward_launch<ADD, XT, 1, 64, 1024>(a, G, s);
-  if (a.n <= 1024) return backward_launch<ADD, XT, 2, 64, 1024>(a, G, s);
+  if (a.n <= 128) return backward_launch<ADD, DB, XT, 1, 16, 1024>(a, G, s);
+  if (a.n <= 512) return backward_launch<ADD, DB, XT, 1, 64, 1024>(a, G, s);
+  if (a.n <= 1024) return backward_launch<ADD, DB, XT, 2, 64, 1024>(a, G, s);
   if constexpr (sizeof(XT) == 2) {  // up to 64 elements to a lane
-    if (a.n <= 2048) return backward_launch<ADD, XT, 4, 64, 1024>(a, G, s);
-    if (a.n <= 4096) return backward_launch<ADD, XT, 8, 64, 512>(a, G, s);
-    if (a.n <= 8192) return backward_launch<ADD, XT, 8, 128, 512>(a, G, s);
-    backward_launch<ADD, XT, 8, 256, 512>(a, G, s);
+    if (a.n <= 2048) return backward_launch<ADD, DB, XT, 4, 64, 1024>(a, G, s);
+    if (a.n <= 4096) return backward_launch<ADD, DB, XT, 8, 64, 512>(a, G, s);
+    if (a.n <= 8192) return backward_launch<ADD, DB, XT, 8, 128, 512>(a, G, s);
+    backward_launch<ADD, DB, XT, 8, 256, 512>(a, G, s);
   } else {  // up to 32
-    if (a.n <= 2048) return backward_launch<ADD, XT, 4, 64, 512>(a, G, s);
-    if (a.n <= 4096) return backward_launch<ADD, XT, 4, 128, 512>(a, G, s);
-    if (a.n <= 8192) return backward_launch<ADD, XT, 4, 256, 512>(a, G, s);
-    backward_launch<ADD, XT, 4, 512, 512>(a, G, s);
+    if (a.n <= 2048) return backward_launch<ADD, DB, XT, 4, 64, 512>(a, G, s);
+    if (a.n <= 4096) return backward_launch<ADD, DB, XT, 4, 128, 512>(a, G, s);
+    if (a.n <= 8192) return backward_launch<ADD, DB, XT, 4, 256, 512>(a, G, s);
+    backward_launch<ADD, DB, XT, 4, 512, 512>(a, G, s);
   }
 }
 
@@ -641,11 +646,11 @@ rgc_status_t backward_impl(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt,
   a.w_f32 = wt == RGC_F32, a.centre = kind == RGC_NORM_LAYER, a.db = dbias != nullptr;
   const int64_t G = backward_groups(rows, n, xt);
   if (dS) {
-    if (xt == RGC_F32) backward_pick<true, float>(a, G, s);
-    else backward_pick<true, uint16_t>(a, G, s);
+    if (xt == RGC_F32) dbias ? backward_pick<true, true, float>(a, G, s) : backward_pick<true, false, float>(a, G, s);
+    else dbias ? backward_pick<true, true, uint16_t>(a, G, s) : backward_pick<true, false, uint16_t>(a, G, s);
   } else {
-    if (xt == RGC_F32) backward_pick<false, float>(a, G, s);
-    else backward_pick<false, uint16_t>(a, G, s);
+    if (xt == RGC_F32) backward_pick<false, true, float>(a, G, s);
+    else backward_pick<false, true, uint16_t>(a, G, s);
   }
   if ((st = launched()) != RGC_OK) return st;
   hipLaunchKernelGGL(norm_params_kernel, params, dim3(1024), 0, s, a.part, G, n, a.w_f32, dweight, dbias);
