@@ -528,7 +528,7 @@ rgc_status_t rgc_log_prob_backward(rgc_dtype_t zt, const void* Z, int64_t ldz, c
 
 /* ---- The gradients' global norm, and clipping ------------------------------------
  *
- * out[0] = norm = |s| sqrt(sum over n tensors of their squares), out[1] = scale =
+ * *norm = |s| sqrt(sum over n tensors of their squares), *scale =
  * s min(1, max_norm / norm), s = *grad_scale (1 if NULL): the factor that brings
  * gradients that are to be multiplied by s anyway to a norm of max_norm at most.
  * scale is what rgc_adamw_batch takes as grad_scale, on the device. A norm that is
@@ -537,13 +537,13 @@ rgc_status_t rgc_log_prob_backward(rgc_dtype_t zt, const void* Z, int64_t ldz, c
  * rgc_scale_batch multiplies the tensors by *scale in place (bf16 rounded to
  * nearest); a scale that is 1 or not finite changes nothing.
  * Gs, gts, numels: HOST arrays of n entries (at most 2^24): tensor i has numels[i] (at most 2^34)
- * contiguous elements of type gts[i], aligned to its elements. out: float[2].
+ * contiguous elements of type gts[i], aligned to its elements. norm, scale: a float each.
  * max_norm may be infinite (the norm alone); RGC_ERR_VALUE if it is negative or NaN.
  * In rgc_scale_batch no two tensors share memory. */
 size_t rgc_grad_norm_batch_workspace_size(int64_t n, const int64_t* numels);
 rgc_status_t rgc_grad_norm_batch(int64_t n, const rgc_dtype_t* gts, const void* const* Gs, const int64_t* numels,
-                                 double max_norm, const float* grad_scale, float* out, void* ws, size_t ws_bytes,
-                                 void* stream);
+                                 double max_norm, const float* grad_scale, float* norm, float* scale, void* ws,
+                                 size_t ws_bytes, void* stream);
 rgc_status_t rgc_scale_batch(int64_t n, const rgc_dtype_t* gts, void* const* Gs, const int64_t* numels,
                              const float* scale, void* stream);
 

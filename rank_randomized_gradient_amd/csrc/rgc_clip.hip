@@ -136,9 +136,9 @@ __global__ __launch_bounds__(kClipThreads) void clip_squares_kernel(ClipArgs a) 
   if (threadIdx.x == 0) a.part[blockIdx.x] = (waves[0] + waves[1]) + (waves[2] + waves[3]);
 }
 
-// The partial sums added, and out = norm, scale.
+// The partial sums added, and the norm and the scale.
 __global__ __launch_bounds__(1024) void clip_join_kernel(const double* part, int64_t count, double max_norm,
-                                                         const float* grad_scale, float* out) {
+                                                         const float* grad_scale, float* norm_out, float* scale_out) {
   __shared__ double waves[16];
   double s = 0;
 #pragma unroll 8
@@ -152,9 +152,9 @@ __global__ __launch_bounds__(1024) void clip_join_kernel(const double* part, int
   for (int i = 0; i < 16; ++i) s += waves[i];
   const double factor = grad_scale ? (double)*grad_scale : 1.0;
   const double norm = __builtin_fabs(factor) * sqrt(s);
-  out[0] = (float)norm;
+  *norm_out = (float)norm;
   // (the difference is 0 for every finite number)
-  out[1] = norm - norm == 0 ? (float)(norm > max_norm ? factor * (max_norm / norm) : factor) : __builtin_nanf("");
+  *scale_out = norm - norm == 0 ? (float)(norm > max_norm ? factor * (max_norm / norm) : factor) : __builtin_nanf("");
 }
 
 template <typename Vec, typename T>
@@ -258,13 +258,13 @@ extern "C" size_t rgc_grad_norm_batch_workspace_size(int64_t n, const int64_t* n
 }
 
 extern "C" rgc_status_t rgc_grad_norm_batch(int64_t n, const rgc_dtype_t* gts, const void* const* Gs,
-                                            const int64_t* numels, double max_norm, const float* grad_scale, float* out,
-                                            void* ws, size_t ws_bytes, void* stream) {
+                                            const int64_t* numels, double max_norm, const float* grad_scale, float* norm,
+                                            float* scale, void* ws, size_t ws_bytes, void* stream) {
   rgc_status_t st = check_tensors(n, gts, Gs, numels);
   if (st != RGC_OK) return st;
   if (!(max_norm >= 0)) return RGC_ERR_VALUE;
-  if (!out) return RGC_ERR_NULL;
-  if (!aligned_to(out, 4) || !aligned_to(grad_scale, 4)) return RGC_ERR_ALIGN;
+  if (!norm || !scale) return RGC_ERR_NULL;
+  if (!aligned_to(norm, 4) || !aligned_to(scale, 4) || !aligned_to(grad_scale, 4)) return RGC_ERR_ALIGN;
   const int64_t chunk = chunk_of(n, numels), chunks = chunks_of(n, numels, chunk);
   if (chunks > 0 && (!ws || ws_bytes < (size_t)chunks * sizeof(double))) return RGC_ERR_WORKSPACE;
   if (!aligned_to(ws, 256)) return RGC_ERR_ALIGN;
@@ -277,7 +277,7 @@ extern "C" rgc_status_t rgc_grad_norm_batch(int64_t n, const rgc_dtype_t* gts, c
   });
   if (st != RGC_OK) return st;
   hipLaunchKernelGGL(clip_join_kernel, dim3(1), dim3(1024), 0, s, static_cast<const double*>(ws), chunks, max_norm,
-                     grad_scale, out);
+                     grad_scale, norm, scale);
   return hipGetLastError() == hipSuccess ? RGC_OK : RGC_ERR_HIP;
 }
 

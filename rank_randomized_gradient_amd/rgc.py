@@ -158,7 +158,7 @@ SIGNATURES = {
                                              _vp]),
     "rgc_grad_norm_batch_workspace_size": (_sz, [_i64, ctypes.POINTER(_i64)]),
     "rgc_grad_norm_batch": (ctypes.c_int, [_i64, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(_vp), ctypes.POINTER(_i64),
-                                           _f64, _vp, _vp, _vp, _sz, _vp]),
+                                           _f64, _vp, _vp, _vp, _vp, _sz, _vp]),
     "rgc_scale_batch": (ctypes.c_int, [_i64, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(_vp), ctypes.POINTER(_i64),
                                        _vp, _vp]),
     "rgc_adamw_batch_with": (ctypes.c_int, [ctypes.c_uint, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
@@ -728,6 +728,18 @@ def _scratch(workspace: Workspace | None, nbytes: int, dev: torch.device):
     return ctypes.c_void_p(buf.data_ptr()), nbytes, buf
 
 
+def _fresh(like: torch.Tensor, workspace: Workspace | None, nbytes: int, *specs):
+    """The new tensors of `specs` (a dtype and a shape each, None for none) on like's device, then the
+    call's workspace as _scratch gives it. One call of the compiled module: an allocation through Python costs
+    twice as much, and a small call has five."""
+    if workspace is not None or nbytes == 0:
+        made = _lists().fresh(like, *specs)
+        scratch = _scratch(workspace, nbytes, like.device) if workspace is not None else (None, 0, None)
+        return (*made, scratch)
+    *made, buf = _lists().fresh(like, *specs, torch.uint8, (nbytes,))
+    return (*made, (buf.data_ptr(), nbytes, buf))
+
+
 def _head_args(X, W, targets, name="targets"):
     ldx = _rows(X, torch.bfloat16, "X")
     ldw = _rows(W, torch.bfloat16, "W")
@@ -821,10 +833,11 @@ def rgc_linear_log_prob_forward(X: torch.Tensor, W: torch.Tensor, tokens: torch.
         if P.dim() != 2 or P.shape[0] != k or P.shape[1] == 0:
             raise RgcError("P must be k x r with k = X.shape[1]")
         r = P.shape[1]
-        XP = torch.empty((T, r), dtype=torch.bfloat16, device=dev)
-    logp, entropy, lse = (torch.empty(T, dtype=torch.float32, device=dev) for _ in range(3))
+    f32 = torch.float32
     with _on(dev):
-        wp, wn, _keep = _scratch(workspace, lib.rgc_linear_log_prob_forward_workspace_size(T, V, k, r), dev)
+        logp, entropy, lse, XP, (wp, wn, _keep) = _fresh(
+            X, workspace, lib.rgc_linear_log_prob_forward_workspace_size(T, V, k, r), f32, (T,), f32, (T,), f32, (T,),
+            torch.bfloat16, (T, r) if r else None)
         _check(lib.rgc_linear_log_prob_forward(X.data_ptr(), ldx, W.data_ptr(), ldw, P.data_ptr() if r else None,
                                                tokens.data_ptr(), logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
                                                XP.data_ptr() if r else None, T, V, k, r, wp, wn, _stream(dev)))
@@ -915,12 +928,11 @@ def rgc_log_prob_forward(Z: torch.Tensor, tokens: torch.Tensor | None = None, to
             raise RgcError("tokens must have one value per row of Z")
     if not 0 <= top <= 64:
         raise RgcError("top must lie in 0 .. 64")
-    logp = torch.empty(rows, dtype=torch.float32, device=dev) if tokens is not None else None
-    entropy, lse = (torch.empty(rows, dtype=torch.float32, device=dev) for _ in range(2))
-    top_logp = torch.empty((rows, top), dtype=torch.float32, device=dev) if top else None
-    top_ids = torch.empty((rows, top), dtype=torch.int64, device=dev) if top else None
+    f32, some = torch.float32, (rows, top) if top else None
     with _on(dev):
-        wp, wn, _keep = _scratch(workspace, lib.rgc_log_prob_forward_workspace_size(rows, V, top), dev)
+        entropy, lse, logp, top_logp, top_ids, (wp, wn, _keep) = _fresh(
+            Z, workspace, lib.rgc_log_prob_forward_workspace_size(rows, V, top), f32, (rows,), f32, (rows,),
+            f32, (rows,) if tokens is not None else None, f32, some, torch.int64, some)
         _check(lib.rgc_log_prob_forward(_DTYPES[Z.dtype], Z.data_ptr(), ldz, _pointer(tokens), _pointer(logp),
                                         entropy.data_ptr(), lse.data_ptr(), top, _pointer(top_logp), _pointer(top_ids),
                                         rows, V, wp, wn, _stream(dev)))
@@ -1050,16 +1062,15 @@ def rgc_add_norm_forward(X: torch.Tensor, R: torch.Tensor, weight: torch.Tensor 
     rows, n = X.shape
     kid = _norm_kind(kind)
     wt = _norm_params(n, weight, bias)
-    if S is None:
-        S = torch.empty((rows, n), dtype=X.dtype, device=dev)
-    if Y is None:
-        Y = torch.empty((rows, n), dtype=X.dtype, device=dev)
-    lds, ldy = _norm_rows(S, X, "S"), _norm_rows(Y, X, "Y")
-    if S.data_ptr() == Y.data_ptr() and S.numel() > 0:
+    lds = _norm_rows(S, X, "S") if S is not None else n
+    ldy = _norm_rows(Y, X, "Y") if Y is not None else n
+    if S is not None and Y is not None and S.data_ptr() == Y.data_ptr() and S.numel() > 0:
         raise RgcError("S and Y must be two tensors")
-    mean = torch.empty(rows, dtype=torch.float32, device=dev) if kid == RGC_NORM_LAYER else None
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     with _on(dev):
+        newS, newY, mean, rstd, _ = _fresh(X, None, 0, X.dtype, (rows, n) if S is None else None,
+                                           X.dtype, (rows, n) if Y is None else None,
+                                           torch.float32, (rows,) if kid == RGC_NORM_LAYER else None, torch.float32, (rows,))
+        S, Y = newS if S is None else S, newY if Y is None else Y
         _check(lib.rgc_add_norm_forward(kid, _DTYPES[X.dtype], wt, X.data_ptr(), ldx, R.data_ptr(), ldr,
                                         _pointer(weight), _pointer(bias), eps, S.data_ptr(), lds, Y.data_ptr(), ldy,
                                         _pointer(mean), rstd.data_ptr(), rows, n, _stream(dev)))
@@ -1087,14 +1098,13 @@ def rgc_add_norm_backward(dY: torch.Tensor, dS: torch.Tensor | None, S: torch.Te
         _dense(t, torch.float32, name)
         if tuple(t.shape) != (rows,):
             raise RgcError(f"{name} must have one value per row")
-    if dX is None:
-        dX = torch.empty((rows, n), dtype=S.dtype, device=dev)
-    lddx = _norm_rows(dX, S, "dX")
+    lddx = _norm_rows(dX, S, "dX") if dX is not None else n
     pt = torch.float32 if weight is None else weight.dtype
-    dweight = torch.empty(n, dtype=pt, device=dev)
-    dbias = torch.empty(n, dtype=pt, device=dev) if bias else None
     with _on(dev):
-        wp, wn, _keep = _scratch(workspace, lib.rgc_add_norm_backward_workspace_size(rows, n), dev)
+        new, dweight, dbias, (wp, wn, _keep) = _fresh(S, workspace, lib.rgc_add_norm_backward_workspace_size(rows, n),
+                                                      S.dtype, (rows, n) if dX is None else None, pt, (n,),
+                                                      pt, (n,) if bias else None)
+        dX = new if dX is None else dX
         _check(lib.rgc_add_norm_backward(kid, _DTYPES[S.dtype], wt, dY.data_ptr(), lddy, _pointer(dS), ldds, S.data_ptr(),
                                          lds, _pointer(weight), _pointer(mean), rstd.data_ptr(), dX.data_ptr(), lddx,
                                          dweight.data_ptr(), _pointer(dbias), rows, n, wp, wn, _stream(dev)))
@@ -1151,12 +1161,12 @@ def rgc_grad_norm_batch(Gs, max_norm: float = float("inf"), grad_scale: torch.Te
     if grad_scale is not None:
         _need_gpu(Gs[0], grad_scale)
         _one_float(grad_scale, "grad_scale")
-    out = torch.empty(2, dtype=torch.float32, device=dev)
     with _on(dev):
-        wp, wn, _keep = _scratch(workspace, lib.rgc_grad_norm_batch_workspace_size(n, sizes), dev)
-        _check(lib.rgc_grad_norm_batch(n, types, pointers, sizes, max_norm, _pointer(grad_scale), out.data_ptr(), wp, wn,
-                                       _stream(dev)))
-    return out[:1], out[1:]
+        norm, scale, (wp, wn, _keep) = _fresh(Gs[0], workspace, lib.rgc_grad_norm_batch_workspace_size(n, sizes),
+                                              torch.float32, (1,), torch.float32, (1,))
+        _check(lib.rgc_grad_norm_batch(n, types, pointers, sizes, max_norm, _pointer(grad_scale), norm.data_ptr(),
+                                       scale.data_ptr(), wp, wn, _stream(dev)))
+    return norm, scale
 
 
 def rgc_scale_batch(Gs, scale: torch.Tensor):

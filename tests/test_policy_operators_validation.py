@@ -122,12 +122,12 @@ def _arrays(d):
     (dict(n=-1), SHAPE), (dict(numels=(-1,)), SHAPE), (dict(n=(1 << 24) + 1), UNSUP), (dict(gts=(2,)), UNSUP),
     (dict(numels=((1 << 34) + 1,)), UNSUP), (dict(Gs=(None,)), NULL), (dict(Gs=None), NULL), (dict(gts=None), NULL),
     (dict(numels=None), NULL), (dict(Gs=(FAKE + 1,)), ALIGN), (dict(gts=(1,), Gs=(FAKE + 2,)), ALIGN),
-    (dict(max_norm=-1.0), VALUE), (dict(max_norm=float("nan")), VALUE), (dict(out=None), NULL), (dict(out=FAKE + 2), ALIGN),
-    (dict(scale=FAKE + 2), ALIGN), (dict(ws=None), WS), (dict(nb=7), WS), (dict(ws=FAKE + 64), ALIGN),
+    (dict(max_norm=-1.0), VALUE), (dict(max_norm=float("nan")), VALUE), (dict(norm=None), NULL), (dict(norm=FAKE + 2), ALIGN),
+    (dict(out=None), NULL), (dict(out=FAKE + 2), ALIGN), (dict(scale=FAKE + 2), ALIGN), (dict(ws=None), WS), (dict(nb=7), WS), (dict(ws=FAKE + 64), ALIGN),
 ])
 def test_grad_norm(lib, kw, want):
-    d = {**ARR, "max_norm": 1.0, "scale": None, "out": FAKE, "ws": FAKE, "nb": 1 << 20, **kw}
-    assert lib.rgc_grad_norm_batch(*_arrays(d), d["max_norm"], d["scale"], d["out"], d["ws"], d["nb"], None) == want
+    d = {**ARR, "max_norm": 1.0, "scale": None, "norm": FAKE, "out": FAKE, "ws": FAKE, "nb": 1 << 20, **kw}
+    assert lib.rgc_grad_norm_batch(*_arrays(d), d["max_norm"], d["scale"], d["norm"], d["out"], d["ws"], d["nb"], None) == want
 
 
 @pytest.mark.parametrize("kw,want", [
