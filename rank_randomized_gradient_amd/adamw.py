@@ -49,8 +49,8 @@ class AdamW:
         device, e.g. a clipping coefficient; one that is not finite leaves the
         parameters and moments as they are, though the step is counted). A step that is
         refused changes nothing. With max_norm the gradients, times grad_scale, are clipped to that
-        global norm as the step reads them (they stay as they are in memory), and their norm before clipping is
-        returned, a float32 on the device; a norm that is not finite is a grad_scale that is not."""
+        global norm as the step reads them (they stay as they are in memory; all on one device), and their norm before
+        clipping is returned, a float32 on the device; a norm that is not finite is a grad_scale that is not."""
         norm = None
         grads = [p.grad for p in self.params if p.grad is not None] if max_norm is not None else []
         if grads:

@@ -5,7 +5,9 @@
 // cost a call of torch.empty each otherwise.
 #include <ATen/ops/empty.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <algorithm>
 #include <cstdint>
@@ -121,41 +123,38 @@ PyObject* pack_gradients(PyObject*, PyObject* list) {
 // fresh(like, dtype, shape, dtype, shape, ...) -> tuple of new dense tensors on like's device, their contents
 // whatever the memory holds; shape: a tuple of integers, or None for None in the tensor's place
 PyObject* fresh(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS  // torch's own exceptions, out of memory among them, as torch.empty raises them
   if (n < 1 || n % 2 == 0 || !THPVariable_Check(args[0])) {
     PyErr_SetString(PyExc_TypeError, "a tensor, then pairs of a dtype and a shape are wanted");
     return nullptr;
   }
   const at::Device device = THPVariable_Unpack(args[0]).device();
-  PyObject* out = PyTuple_New(n / 2);
+  THPObjectPtr out(PyTuple_New(n / 2));
   if (!out) return nullptr;
   for (Py_ssize_t i = 0; i < n / 2; ++i) {
     PyObject *type = args[1 + 2 * i], *shape = args[2 + 2 * i];
-    PyObject* made = nullptr;
+    PyObject* made = Py_None;
     if (shape == Py_None) {
       Py_INCREF(Py_None);
-      made = Py_None;
-    } else if (!THPDtype_Check(type) || !PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) > 4) {
-      PyErr_SetString(PyExc_TypeError, "a dtype and a tuple of up to four integers are wanted");
     } else {
+      if (!THPDtype_Check(type) || !PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) > 4) {
+        PyErr_SetString(PyExc_TypeError, "a dtype and a tuple of up to four integers are wanted");
+        return nullptr;
+      }
       int64_t sizes[4];
       const Py_ssize_t dims = PyTuple_GET_SIZE(shape);
-      for (Py_ssize_t d = 0; d < dims && !PyErr_Occurred(); ++d) sizes[d] = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, d));
-      if (!PyErr_Occurred()) {
-        try {
-          made = THPVariable_Wrap(at::empty(at::IntArrayRef(sizes, dims),
-                                            at::TensorOptions().dtype(reinterpret_cast<THPDtype*>(type)->scalar_type).device(device)));
-        } catch (const std::exception& e) {  // e.g. out of memory
-          PyErr_SetString(PyExc_RuntimeError, e.what());
-        }
+      for (Py_ssize_t d = 0; d < dims; ++d) {
+        sizes[d] = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, d));
+        if (PyErr_Occurred()) return nullptr;
       }
+      made = THPVariable_Wrap(at::empty(at::IntArrayRef(sizes, dims),
+                                        at::TensorOptions().dtype(reinterpret_cast<THPDtype*>(type)->scalar_type).device(device)));
+      if (!made) return nullptr;
     }
-    if (!made) {
-      Py_DECREF(out);
-      return nullptr;
-    }
-    PyTuple_SET_ITEM(out, i, made);
+    PyTuple_SET_ITEM(out.get(), i, made);
   }
-  return out;
+  return out.release();
+  END_HANDLE_TH_ERRORS
 }
 
 struct Range {

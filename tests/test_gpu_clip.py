@@ -128,6 +128,13 @@ def test_squares_neither_overflow_nor_vanish(dev, size):
         _near(scale, 0.5 if n else 1.0)  # (bf16 has no 1e-44: zeros, and a max_norm of zero clips nothing of them)
 
 
+def test_tensors_of_nothing(dev):
+    empty = [torch.zeros(0, device=dev), torch.zeros(0, 5, dtype=BF, device=dev)]
+    norm, scale = rgc.rgc_grad_norm_batch(empty, 1.0)
+    assert float(norm) == 0 and float(scale) == 1
+    rgc.rgc_scale_batch(empty, scale)
+
+
 def test_many_chunks(dev):
     """More elements than the join has partial sums for at the smallest chunk, past 2^32 bytes."""
     n = (1 << 31) + 4099

@@ -202,7 +202,7 @@ def test_nan_and_infinity_stay_in_their_rows(dev, zt, V):
     assert torch.equal(top_ids.cpu()[keep], good["top_ids"][keep])
 
 
-@pytest.mark.parametrize("spread", [1e-3, 30.0, 1e30])
+@pytest.mark.parametrize("spread", [1e-3, 30.0, 300.0, 2000.0, 2e4, 1e30])
 def test_flat_peaked_and_extreme(dev, spread):
     _compare(dev, *_inputs(20, 5003, F32, 5, spread=spread, masked=0.0), 6, f"spread {spread}")
 

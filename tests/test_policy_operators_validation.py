@@ -201,3 +201,17 @@ def test_lists_of_gradients():
         assert pack(bad) is None
     with pytest.raises(TypeError):
         pack(3)
+
+
+def test_fresh_tensors():
+    fresh = rgc._lists().fresh
+    x = torch.zeros(3)
+    a, none, b, c = fresh(x, torch.bfloat16, (2, 5), torch.int64, None, torch.uint8, (0,), torch.float32, ())
+    assert a.dtype == torch.bfloat16 and a.shape == (2, 5) and none is None and b.shape == (0,) and c.dim() == 0
+    assert a.is_contiguous() and a.device == x.device and fresh(x) == ()
+    for bad in ((), (x, torch.float32), (3, torch.float32, (1,)), (x, 5, (1,)), (x, torch.float32, [1]),
+                (x, torch.float32, (1.5,)), (x, torch.float32, (1, 1, 1, 1, 1))):
+        with pytest.raises(TypeError):
+            fresh(*bad)
+    with pytest.raises(RuntimeError):
+        fresh(x, torch.float32, (-1,))
