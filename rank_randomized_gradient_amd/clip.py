@@ -8,7 +8,7 @@ from . import rgc
 
 @torch.no_grad()
 def clip_grad_norm(params, max_norm: float) -> torch.Tensor:
-    """Multiplies the parameters' gradients, in place, by min(1, max_norm / norm) and
+    """Multiplies the parameters' gradients (all on one device), in place, by min(1, max_norm / norm) and
     returns their norm (a scalar on the device; nothing waits for it). A norm that is not
     finite leaves the gradients as they are. Where AdamW takes the gradients
     next, its step(max_norm=...) clips them as it reads them instead."""
