@@ -1,5 +1,5 @@
-// Layer norm and root-mean-square norm, forward and backward with the weights'
-// gradients, for rows of up to 65536 elements in bf16 or fp32.
+// Layer norm and root-mean-square norm, of a tensor or of its sum with a residual, forward and backward
+// with the weights' gradients, for rows of up to 65536 elements in bf16 or fp32.
 //
 //   mu = mean(x) (0 for rms), rstd = 1 / sqrt(mean((x - mu)^2) + eps)
 //   xhat = (x - mu) rstd,     y = xhat w + b
@@ -29,6 +29,12 @@
 //   makes the column sums, another dx, reading each row twice (the second time
 //   from cache), both element by element: 4096 x 32768 bf16 in 503 us, 1.6 TB/s
 //   of x, dy and dx once. (Up to 16384: 8192 x 16384 in 185 us, 4.3 TB/s.)
+//
+// The residual norm (ADD) is the same kernels with one more operand: the forward
+// adds r to x, stores the sum and goes on with what it stored; the backward adds the sum's own gradient to
+// dx before the rounding. That gradient is loaded with x and dy: behind the row's sums
+// its loads' branches split the sums' code and 300 registers were spilled (8192 x 4096 rms 178 us,
+// 50 so). 8192 x 4096 bf16, rms: forward 43 us (6.2 TB/s of x, r, sum and y), backward 50 (5.3).
 //
 // Measured on MI355X, bf16, where a copy reaches 5.2 TB/s: forward of 32768 x
 // 4096 in 104 us (5.1 TB/s), backward in 170 (4.7); 4096 x 4096 in 15 and 32.
@@ -567,7 +573,8 @@ void backward_pick(const NormArgs& a, int64_t G, hipStream_t s) {
   if (a.n <= 512) return backward_launch<ADD, DB, XT, 1, 64, 1024>(a, G, s);
   if (a.n <= 1024) return backward_launch<ADD, DB, XT, 2, 64, 1024>(a, G, s);
   if constexpr (sizeof(XT) == 2) {  // up to 64 elements to a lane
-    if (a.n <= 2048) return backward_launch<ADD, DB, XT, 4, 64, 1024>(a, G, s);
+    // three rows' values and two rows' sums do not fit the 128 registers of 1024 threads: 16384 x 2048, layer, 79 us so, 53 on 512
+    if (a.n <= 2048) return backward_launch<ADD, DB, XT, 4, 64, ADD && DB ? 512 : 1024>(a, G, s);
     if (a.n <= 4096) return backward_launch<ADD, DB, XT, 8, 64, 512>(a, G, s);
     if (a.n <= 8192) return backward_launch<ADD, DB, XT, 8, 128, 512>(a, G, s);
     backward_launch<ADD, DB, XT, 8, 256, 512>(a, G, s);
@@ -644,7 +651,8 @@ rgc_status_t backward_impl(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt,
   a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
   a.ldx = ldx, a.ldr = ldds, a.lddy = lddy, a.ldo = lddx, a.rows = rows, a.n = n;
   a.w_f32 = wt == RGC_F32, a.centre = kind == RGC_NORM_LAYER, a.db = dbias != nullptr;
-  const int64_t G = backward_groups(rows, n, xt);
+  // (with the sum's gradient and db, bf16 rows of 1025 to 2048 go eight at a time, as fp32 ones)
+  const int64_t G = backward_groups(rows, n, dS && dbias && n > 1024 && n <= 2048 ? RGC_F32 : xt);
   if (dS) {
     if (xt == RGC_F32) dbias ? backward_pick<true, true, float>(a, G, s) : backward_pick<true, false, float>(a, G, s);
     else dbias ? backward_pick<true, true, uint16_t>(a, G, s) : backward_pick<true, false, uint16_t>(a, G, s);

@@ -1,9 +1,9 @@
 """The residual norm, rgc_add_norm_forward and _backward. The sum is one rounding of
 an fp32 sum: torch's bits. Y, mean and rstd are those of rgc_layer_norm_forward of the
-sum, bit for bit, and so are dweight, dbias and, without a gradient of the sum, dX. With one, dX is
-the norm's own dx in fp32 plus it, rounded once: rgc_layer_norm_backward's dX in fp32
-(its rows widened exactly) is that dx up to the order of its row sums (2^-17 of
-their magnitudes, as that call's own tests bound it), so both are compared with the formula in 64 bits.
+sum, bit for bit, and so are dX, dweight and dbias without a gradient of the sum. With one, dX is
+the norm's own dx in fp32 plus it, rounded once, and the column sums may be taken of other rows together:
+all three are compared with the formulas in 64 bits. Row sums are off by 2^-17 of their magnitudes, as
+rgc_layer_norm_backward's tests derive; a column's sum takes at most `rows` additions in sequence and 32 joining ones.
 """
 import pytest
 import torch
@@ -35,7 +35,8 @@ def _inputs(rows, n, xt, wt, seed):
 
 
 def _dx(s, dy, ds, w, kind):
-    """dX in 64 bits and its bound: what rgc_layer_norm_backward's tests derive, and one rounding of the whole."""
+    """dX, dweight and dbias in 64 bits with their bounds (the last two before their rounding): what
+    rgc_layer_norm_backward's tests derive, and one rounding of the whole of dX."""
     half = torch.finfo(s.dtype).eps / 2
     x, dy, ds = s.double(), dy.double(), ds.double()
     w = w.double() if w is not None else torch.ones(s.shape[1], dtype=torch.float64)
@@ -56,7 +57,10 @@ def _dx(s, dy, ds, w, kind):
     size = h.abs() + h.abs().mean(1, keepdim=True) + (xhat * along).abs()
     off = (dflat + dxhat * along.abs() + xhat.abs() * dalong + 2.0 ** -21 * size) * rstd + own.abs() * dvar / 2
     out = own + ds
-    return out, off + (half + 2.0 ** -23) * out.abs() + 2.0 ** -23 * own.abs()
+    steps = (len(s) + 32) * 2.0 ** -24
+    dw, db = (dy * xhat).sum(0), dy.sum(0)
+    columns = ((dw, (dy.abs() * dxhat).sum(0) + steps * (dy * xhat).abs().sum(0)), (db, steps * dy.abs().sum(0)))
+    return (out, off + (half + 2.0 ** -23) * out.abs() + 2.0 ** -23 * own.abs()), *columns
 
 
 def _check(got, want, bound, what):
@@ -83,9 +87,14 @@ def _run(dev, rows, n, xt, wt, kind, seed, weight=True, bias=True):
     assert all(_equal(p, q) for p, q in zip(got, want))
     dx, dw, db = rgc.rgc_add_norm_backward(dy, ds, s, w, mean, rstd, bias=bias, kind=kind)
     torch.cuda.synchronize()
-    assert _equal(dw, want[1]) and _equal(db, want[2])
-    ref, bound = _dx(s.cpu(), dy.cpu(), ds.cpu(), w.cpu() if weight else None, kind)
-    _check(dx, ref, bound, f"{rows}x{n} {xt} {wt} {kind}")
+    what = f"{rows}x{n} {xt} {wt} {kind}"
+    (ref, bound), *columns = _dx(s.cpu(), dy.cpu(), ds.cpu(), w.cpu() if weight else None, kind)
+    _check(dx, ref, bound, "dX " + what)
+    for got, plain, (ref, bound), name in zip((dw, db), want[1:], columns, ("dweight ", "dbias ")):
+        assert (got is None) == (plain is None)
+        if got is not None:
+            assert got.dtype == plain.dtype
+            _check(got, ref, bound + torch.finfo(got.dtype).eps / 2 * ref.abs(), name + what)
 
 
 WIDTHS = [1, 2, 7, 8, 64, 65, 128, 136, 257, 512, 520, 1000, 1003, 1024, 1032, 2048, 2056, 4095, 4096, 4097, 8192, 8200,
@@ -101,9 +110,10 @@ def test_every_width(dev, n):
 
 
 @pytest.mark.parametrize("rows", [1, 2, 255, 257, 5000])
-@pytest.mark.parametrize("n", [128, 1003, 4096])
+@pytest.mark.parametrize("n", [128, 1003, 1800, 4096])
 def test_row_counts(dev, rows, n):
     _run(dev, rows, n, BF, F32, "rms", rows, bias=False)
+    _run(dev, rows, n, BF, F32, "layer", rows)
 
 
 @pytest.mark.parametrize("xt", [BF, F32])
