@@ -290,6 +290,41 @@ def test_offsets_past_two_to_the_32(dev):
     assert torch.equal(zs, dz)
 
 
+@pytest.mark.parametrize("zt", [BF, F32])
+def test_far_rows_in_place(dev, zt):
+    """Rows with |lse| above 1024 between near ones, over several batches: one workgroup makes each, in place too."""
+    z, y, gl, ge = _inputs(6, 20003, zt, 21, ignored=0.0)
+    z[1] += 3000
+    z[2] = torch.finfo(zt).min
+    z[4] = torch.where(z[4] == -INF, z[4], z[4] * 500 - 5000)
+    y[1], y[4] = int(z[1].float().argmax()), int(z[4].float().argmax())
+    dz = _compare(dev, z, y, gl, ge, 3, f"far {zt}")[-1]
+    zg, yg, glg, geg = _to(dev, z, y, gl, ge)
+    _, entropy, lse, _, _ = rgc.rgc_log_prob_forward(zg, yg)
+    assert int((lse.abs() >= 1024).sum()) >= 2
+    rgc.rgc_log_prob_backward(zg, yg, lse, entropy, glg, geg, dZ=zg)
+    assert torch.equal(zg, dz)
+
+
+def test_more_rows_than_a_launch_has_workgroups(dev):
+    rows, V = (1 << 20) + 5, 9
+    z = torch.randn(rows, V, generator=torch.Generator(device=dev).manual_seed(1), device=dev)
+    y = torch.arange(rows, device=dev) % V
+    g = torch.ones(rows, device=dev)
+    logp, entropy, lse, top_logp, top_ids = rgc.rgc_log_prob_forward(z, y, 2)
+    dz = rgc.rgc_log_prob_backward(z, y, lse, entropy, g, g)
+    lp = torch.log_softmax(z.double(), 1)
+    h = -(lp.exp() * lp).sum(1)
+    best = torch.sort(z, dim=1, descending=True, stable=True)
+    want = -lp.exp() * (1 + lp + h[:, None])
+    want[torch.arange(rows, device=dev), y] += 1
+    # (u N + 2^-21) (1 + sum p (|d| + d^2)) with N = 100, |d| < 12 and the sums below 20; gradients of size up to 8
+    assert torch.equal(top_ids, best.indices[:, :2])
+    for got, ref in ((logp, lp.gather(1, y[:, None])[:, 0]), (entropy, h), (top_logp, lp.gather(1, top_ids))):
+        assert float((got.double() - ref).abs().max()) <= 2 * 20 * (100 * 2.0 ** -24 + 2.0 ** -21)
+    assert float((dz.double() - want).abs().max()) <= 8 * 2 * 20 * (100 * 2.0 ** -24 + 2.0 ** -21)
+
+
 def test_the_largest_vocabulary(dev):
     V = 1 << 24
     z = torch.randn(2, V, generator=torch.Generator(device=dev).manual_seed(1), device=dev)
