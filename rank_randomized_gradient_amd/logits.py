@@ -18,9 +18,11 @@ class LogProbFunction(torch.autograd.Function):
         z = _row_major(logits)
         t = tokens.reshape(-1).contiguous()
         logp, entropy, lse, _, _ = rgc.rgc_log_prob_forward(z, t)
+        # (tensors of their own and no views, which autograd lets nobody change in place)
+        logp.resize_(tokens.shape), entropy.resize_(tokens.shape)
         ctx.save_for_backward(z, t, lse, entropy)
         ctx.shape = logits.shape
-        return logp.reshape(tokens.shape), entropy.reshape(tokens.shape)
+        return logp, entropy
 
     @staticmethod
     @once_differentiable
@@ -29,7 +31,7 @@ class LogProbFunction(torch.autograd.Function):
         if dlogp is None and dentropy is None:
             return None, None
         flat = lambda g: None if g is None else g.reshape(-1).to(torch.float32).contiguous()  # noqa: E731
-        dz = rgc.rgc_log_prob_backward(z, t, lse, entropy, flat(dlogp), flat(dentropy))
+        dz = rgc.rgc_log_prob_backward(z, t, lse, flat(entropy), flat(dlogp), flat(dentropy))
         return dz.reshape(ctx.shape), None
 
 

@@ -60,10 +60,12 @@ class SketchedLogProbFunction(torch.autograd.Function):
             x2 = x2.contiguous()
         t = tokens.reshape(-1).contiguous()
         logp, entropy, lse, xp = rgc.rgc_linear_log_prob_forward(x2, weight, t, proj)
+        # (tensors of their own and no views, which autograd lets nobody change in place)
+        logp.resize_(tokens.shape), entropy.resize_(tokens.shape)
         ctx.save_for_backward(x2, weight, t, lse, entropy, xp)
         ctx.sketch = sketch
         ctx.in_shape = x.shape
-        return logp.reshape(tokens.shape), entropy.reshape(tokens.shape)
+        return logp, entropy
 
     @staticmethod
     @once_differentiable
@@ -72,7 +74,7 @@ class SketchedLogProbFunction(torch.autograd.Function):
         if dlogp is None and dentropy is None:
             return None, None, None, None, None, None
         flat = lambda g: None if g is None else g.reshape(-1).to(torch.float32).contiguous()  # noqa: E731
-        dx = rgc.rgc_linear_log_prob_backward(x2, weight, t, lse, entropy, flat(dlogp), flat(dentropy), xp, ctx.sketch,
+        dx = rgc.rgc_linear_log_prob_backward(x2, weight, t, lse, flat(entropy), flat(dlogp), flat(dentropy), xp, ctx.sketch,
                                               input_grad=ctx.needs_input_grad[0])
         return None if dx is None else dx.reshape(ctx.in_shape), None, None, None, None, None
 

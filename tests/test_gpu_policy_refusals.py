@@ -94,3 +94,26 @@ def test_a_module_under_no_grad(dev):
     with torch.no_grad():
         logp, entropy = head.log_prob(x, y)
     assert not logp.requires_grad and not entropy.requires_grad and bool((head.sketch == 0).all())
+
+
+@pytest.mark.parametrize("shape", [(6,), (2, 3)])
+@pytest.mark.parametrize("which", ["head", "logits"])
+def test_outputs_changed_in_place(dev, which, shape):
+    """The log probabilities may be changed in place, with the gradient of what they became; the entropies, which the
+    backward reads, are found changed by autograd."""
+    x, y = synth.normal_bf16((*shape, 64), 1.0, seed=1).to(dev), torch.arange(6, device=dev).reshape(shape)
+    head = SketchedCrossEntropy(64, 104, 16, device=dev)
+    head.begin_update(1)
+    call = head.log_prob if which == "head" else log_prob
+    grads = []
+    for change in (lambda t: t.mul_(3.0), lambda t: t * 3.0):
+        leaf = x.clone().requires_grad_()
+        logp, entropy = call(leaf, y)
+        assert logp.shape == entropy.shape == shape
+        (change(logp).sum() + entropy.sum()).backward()
+        grads.append(leaf.grad)
+    assert torch.equal(*grads)
+    leaf = x.clone().requires_grad_()
+    logp, entropy = call(leaf, y)
+    with pytest.raises(RuntimeError, match="in-?place"):
+        entropy.mul_(2.0).sum().backward()
