@@ -534,21 +534,27 @@ void forward_pick(const NormArgs& a, hipStream_t s) {
   else forward_launch<ADD, XT, 8, 1024, 1024>(a, s);
 }
 
-// Rows a workgroup of the backward holds at a time (as backward_pick).
-int backward_rows(int64_t n, rgc_dtype_t xt) {
+// Whether a residual norm's backward of this width runs two workgroups of 512 threads to a
+// compute unit, one's sums at the end under the other's rows (5000 x 1003 fp32: 24.4 us with one of 1024, 22.3 so).
+bool backward_pairs(int64_t n, bool add) { return add && n > 128 && n <= 1024; }
+
+// Rows a workgroup of the backward holds at a time (as backward_pick). add, db: as its template's.
+int backward_rows(int64_t n, rgc_dtype_t xt, bool add, bool db) {
   const bool f32 = xt == RGC_F32;
-  if (n <= 1024) return n <= 128 ? 64 : 16;
-  return (n <= 2048 ? 16 : n <= 4096 ? 8 : n <= 8192 ? 4 : 2) / (f32 ? 2 : 1);
+  if (n <= 128) return 64;
+  if (n <= 1024) return backward_pairs(n, add) ? 8 : 16;
+  if (n <= 2048) return f32 || (add && db) ? 8 : 16;
+  return (n <= 4096 ? 8 : n <= 8192 ? 4 : 2) / (f32 ? 2 : 1);
 }
 
-// Workgroups of the backward, and so partial rows: one per compute unit, or
+// Workgroups of the backward, and so partial rows: one per compute unit (or two), or
 // fewer where the rows do not fill them.
-int64_t backward_groups(int64_t rows, int64_t n, rgc_dtype_t xt) {
-  const int64_t cus = device_compute_units();
+int64_t backward_groups(int64_t rows, int64_t n, rgc_dtype_t xt, bool add, bool db) {
+  const int64_t most = device_compute_units() * (backward_pairs(n, add) ? 2 : 1);
   if (n > kNormHeldBackward) return rows < 64 ? rows : 64;
-  const int64_t per = backward_rows(n, xt);
+  const int64_t per = backward_rows(n, xt, add, db);
   const int64_t need = (rows + per - 1) / per;
-  return need < cus ? need : cus;
+  return need < most ? need : most;
 }
 
 template <bool ADD, bool DB, typename XT, int NV, int TPR, int THREADS>
@@ -570,8 +576,8 @@ void backward_pick(const NormArgs& a, int64_t G, hipStream_t s) {
     return;
   }
   if (a.n <= 128) return backward_launch<ADD, DB, XT, 1, 16, 1024>(a, G, s);
-  if (a.n <= 512) return backward_launch<ADD, DB, XT, 1, 64, 1024>(a, G, s);
-  if (a.n <= 1024) return backward_launch<ADD, DB, XT, 2, 64, 1024>(a, G, s);
+  if (a.n <= 512) return backward_launch<ADD, DB, XT, 1, 64, ADD ? 512 : 1024>(a, G, s);
+  if (a.n <= 1024) return backward_launch<ADD, DB, XT, 2, 64, ADD ? 512 : 1024>(a, G, s);
   if constexpr (sizeof(XT) == 2) {  // up to 64 elements to a lane
     // three rows' values and two rows' sums do not fit the 128 registers of 1024 threads: 16384 x 2048, layer, 79 us so, 53 on 512
     if (a.n <= 2048) return backward_launch<ADD, DB, XT, 4, 64, ADD && DB ? 512 : 1024>(a, G, s);
@@ -616,9 +622,9 @@ rgc_status_t forward_impl(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, 
 }
 
 // The partial rows of whichever type X will have.
-size_t backward_workspace(int64_t rows, int64_t n) {
+size_t backward_workspace(int64_t rows, int64_t n, bool add) {
   if (rows <= 0 || n <= 0 || rows > kNormMaxRows || n > kNormMaxWidth) return 0;
-  const int64_t a = backward_groups(rows, n, RGC_BF16), b = backward_groups(rows, n, RGC_F32);
+  const int64_t a = backward_groups(rows, n, RGC_BF16, add, true), b = backward_groups(rows, n, RGC_F32, add, true);
   return (size_t)(a > b ? a : b) * 2 * (size_t)n * 4;
 }
 
@@ -644,15 +650,14 @@ rgc_status_t backward_impl(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt,
   if (dS && (st = check_rows(dS, ldds, n, xt)) != RGC_OK) return st;
   if (!rstd || (kind == RGC_NORM_LAYER && !mean)) return RGC_ERR_NULL;
   if (!aligned_to(weight, elem(wt)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4)) return RGC_ERR_ALIGN;
-  if (!ws || ws_bytes < backward_workspace(rows, n)) return RGC_ERR_WORKSPACE;
+  if (!ws || ws_bytes < backward_workspace(rows, n, dS != nullptr)) return RGC_ERR_WORKSPACE;
   if (!aligned_to(ws, 256)) return RGC_ERR_ALIGN;
   NormArgs a{};
   a.x = X, a.r = dS, a.dy = dY, a.w = weight, a.out = dX, a.part = static_cast<float*>(ws);
   a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
   a.ldx = ldx, a.ldr = ldds, a.lddy = lddy, a.ldo = lddx, a.rows = rows, a.n = n;
   a.w_f32 = wt == RGC_F32, a.centre = kind == RGC_NORM_LAYER, a.db = dbias != nullptr;
-  // (with the sum's gradient and db, bf16 rows of 1025 to 2048 go eight at a time, as fp32 ones)
-  const int64_t G = backward_groups(rows, n, dS && dbias && n > 1024 && n <= 2048 ? RGC_F32 : xt);
+  const int64_t G = backward_groups(rows, n, xt, dS != nullptr, dbias != nullptr);
   if (dS) {
     if (xt == RGC_F32) dbias ? backward_pick<true, true, float>(a, G, s) : backward_pick<true, false, float>(a, G, s);
     else dbias ? backward_pick<true, true, uint16_t>(a, G, s) : backward_pick<true, false, uint16_t>(a, G, s);
@@ -678,7 +683,7 @@ extern "C" rgc_status_t rgc_layer_norm_forward(rgc_norm_kind_t kind, rgc_dtype_t
                       stream);
 }
 
-extern "C" size_t rgc_layer_norm_backward_workspace_size(int64_t rows, int64_t n) { return backward_workspace(rows, n); }
+extern "C" size_t rgc_layer_norm_backward_workspace_size(int64_t rows, int64_t n) { return backward_workspace(rows, n, false); }
 
 extern "C" rgc_status_t rgc_layer_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* dY,
                                                 int64_t lddy, const void* X, int64_t ldx, const void* weight,
@@ -696,7 +701,7 @@ extern "C" rgc_status_t rgc_add_norm_forward(rgc_norm_kind_t kind, rgc_dtype_t x
   return forward_impl(kind, xt, wt, X, ldx, R, ldr, weight, bias, eps, S, lds, Y, ldy, mean, rstd, rows, n, true, stream);
 }
 
-extern "C" size_t rgc_add_norm_backward_workspace_size(int64_t rows, int64_t n) { return backward_workspace(rows, n); }
+extern "C" size_t rgc_add_norm_backward_workspace_size(int64_t rows, int64_t n) { return backward_workspace(rows, n, true); }
 
 extern "C" rgc_status_t rgc_add_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dtype_t wt, const void* dY,
                                               int64_t lddy, const void* dS, int64_t ldds, const void* S, int64_t lds,
