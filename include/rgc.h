@@ -539,7 +539,8 @@ rgc_status_t rgc_log_prob_backward(rgc_dtype_t zt, const void* Z, int64_t ldz, c
  * Gs, gts, numels: HOST arrays of n entries (at most 2^24): tensor i has numels[i] (at most 2^34)
  * contiguous elements of type gts[i], aligned to its elements. norm, scale: a float each.
  * max_norm may be infinite (the norm alone); RGC_ERR_VALUE if it is negative or NaN.
- * In rgc_scale_batch no two tensors share memory. */
+ * In rgc_scale_batch no two tensors share memory, and *scale lies in none of them (the binding
+ * refuses it). */
 size_t rgc_grad_norm_batch_workspace_size(int64_t n, const int64_t* numels);
 rgc_status_t rgc_grad_norm_batch(int64_t n, const rgc_dtype_t* gts, const void* const* Gs, const int64_t* numels,
                                  double max_norm, const float* grad_scale, float* norm, float* scale, void* ws,

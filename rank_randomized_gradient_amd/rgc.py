@@ -42,6 +42,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -1170,7 +1171,7 @@ def rgc_grad_norm_batch(Gs, max_norm: float = float("inf"), grad_scale: torch.Te
 
 
 def rgc_scale_batch(Gs, scale: torch.Tensor):
-    """Gs times scale (a device float32), in place; a scale that is 1 or not finite
+    """Gs times scale (a device float32 that lies in none of them), in place; a scale that is 1 or not finite
     changes nothing. Returns Gs."""
     lib = load_library()
     if len(Gs) == 0:
@@ -1178,8 +1179,9 @@ def rgc_scale_batch(Gs, scale: torch.Tensor):
     n, types, pointers, sizes, dev, ranges = _gradient_list(Gs)
     _need_gpu(Gs[0], scale)
     _one_float(scale, "scale")
-    if not _lists().disjoint((b"", b"", 1), ranges):
-        raise RgcError("a tensor is listed twice, or shares memory with another")
+    # (every workgroup reads the scale for itself, some after others have written)
+    if not _lists().disjoint((struct.pack("Q", scale.data_ptr()), struct.pack("q", 4), 1), ranges):
+        raise RgcError("a tensor is listed twice, or shares memory with another or with the scale")
     with _on(dev):
         _check(lib.rgc_scale_batch(n, types, pointers, sizes, scale.data_ptr(), _stream(dev)))
     return Gs
