@@ -579,8 +579,8 @@ rgc_status_t rgc_scale_batch(int64_t n, const rgc_dtype_t* gts, void* const* Gs,
  * Arrays are HOST arrays of n entries, n without limit (48 tensors a launch);
  * parameters, gradients and moments 16-byte aligned, at most 2^34 elements. A
  * tensor may be listed once only, and what is written (parameters, moments,
- * scales) shares no memory with any other tensor of the call (the binding refuses
- * it). RGC_ERR_VALUE: step < 1, a beta outside [0, 1) (as fp32: one just below 1
+ * scales) shares no memory with any other tensor of the call, *grad_scale among them
+ * (the binding refuses it). RGC_ERR_VALUE: step < 1, a beta outside [0, 1) (as fp32: one just below 1
  * rounds to it), eps below 2^-126 (as fp32), lr, lr weight_decay or
  * lr/(1 - beta1^step) above 1e30, or a scalar that is not finite. */
 typedef enum {

@@ -1230,14 +1230,15 @@ def _adamw_call(Ps, Gs, Ms, Vs, lr, step, seed, beta1, beta2, eps, weight_decay,
     if any(x[3] != dev.index for x in given):
         raise RgcError("all tensors must be on the same device")
     spans = [(x[0], x[1], _ITEM_BYTES[x[2]]) for x in given]
-    if not _lists().disjoint(spans[1], spans[0], *spans[2:]):
+    read = spans[1]
+    if grad_scale is not None:
+        _one_float(grad_scale, "grad_scale")
+        # (read by every workgroup, as the gradients are; in units of their elements)
+        read = (read[0] + struct.pack("Q", grad_scale.data_ptr()), read[1] + struct.pack("q", 4 // read[2]), read[2])
+    if not _lists().disjoint(read, spans[0], *spans[2:]):
         raise RgcError("a tensor is listed twice, or shares memory with another that the step writes")
     pp, gp, mp, vp, *scales = [(_vp * n).from_buffer_copy(x[0]) for x in given]
     msp, vsp = scales if eight else (None, None)
-    if grad_scale is not None:
-        _dense(grad_scale, torch.float32, "grad_scale")
-        if grad_scale.numel() != 1:
-            raise RgcError("grad_scale must be one float32")
     counts = (_i64 * n).from_buffer_copy(sizes)
 
     def call(flags: int = 0) -> None:
