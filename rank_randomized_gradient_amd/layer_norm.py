@@ -27,7 +27,7 @@ class LayerNormFunction(torch.autograd.Function):
         ctx.kind = kind
         ctx.bias_dtype = None if bias is None else bias.dtype
         ctx.shape = x.shape
-        return y.reshape(x.shape)
+        return y.resize_(x.shape)  # (a tensor of its own and no view, which autograd lets nobody change in place)
 
     @staticmethod
     @once_differentiable
@@ -40,28 +40,29 @@ class LayerNormFunction(torch.autograd.Function):
 
 
 class AddNormFunction(torch.autograd.Function):
-    """(norm of x + residual, x + residual); saves the sum and each row's mean and rstd."""
+    """(norm of x + residual, x + residual); saves the sum and each row's mean and rstd. Both outputs may be
+    changed in place, the sum where no gradient of the norm follows (autograd finds it changed)."""
 
     @staticmethod
     def forward(ctx, x, residual, weight, bias, eps, kind):
         ctx.set_materialize_grads(False)
         s, y, mean, rstd = rgc.rgc_add_norm_forward(_row_major(x), _row_major(residual), weight, bias, eps=eps, kind=kind)
+        y.resize_(x.shape), s.resize_(x.shape)  # (no views here either)
         ctx.save_for_backward(s, weight, mean, rstd)
         ctx.kind = kind
         ctx.bias_dtype = None if bias is None else bias.dtype
-        ctx.shape = x.shape
-        return y.reshape(x.shape), s.reshape(x.shape)
+        return y, s
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dsum):
-        s, weight, mean, rstd = ctx.saved_tensors
         if dy is None:  # the sum alone was used
             return dsum, dsum, None, None, None, None
+        s, weight, mean, rstd = ctx.saved_tensors
         rows = lambda g: None if g is None else _row_major(g if g.dtype == s.dtype else g.to(s.dtype))  # noqa: E731
-        dx, dw, db = rgc.rgc_add_norm_backward(rows(dy), rows(dsum), s, weight, mean, rstd, bias=ctx.bias_dtype is not None,
-                                               kind=ctx.kind)
-        dx = dx.reshape(ctx.shape)
+        dx, dw, db = rgc.rgc_add_norm_backward(rows(dy), rows(dsum), rows(s), weight, mean, rstd,
+                                               bias=ctx.bias_dtype is not None, kind=ctx.kind)
+        dx = dx.reshape(s.shape)
         return dx, dx, dw if weight is not None else None, None if db is None else db.to(ctx.bias_dtype), None, None
 
 

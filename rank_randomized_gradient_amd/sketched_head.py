@@ -36,7 +36,7 @@ class SketchedCrossEntropyFunction(torch.autograd.Function):
         ctx.save_for_backward(x2, weight, t, lse, xp)
         ctx.sketch = sketch
         ctx.in_shape = x.shape
-        return loss.reshape(targets.shape)
+        return loss.resize_(targets.shape)  # (a tensor of its own and no view, which autograd lets nobody change in place)
 
     @staticmethod
     @once_differentiable

@@ -40,7 +40,8 @@ class SketchedLinearFunction(torch.autograd.Function):
         ctx.sketch = sketch
         ctx.workspace = workspace
         ctx.in_shape = x.shape
-        return y.reshape(*x.shape[:-1], weight.shape[0])
+        # (a tensor of its own and no view, which autograd lets nobody change in place)
+        return y.resize_(*x.shape[:-1], weight.shape[0])
 
     @staticmethod
     def backward(ctx, dy):
