@@ -92,26 +92,33 @@ class SketchedCrossEntropy(SketchedLinear):
 
     log_prob(x, tokens) gives (log probabilities, entropies) instead, for a policy's
     loss: its backward takes the gradients of both and adds to `sketch` likewise.
+    Losses and log probabilities need no projection under torch.no_grad(): begin_update may come later, or never.
     alternatives(x, top) gives each row's `top` most likely entries.
     """
 
-    def forward(self, x: torch.Tensor, targets: torch.Tensor) -> torch.Tensor:
+    def _projection(self) -> torch.Tensor | None:
+        """What X is projected with for the backward; none where no gradient is recorded."""
+        if not torch.is_grad_enabled():
+            return None
         if self.proj_seed is None:
             raise rgc.RgcError("begin_update(seed) must draw the projection before the first forward")
+        return self.proj
+
+    def forward(self, x: torch.Tensor, targets: torch.Tensor) -> torch.Tensor:
+        proj = self._projection()
         if targets.dtype != torch.int64 or targets.shape != x.shape[:-1]:
             raise rgc.RgcError("targets must be int64, one for each row of x")
         anchor = torch.zeros((), device="cpu", requires_grad=True)
-        return SketchedCrossEntropyFunction.apply(x, self.weight, targets, self.proj, self.sketch, anchor)
+        return SketchedCrossEntropyFunction.apply(x, self.weight, targets, proj, self.sketch, anchor)
 
     def log_prob(self, x: torch.Tensor, tokens: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
         """(log probability of each token, entropy of its distribution), float32; both 0 for a token outside
         0 .. vocabulary - 1."""
-        if self.proj_seed is None:
-            raise rgc.RgcError("begin_update(seed) must draw the projection before the first forward")
+        proj = self._projection()
         if tokens.dtype != torch.int64 or tokens.shape != x.shape[:-1]:
             raise rgc.RgcError("tokens must be int64, one for each row of x")
         anchor = torch.zeros((), device="cpu", requires_grad=True)
-        return SketchedLogProbFunction.apply(x, self.weight, tokens, self.proj, self.sketch, anchor)
+        return SketchedLogProbFunction.apply(x, self.weight, tokens, proj, self.sketch, anchor)
 
     @torch.no_grad()
     def alternatives(self, x: torch.Tensor, top: int) -> tuple[torch.Tensor, torch.Tensor]:
