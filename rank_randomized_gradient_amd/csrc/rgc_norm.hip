@@ -35,6 +35,11 @@
 // dx before the rounding. That gradient is loaded with x and dy: behind the row's sums
 // its loads' branches split the sums' code and 300 registers were spilled (8192 x 4096 rms 178 us,
 // 50 so). 8192 x 4096 bf16, rms: forward 43 us (6.2 TB/s of x, r, sum and y), backward 50 (5.3).
+// A thread of the widest rows holds eight vectors of x and four of r at a time, and the row's last elements, where they
+// are no whole vector, in one thread: with all eight of r, and every vector's code for a ragged end, up to 278
+// registers were spilled and the addition apart from the norm was faster (rms, with all / so / apart:
+// 2048 x 40003 bf16 283, 195, 210 us; 2048 x 20000 fp32 235, 168, 196; 1024 x 40003 fp32 326, 179, 196;
+// 4096 x 32768 bf16 217, 210, 254). In fp32 up to 64 are still spilled; the plain norm's 46.
 //
 // Measured on MI355X, bf16, where a copy reaches 5.2 TB/s: forward of 32768 x
 // 4096 in 104 us (5.1 TB/s), backward in 170 (4.7); 4096 x 4096 in 15 and 32.
@@ -237,24 +242,52 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
   __shared__ float slots[2][THREADS / 64];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, n = (int)a.n;
   const float inv_n = 1.0f / (float)n;
+  // the last elements of a wide row, no whole vector, are one thread's and apart from the others
+  constexpr bool TAIL = ADD && RAGGED && NV > 4;
+  const int end = n / 8 * 8;
+  const bool mine = n / 8 % TPR == t;
   for (int64_t row0 = (int64_t)blockIdx.x * GROUPS; row0 < a.rows; row0 += (int64_t)gridDim.x * GROUPS) {
     const int64_t row = row0 + grp;
     const bool live = row < a.rows;
     const XT* x = static_cast<const XT*>(a.x) + (live ? row : row0) * a.ldx;
     Raw<XT> raw[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_at<RAGGED>(raw[j], x, (j * TPR + t) * 8, n);
+    for (int j = 0; j < NV; ++j) load_at<RAGGED && !TAIL>(raw[j], x, (j * TPR + t) * 8, n);
+    Raw<XT> last;
+    if constexpr (TAIL) {
+      last.zero();
+      if (mine) last.load_some(x + end, n - end);
+    }
     if constexpr (ADD) {
       const XT* r = static_cast<const XT*>(a.r) + (live ? row : row0) * a.ldr;
       XT* sum = static_cast<XT*>(a.sum) + row * a.lds;
-      Raw<XT> other[NV];
+      constexpr int AT = NV < 4 ? NV : 4;  // of r's vectors at a time
 #pragma unroll
-      for (int j = 0; j < NV; ++j) load_at<RAGGED>(other[j], r, (j * TPR + t) * 8, n);
+      for (int j0 = 0; j0 < NV; j0 += AT) {
+        Raw<XT> other[AT];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        raw[j].add(other[j]);
-        if (live) raw[j].template keep<RAGGED>(sum, (j * TPR + t) * 8, n);
+        for (int j = 0; j < AT; ++j) load_at<RAGGED && !TAIL>(other[j], r, ((j0 + j) * TPR + t) * 8, n);
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+          raw[j0 + j].add(other[j]);
+          if (live) raw[j0 + j].template keep<RAGGED && !TAIL>(sum, ((j0 + j) * TPR + t) * 8, n);
+        }
+        if constexpr (AT < NV) __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (TAIL) {
+        if (mine) {
+          Raw<XT> other;
+          other.zero();
+          other.load_some(r + end, n - end);
+          last.add(other);
+          if (live) last.template keep<true>(sum, end, n);
+        }
+      }
+    }
+    if constexpr (TAIL) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if ((j * TPR + t) * 8 == end) raw[j] = last;
     }
     float mu = 0.f;
     if (a.centre) {
@@ -287,22 +320,38 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TPR + t) * 8;
-      if (c >= n || !live) continue;
+      if (c + (TAIL ? 7 : 0) >= n || !live) continue;
       raw[j].again();
       float f[8], p[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = (raw[j].get(e) - mu) * rstd;
       if (a.w) {
-        load_params<RAGGED>(a.w, a.w_f32, c, n, p);
+        load_params<RAGGED && !TAIL>(a.w, a.w_f32, c, n, p);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = f[e] * p[e];
       }
       if (a.b) {
-        load_params<RAGGED>(a.b, a.w_f32, c, n, p);
+        load_params<RAGGED && !TAIL>(a.b, a.w_f32, c, n, p);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = f[e] + p[e];
       }
-      store_at<RAGGED>(y, c, n, f);
+      store_at<RAGGED && !TAIL>(y, c, n, f);
+    }
+    if constexpr (TAIL) {
+      if (mine && live) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if ((j * TPR + t) * 8 == end) last = raw[j];
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 7; ++e) {
+          if (end + e >= n) continue;
+          f[e] = (last.get(e) - mu) * rstd;
+          if (a.w) f[e] = f[e] * load_param(a.w, a.w_f32, end + e);
+          if (a.b) f[e] = f[e] + load_param(a.b, a.w_f32, end + e);
+        }
+        Raw<XT>::store_some(y + end, f, n - end);
+      }
     }
     if constexpr (TPR > 64) __syncthreads();  // before the next rows' sums reuse the slots
   }
