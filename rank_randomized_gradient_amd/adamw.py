@@ -7,7 +7,6 @@ from __future__ import annotations
 import torch
 
 from . import rgc
-from .clip import no_norm
 
 
 class AdamW:
@@ -51,16 +50,12 @@ class AdamW:
         parameters and moments as they are, though the step is counted). A step that is
         refused changes nothing. With max_norm the gradients, times grad_scale, are clipped to that
         global norm as the step reads them (they stay as they are in memory; all on one device), and their norm before
-        clipping is returned, a float32 on the device (zero where there are none); a norm that is not finite (in 64 bits)
-        is a grad_scale that is not."""
+        clipping is returned, a float32 on the device (None where no parameter has a gradient); a norm that is not finite
+        (in 64 bits) is a grad_scale that is not."""
         norm = None
-        if max_norm is not None:
-            grads = [p.grad for p in self.params if p.grad is not None]
-            if grads:
-                norms, grad_scale = rgc.rgc_grad_norm_batch(grads, max_norm, grad_scale)
-                norm = norms[0]
-            else:
-                norm = no_norm(self.params)
+        grads = [p.grad for p in self.params if p.grad is not None] if max_norm is not None else []
+        if grads:
+            norm, grad_scale = rgc.rgc_grad_norm_batch(grads, max_norm, grad_scale)
         groups: dict = {}  # one call for each pair of types, device and step count
         for i, p in enumerate(self.params):
             if p.grad is None:
@@ -86,7 +81,7 @@ class AdamW:
             for i in at:
                 self.state[i]["step"] = t
         self.steps += 1
-        return norm
+        return None if norm is None else norm[0]
 
     def zero_grad(self, set_to_none: bool = True) -> None:
         for p in self.params:

@@ -6,11 +6,6 @@ import torch
 from . import rgc
 
 
-def no_norm(params: list) -> torch.Tensor:
-    """The norm of no gradients: zero, where the parameters are."""
-    return torch.zeros((), dtype=torch.float32, device=params[0].device if params else None)
-
-
 @torch.no_grad()
 def clip_grad_norm(params, max_norm: float) -> torch.Tensor:
     """Multiplies the parameters' gradients (all on one device), in place, by min(1, max_norm / norm) and
@@ -24,7 +19,7 @@ def clip_grad_norm(params, max_norm: float) -> torch.Tensor:
             seen.add(id(p))
             grads.append(p.grad)
     if not grads:
-        return no_norm(params)
+        return torch.zeros((), dtype=torch.float32, device=params[0].device if params else None)
     norm, scale = rgc.rgc_grad_norm_batch(grads, max_norm)
     rgc.rgc_scale_batch(grads, scale)
     return norm[0]
