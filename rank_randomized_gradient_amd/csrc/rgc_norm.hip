@@ -583,15 +583,21 @@ void forward_pick(const NormArgs& a, hipStream_t s) {
   else forward_launch<ADD, XT, 8, 1024, 1024>(a, s);
 }
 
-// Whether a residual norm's backward of this width runs two workgroups of 512 threads to a
-// compute unit, one's sums at the end under the other's rows (5000 x 1003 fp32: 24.4 us with one of 1024, 22.3 so).
-bool backward_pairs(int64_t n, bool add) { return add && n > 128 && n <= 1024; }
+// Whether a residual norm's backward runs two workgroups of 512 threads to a compute unit, one's sums at the
+// end under the other's rows, in the place of one of 1024: fp32 rows of 513 to 1024 where there are more than one
+// workgroup to each compute unit holds. rms, two against one: 5000 x 768 19.3 and 20.1 us, 5000 x 1003 27.0 and 28.2, 5000 x
+// 1024 22.6 and 24.8, 65536 x 1024 207 and 215 (8192 x 768, two whole rounds of rows, 24.5 and 23.7). Fewer rows only have more partial
+// rows to add (2500 x 1003 16.0 and 14.7), and in bf16 and narrower rows there is less to hide: 2500 x 1003
+// bf16 14.1 and 12.5, 8192 x 512 bf16 11.7 and 10.7, 20000 x 512 20.3 and 18.9.
+bool backward_pairs(int64_t rows, int64_t n, rgc_dtype_t xt, bool add) {
+  return add && xt == RGC_F32 && n > 512 && n <= 1024 && rows > 16 * (int64_t)device_compute_units();
+}
 
 // Rows a workgroup of the backward holds at a time (as backward_pick). add, db: as its template's.
-int backward_rows(int64_t n, rgc_dtype_t xt, bool add, bool db) {
+int backward_rows(int64_t rows, int64_t n, rgc_dtype_t xt, bool add, bool db) {
   const bool f32 = xt == RGC_F32;
   if (n <= 128) return 64;
-  if (n <= 1024) return backward_pairs(n, add) ? 8 : 16;
+  if (n <= 1024) return backward_pairs(rows, n, xt, add) ? 8 : 16;
   if (n <= 2048) return f32 || (add && db) ? 8 : 16;
   return (n <= 4096 ? 8 : n <= 8192 ? 4 : 2) / (f32 ? 2 : 1);
 }
@@ -599,9 +605,9 @@ int backward_rows(int64_t n, rgc_dtype_t xt, bool add, bool db) {
 // Workgroups of the backward, and so partial rows: one per compute unit (or two), or
 // fewer where the rows do not fill them.
 int64_t backward_groups(int64_t rows, int64_t n, rgc_dtype_t xt, bool add, bool db) {
-  const int64_t most = device_compute_units() * (backward_pairs(n, add) ? 2 : 1);
+  const int64_t most = device_compute_units() * (backward_pairs(rows, n, xt, add) ? 2 : 1);
   if (n > kNormHeldBackward) return rows < 64 ? rows : 64;
-  const int64_t per = backward_rows(n, xt, add, db);
+  const int64_t per = backward_rows(rows, n, xt, add, db);
   const int64_t need = (rows + per - 1) / per;
   return need < most ? need : most;
 }
@@ -625,10 +631,14 @@ void backward_pick(const NormArgs& a, int64_t G, hipStream_t s) {
     return;
   }
   if (a.n <= 128) return backward_launch<ADD, DB, XT, 1, 16, 1024>(a, G, s);
-  if (a.n <= 512) return backward_launch<ADD, DB, XT, 1, 64, ADD ? 512 : 1024>(a, G, s);
-  if (a.n <= 1024) return backward_launch<ADD, DB, XT, 2, 64, ADD ? 512 : 1024>(a, G, s);
+  if (a.n <= 512) return backward_launch<ADD, DB, XT, 1, 64, 1024>(a, G, s);
+  if constexpr (ADD && sizeof(XT) == 4) {
+    if (backward_pairs(a.rows, a.n, RGC_F32, true)) return backward_launch<ADD, DB, XT, 2, 64, 512>(a, G, s);
+  }
+  if (a.n <= 1024) return backward_launch<ADD, DB, XT, 2, 64, 1024>(a, G, s);
   if constexpr (sizeof(XT) == 2) {  // up to 64 elements to a lane
-    // three rows' values and two rows' sums do not fit the 128 registers of 1024 threads: 16384 x 2048, layer, 79 us so, 53 on 512
+    // three rows' values and two rows' sums do not fit the 128 registers of 1024 threads (layer, on 512 and on 1024: 1000 x 1032
+    // 12.6 and 17.0 us, 5000 x 1536 20.9 and 31.0, 20000 x 1032 39.5 and 66.7, 20000 x 2048 69 and 92)
     if (a.n <= 2048) return backward_launch<ADD, DB, XT, 4, 64, ADD && DB ? 512 : 1024>(a, G, s);
     if (a.n <= 4096) return backward_launch<ADD, DB, XT, 8, 64, 512>(a, G, s);
     if (a.n <= 8192) return backward_launch<ADD, DB, XT, 8, 128, 512>(a, G, s);
