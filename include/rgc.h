@@ -513,7 +513,8 @@ rgc_status_t rgc_add_norm_backward(rgc_norm_kind_t kind, rgc_dtype_t xt, rgc_dty
  * Backward, from grad_logp and grad_entropy (either may be NULL: zeros) and the
  * forward's lse and entropy (entropy may be NULL without grad_entropy):
  *   dz_v = grad_logp ([v = token] - p_v) - grad_entropy p_v (z_v - lse + entropy),
- * a row of zeros for a token that takes no part and for a row of -inf.
+ * a row of zeros for a token that takes no part and for a row of -inf. (An entry of -inf has p = 0:
+ * its gradient is 0, or grad_logp where it is the token.)
  * Z, dZ: rows x V of type zt, row strides at least V (at most 2^31), aligned to
  * their elements; dZ may be Z, with the same row stride. logp, entropy, lse,
  * top_logp, grads: float; tokens, top_ids: int64. Sums in fp32, in a fixed order.

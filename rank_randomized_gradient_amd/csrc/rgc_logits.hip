@@ -6,8 +6,9 @@
 //   dz_v = p_v (-gl - ge (z_v - lse + H)) + gl [v = y],  p = exp(z - lse)
 //
 // Entries of -inf have no probability: they add nothing to s and q and get no
-// gradient. A row of nothing else has lse = -inf, a log probability of -inf, an
-// entropy of 0 and no gradient. NaN and +inf make their row NaN.
+// gradient but the token's own gl, which it gets whatever its logit. A row of nothing
+// else has lse = -inf, a log probability of -inf, an entropy of 0 and no gradient at all.
+// NaN and +inf make their row NaN.
 //
 // Both directions are bound by memory: the forward reads a row once, the
 // backward reads and writes it once. MI355X, 4096 x 131072 bf16: forward 201 us (5.3 TB/s;
@@ -16,7 +17,7 @@
 //
 // The backward's z - lse loses log s where lse is large (a row of the type's
 // lowest value throughout: its probabilities would be 1 each). From |lse| = 1024 on, where
-// half a step of lse is 2^-15, it makes m and log s anew and takes z - m - log s.
+// half a step of lse is 2^-14, it makes m and log s anew and takes z - m - log s.
 //
 // Forward: a workgroup takes a row, or one of several parts of it where there are
 // few rows; a second launch then joins the parts. Every thread keeps its own
@@ -37,6 +38,10 @@
 // log(n / 8192)) of them; where rows tie at the bar and the list fills, it
 // is cut down to its own `top`, and keys decide from then on. At the end
 // each listed key's place is the number of larger ones, counted by a thread of its own.
+// The slow orders (1024 x 131072 bf16 without alternatives, with 8 and with 64; random rows take 57, 61 and 88 us): where
+// entries rise along the row all that follow the last raise pass the bar, and the list is cut for every 64 of
+// them: 48, 541 and 1545 us; a row whose largest entry lies beyond 8192 is read twice, by a vector's elements the second
+// time: 185, 208 and 229.
 #include <math.h>
 
 #include "rgc_internal.hpp"
