@@ -123,8 +123,9 @@ class SketchedCrossEntropy(SketchedLinear):
     @torch.no_grad()
     def alternatives(self, x: torch.Tensor, top: int) -> tuple[torch.Tensor, torch.Tensor]:
         """(log probabilities, indices) of each row's `top` most likely entries, in descending order, (..., top)
-        each. The logits are formed in bf16 (as a plain head's are), up to 256 MB of them at a time; of equal
-        ones the lowest index comes first."""
+        each. The logits are formed in bf16 (as a plain head's are), up to 256 MB of them at a time, so that a log
+        probability may be off from log_prob's by half a bf16 step of its logit (1/16 at 16 to 32); of equal ones the
+        lowest index comes first."""
         if not 1 <= top <= 64:
             raise rgc.RgcError("top must lie in 1 .. 64")
         x2 = x.reshape(-1, x.shape[-1])
